@@ -27,7 +27,8 @@ LQ_OK, LQ_ERR_INVALID_ARG, LQ_ERR_UNSUPPORTED, LQ_ERR_HIP, LQ_ERR_NO_DEVICE = ra
 
 ENTRY_POINTS = ("quantize_groupwise", "dequantize_groupwise", "w4a16_gemv", "w8a16_gemv", "w4a16_gemm",
                 "smooth_scale", "quant_per_token_int8", "w8a8_gemm", "act_absmean", "awq_search",
-                "mxfp4_quantize", "mxfp4_gemv", "mxfp4_gemm", "gptq_hessian_factor", "gptq_quantize")
+                "mxfp4_quantize", "mxfp4_gemv", "mxfp4_gemm", "gptq_hessian_factor", "gptq_quantize",
+                "rms_norm_int8", "kv_cache_write", "kv_cache_read", "paged_attention")
 
 
 class LibquantError(RuntimeError):
@@ -68,6 +69,13 @@ def load_library(path: Optional[str] = None):
         "gptq_quantize_noalloc": [P, I64, I64, P, I, I, I64, P, P, P, P],
         "awq_search": [P, I64, P, I64, I64, I, I64, I, P, P, I64, P, P, P, P, P, P, P],
     }
+    D = ctypes.c_double
+    sigs |= {
+        "rms_norm_int8": [P, I, P, I, P, I, I64, I64, D, P, P, P, P],
+        "kv_cache_write": [P, P, P, I, I64, I64, I64, P, I64, P, P, I64, I64, P],
+        "kv_cache_read": [P, P, P, I, I64, P, I64, P, P, I64, I64, P],
+        "paged_attention": [P, P, I64, I64, I64, F, P, I64, P, P, I64, I64, I64, P, I64, P, P, P],
+    }
     for name, argtypes in sigs.items():
         fn = getattr(lib, name)
         fn.argtypes = argtypes
@@ -83,6 +91,8 @@ def load_library(path: Optional[str] = None):
     lib.gptq_workspace_bytes.restype = ctypes.c_int64
     lib.gptq_quantize_noalloc_max_bytes.argtypes = []
     lib.gptq_quantize_noalloc_max_bytes.restype = ctypes.c_int64
+    lib.paged_attention_workspace_bytes.argtypes = [I64] * 9
+    lib.paged_attention_workspace_bytes.restype = ctypes.c_int64
     lib.lq_read_probe_sink_words.argtypes = []
     lib.lq_read_probe_sink_words.restype = ctypes.c_int64
     lib.lq_hbm_read_probe.argtypes = [P, I64, P, P]
@@ -435,3 +445,228 @@ def gptq_quantize_noalloc(w: torch.Tensor, u: torch.Tensor, bits: int = 4, symme
     _call("gptq_quantize_noalloc", _ptr(w), n, k, _ptr(u), bits, int(bool(symmetric)), group, _ptr(out.codes),
           _ptr(out.scales), _ptr(out.zeros), _stream())
     return out
+
+
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}  # lq_dtype
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    return d
+
+
+def _launch(name: str, device: torch.device, *args) -> None:
+    """The call on the current stream of the tensors' own device."""
+    lib = _lib or load_library()
+    index = device.index
+    if index == torch.cuda.current_device():
+        st = getattr(lib, name)(*args, torch.cuda.current_stream(index).cuda_stream)
+    else:
+        with torch.cuda.device(index):
+            st = getattr(lib, name)(*args, torch.cuda.current_stream(index).cuda_stream)
+    if st != LQ_OK:
+        detail = lib.lq_last_error().decode() or lib.lq_status_string(st).decode()
+        raise LibquantError(st, name, detail)
+
+
+def _on(device: torch.device, t: torch.Tensor, name: str, dtype, shape):
+    """_need, on the device of the call's first tensor."""
+    _need(t, name, dtype, shape)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's first tensor on {device}")
+    return t
+
+
+def rms_norm_int8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: Optional[torch.Tensor] = None,
+                  residual_out: Optional[torch.Tensor] = None, qx: Optional[torch.Tensor] = None,
+                  sx: Optional[torch.Tensor] = None):
+    """h = x + residual, RMS norm of h times weight, dynamic per-token INT8 of
+    that -> (qx int8 [t][k], sx fp32 [t], residual_out or None). x, residual and
+    weight bf16 or fp32; residual_out has residual's type and may be residual."""
+    _need(x, "x", x.dtype if isinstance(x, torch.Tensor) else None)
+    xt, dev = _dtype(x, "x"), x.device
+    t, k = x.shape
+    _on(dev, weight, "weight", weight.dtype, (k,))
+    wt, rt = _dtype(weight, "weight"), 0
+    if residual is not None:
+        _on(dev, residual, "residual", residual.dtype, (t, k))
+        rt = _dtype(residual, "residual")
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+        _on(dev, residual_out, "residual_out", residual.dtype, (t, k))
+    elif residual_out is not None:
+        raise ValueError("residual_out needs residual")
+    if qx is None:
+        qx = torch.empty((t, k), dtype=torch.int8, device=dev)
+    if sx is None:
+        sx = torch.empty(t, dtype=torch.float32, device=dev)
+    _on(dev, qx, "qx", torch.int8, (t, k))
+    _on(dev, sx, "sx", torch.float32, (t,))
+    _launch("rms_norm_int8", dev, x.data_ptr(), xt, None if residual is None else residual.data_ptr(), rt,
+            weight.data_ptr(), wt, t, k, float(eps), None if residual is None else residual_out.data_ptr(),
+            qx.data_ptr(), sx.data_ptr())
+    return qx, sx, residual_out
+
+
+class _KvCacheRecord(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scales", "k_zeros", "v_scales", "v_zeros")]
+                + [(n, ctypes.c_int64) for n in ("pages", "page_size", "heads", "head_dim")]
+                + [(n, ctypes.c_int) for n in ("bits", "symmetric")])
+
+
+class KVCache:
+    """The quantized paged cache of kv_cache_write, kv_cache_read and
+    paged_attention over the caller's tensors (layout: lq_kv_cache in
+    libquant.h): codes uint8 k [pages][heads][page_size][row] and
+    v [pages][heads][page_size / 4][row][4], row = head_dim * bits / 8; scales
+    and zeros fp32 [pages][heads][page_size] (zeros None: symmetric)."""
+
+    def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                 k_zeros: Optional[torch.Tensor], v_zeros: Optional[torch.Tensor], head_dim: int, bits: int):
+        if (k_zeros is None) != (v_zeros is None):
+            raise ValueError("k_zeros and v_zeros are given together or not at all")
+        if bits not in (4, 8):
+            raise ValueError(f"bits must be 4 or 8, got {bits}")
+        if not isinstance(k_codes, torch.Tensor) or k_codes.dim() != 4:
+            raise ValueError("k_codes must be a tensor [pages][heads][page_size][row]")
+        row, dev = head_dim * bits // 8, k_codes.device
+        pages, heads, page_size = k_codes.shape[:3]
+        meta = (pages, heads, page_size)
+        _need(k_codes, "k_codes", torch.uint8, (*meta, row))
+        _on(dev, v_codes, "v_codes", torch.uint8, (pages, heads, page_size // 4, row, 4))
+        _on(dev, k_scales, "k_scales", torch.float32, meta)
+        _on(dev, v_scales, "v_scales", torch.float32, meta)
+        if k_zeros is not None:
+            _on(dev, k_zeros, "k_zeros", torch.float32, meta)
+            _on(dev, v_zeros, "v_zeros", torch.float32, meta)
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.k_zeros, self.v_zeros = k_zeros, v_zeros
+        self.pages, self.heads, self.page_size, self.head_dim = pages, heads, page_size, head_dim
+        self.bits, self.symmetric, self.device = bits, k_zeros is None, dev
+        self._record = _KvCacheRecord(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
+                                      None if k_zeros is None else k_zeros.data_ptr(), v_scales.data_ptr(),
+                                      None if v_zeros is None else v_zeros.data_ptr(), pages, page_size, heads,
+                                      head_dim, bits, int(k_zeros is None))
+        self._ref = ctypes.addressof(self._record)
+
+    @classmethod
+    def empty(cls, pages: int, page_size: int, heads: int, head_dim: int, bits: int = 8, symmetric: bool = True,
+              device="cuda") -> "KVCache":
+        """A pool of pages whose contents are not set."""
+        row = head_dim * bits // 8
+
+        def meta():
+            return torch.empty((pages, heads, page_size), dtype=torch.float32, device=device)
+
+        return cls(torch.empty((pages, heads, page_size, row), dtype=torch.uint8, device=device),
+                   torch.empty((pages, heads, page_size // 4, row, 4), dtype=torch.uint8, device=device), meta(), meta(),
+                   None if symmetric else meta(), None if symmetric else meta(), head_dim, bits)
+
+    def nbytes(self) -> int:
+        return self.k_codes.numel() * 2 + self.k_scales.numel() * (8 if self.symmetric else 16)
+
+
+def _batch(cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor, row_starts: torch.Tensor):
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a tensor [b][max_pages]")
+    b, dev = block_table.shape[0], cache.device
+    _on(dev, block_table, "block_table", torch.int32, None)
+    _on(dev, kv_lens, "kv_lens", torch.int32, (b,))
+    _on(dev, row_starts, "row_starts", torch.int32, (b + 1,))
+    return block_table.data_ptr(), block_table.shape[1], kv_lens.data_ptr(), row_starts.data_ptr(), b
+
+
+def _rows(cache: KVCache, t: torch.Tensor, name: str, heads: Optional[int]) -> int:
+    """Checks [rows][heads][head_dim] rows that may lie apart (a slice of a
+    fused product's output); the step from row to row."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a tensor [rows][heads][head_dim]")
+    if t.device != cache.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+    d = cache.head_dim
+    if t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, the cache {cache.heads} heads of {d}")
+    rows, h, _ = t.shape
+    step = t.stride()
+    if step[2] != 1 or (h > 1 and step[1] != d):
+        raise ValueError(f"{name}: a row's heads must be contiguous")
+    return step[0] if rows > 1 else h * d
+
+
+def kv_cache_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                   row_starts: torch.Tensor, max_rows: int = 0) -> None:
+    """Quantize the new rows k, v [rows][heads][head_dim] (bf16 or fp32, rows
+    possibly apart) into the cache: rows row_starts[i] .. row_starts[i + 1] - 1
+    are the last tokens of sequence i, which holds kv_lens[i] with them.
+    max_rows: a bound of any one sequence's rows, if known."""
+    ks, vs = _rows(cache, k, "k", cache.heads), _rows(cache, v, "v", cache.heads)
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must share shape and type")
+    _launch("kv_cache_write", cache.device, cache._ref, k.data_ptr(), v.data_ptr(), _dtype(k, "k"), k.shape[0], ks, vs,
+            *_batch(cache, block_table, kv_lens, row_starts), int(max_rows))
+
+
+def kv_cache_read(cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor, row_starts: torch.Tensor,
+                  rows: int, dtype: torch.dtype = torch.bfloat16, max_rows: int = 0,
+                  k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None):
+    """The values (q - z) s of the rows' keys and values, [rows][heads][head_dim]
+    of dtype (bf16 or fp32) -> (k, v). Rows that belong to no sequence are left
+    as they were in k and v."""
+    shape = (rows, cache.heads, cache.head_dim)
+    if k is None:
+        k = torch.empty(shape, dtype=dtype, device=cache.device)
+    if v is None:
+        v = torch.empty(shape, dtype=dtype, device=cache.device)
+    _on(cache.device, k, "k", dtype, shape)
+    _on(cache.device, v, "v", dtype, shape)
+    _launch("kv_cache_read", cache.device, cache._ref, k.data_ptr(), v.data_ptr(), _dtype(k, "k"), rows,
+            *_batch(cache, block_table, kv_lens, row_starts), int(max_rows))
+    return k, v
+
+
+def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                    row_starts: torch.Tensor, scale: Optional[float] = None, max_rows: int = 0, max_kv: int = 0,
+                    out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Causal attention of the new rows q [rows][q_heads][head_dim] (bf16, rows
+    possibly apart) over the cache -> out bf16 [rows][q_heads][head_dim]. The
+    rows' own keys and values are in the cache already. scale defaults to
+    head_dim^-1/2; lse (fp32 [rows][q_heads]), if given, takes the log-sum-exp;
+    max_rows and max_kv bound any one sequence's rows and tokens, if known;
+    workspace: uint8, of at least paged_attention_workspace(...) bytes."""
+    qs = _rows(cache, q, "q", None)
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"q must be {torch.bfloat16}, got {q.dtype}")
+    rows, q_heads, d = q.shape
+    dev = cache.device
+    table, max_pages, lens, starts, b = _batch(cache, block_table, kv_lens, row_starts)
+    if out is None:
+        out = torch.empty((rows, q_heads, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _on(dev, out, "out", torch.bfloat16, (rows, q_heads, d))
+    if lse is not None:
+        _on(dev, lse, "lse", torch.float32, (rows, q_heads))
+    if workspace is None:
+        need = (_lib or load_library()).paged_attention_workspace_bytes(rows, q_heads, cache.heads, d, b, max_pages,
+                                                                        cache.page_size, max_rows, max_kv)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _on(dev, workspace, "workspace", torch.uint8, None)
+    _launch("paged_attention", dev, cache._ref, q.data_ptr(), rows, q_heads, qs,
+            d ** -0.5 if scale is None else float(scale), table, max_pages, lens, starts, b, int(max_rows), int(max_kv),
+            None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
+            out.data_ptr(), None if lse is None else lse.data_ptr())
+    return out
+
+
+def paged_attention_workspace(rows: int, q_heads: int, cache: KVCache, b: int, max_pages: int, max_rows: int = 0,
+                              max_kv: int = 0) -> int:
+    """Bytes of workspace paged_attention needs for these sizes."""
+    need = load_library().paged_attention_workspace_bytes(rows, q_heads, cache.heads, cache.head_dim, b, max_pages,
+                                                          cache.page_size, max_rows, max_kv)
+    if need < 0:
+        raise LibquantError(LQ_ERR_INVALID_ARG, "paged_attention", "sizes out of range")
+    return need

@@ -19,7 +19,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libquant.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
-SOURCES = ["api.cpp", "quantize.hip", "gemv.hip", "gemv_shared.hip", "gemv8.hip", "gemm.hip", "smooth.hip", "w8a8.hip", "awq.hip", "mx.hip", "gptq.hip", "probe.hip"]
+SOURCES = ["api.cpp", "quantize.hip", "gemv.hip", "gemv_shared.hip", "gemv8.hip", "gemm.hip", "smooth.hip", "w8a8.hip", "awq.hip", "mx.hip", "gptq.hip", "probe.hip",
+           "norm.hip", "kvcache.hip", "attention.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -43,6 +44,7 @@ EXTRA = {
     "gemv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "gemv_shared.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "awq.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

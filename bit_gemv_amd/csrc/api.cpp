@@ -9,6 +9,7 @@
 #include <cstring>
 
 #include "../../include/libquant.h"
+#include "kv.hpp"
 #include "launch.hpp"
 
 namespace {
@@ -120,6 +121,51 @@ lq_status check_wo(const char *fn, int bits, const void *x, int64_t m, const voi
         return fail(LQ_ERR_INVALID_ARG, "%s: output overlaps an input", fn);
     return LQ_OK;
 }
+
+bool is_dtype(int t) { return t == LQ_BF16 || t == LQ_FP32; }
+int64_t dtype_bytes(int t) { return t == LQ_FP32 ? 4 : 2; }
+
+// Shared checks of the paged-cache calls: the cache record, the batch's
+// device arrays and their sizes. Fills the launcher's records.
+lq_status check_kv(const char *fn, const lq_kv_cache *c, int64_t rows, const int32_t *table, int64_t max_pages,
+                   const int32_t *lens, const int32_t *starts, int64_t b, int64_t max_rows, lq::KvCache *out,
+                   lq::KvBatch *batch) {
+    if (!c) return fail(LQ_ERR_INVALID_ARG, "%s: cache null", fn);
+    if (c->bits != 4 && c->bits != 8) return fail(LQ_ERR_INVALID_ARG, "%s: bits must be 4 or 8 (got %d)", fn, c->bits);
+    if (c->pages <= 0 || c->page_size <= 0 || c->heads <= 0 || c->head_dim <= 0)
+        return fail(LQ_ERR_INVALID_ARG, "%s: pages, page_size, heads and head_dim must be positive", fn);
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+        return fail(LQ_ERR_UNSUPPORTED, "%s: head_dim %lld (64, 128 or 256)", fn, (long long)c->head_dim);
+    if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
+        return fail(LQ_ERR_UNSUPPORTED, "%s: page_size %lld (a power of two, 16 to 256)", fn, (long long)c->page_size);
+    if (rows < 0 || b < 0 || max_pages < 0 || max_rows < 0) return fail(LQ_ERR_INVALID_ARG, "%s: negative size", fn);
+    if (c->pages > kMaxDim || c->heads > 65536 || rows > kMaxDim || max_pages > kMaxDim / c->page_size || b > 65535 ||
+        c->pages * c->heads > kMaxElems / (c->page_size * c->head_dim) || b * max_pages > kMaxElems ||
+        rows > kMaxElems / (c->heads * c->head_dim))
+        return fail(LQ_ERR_UNSUPPORTED, "%s: cache or batch too large", fn);
+    if (!c->k_codes || !aligned(c->k_codes, 16) || !c->v_codes || !aligned(c->v_codes, 16))
+        return fail(LQ_ERR_INVALID_ARG, "%s: cache codes null or not 16-byte aligned", fn);
+    if (!c->k_scales || !aligned(c->k_scales, 16) || !c->v_scales || !aligned(c->v_scales, 16))
+        return fail(LQ_ERR_INVALID_ARG, "%s: cache scales null or not 16-byte aligned", fn);
+    if (c->symmetric ? (c->k_zeros || c->v_zeros)
+                     : (!c->k_zeros || !aligned(c->k_zeros, 16) || !c->v_zeros || !aligned(c->v_zeros, 16)))
+        return fail(LQ_ERR_INVALID_ARG, "%s: cache zeros must be NULL for symmetric and 16-byte aligned otherwise", fn);
+    if (rows > 0 && b > 0) {
+        if ((max_pages > 0 && (!table || !aligned(table, 4))) || !lens || !aligned(lens, 4) || !starts ||
+            !aligned(starts, 4))
+            return fail(LQ_ERR_INVALID_ARG, "%s: block_table, kv_lens or row_starts null or misaligned", fn);
+    }
+    int shift = 4;
+    while ((int64_t(1) << shift) < c->page_size) ++shift;
+    *out = lq::KvCache{static_cast<uint8_t *>(c->k_codes), static_cast<uint8_t *>(c->v_codes), c->k_scales, c->k_zeros,
+                       c->v_scales, c->v_zeros, c->pages, shift, (int)c->heads, (int)c->head_dim, c->bits,
+                       c->symmetric != 0};
+    *batch = lq::KvBatch{table, lens, starts, b, max_pages, rows};
+    return LQ_OK;
+}
+
+int64_t kv_code_bytes(const lq_kv_cache *c) { return c->pages * c->page_size * c->heads * (c->head_dim * c->bits / 8); }
+int64_t kv_meta_bytes(const lq_kv_cache *c) { return c->pages * c->page_size * c->heads * 4; }
 
 }  // namespace
 
@@ -524,6 +570,155 @@ lq_status awq_search(const void *x_bf16, int64_t t, const void *w_bf16, int64_t 
 }
 
 }  // extern "C"
+
+lq_status rms_norm_int8(const void *x, lq_dtype x_type, const void *residual, lq_dtype residual_type,
+                        const void *weight, lq_dtype weight_type, int64_t t, int64_t k, double eps,
+                        void *residual_out, int8_t *qx, float *sx, void *stream) {
+    const char *fn = "rms_norm_int8";
+    if (!is_dtype(x_type) || !is_dtype(weight_type) || (residual && !is_dtype(residual_type)))
+        return fail(LQ_ERR_INVALID_ARG, "%s: unknown element type", fn);
+    if (t < 0 || k <= 0) return fail(LQ_ERR_INVALID_ARG, "%s: t must be >= 0 and k > 0", fn);
+    if (!(eps >= 0.0 && eps <= 1e30)) return fail(LQ_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", fn);
+    if (!residual && residual_out)
+        return fail(LQ_ERR_INVALID_ARG, "%s: residual_out without residual", fn);
+    if (k % 128 != 0) return fail(LQ_ERR_UNSUPPORTED, "%s: k must be a multiple of 128", fn);
+    if (t > kMaxDim || k > kMaxDim || t * k > kMaxElems) return fail(LQ_ERR_UNSUPPORTED, "%s: tensor too large", fn);
+    if (t == 0) return LQ_OK;
+    if (!x || !aligned(x, 16)) return fail(LQ_ERR_INVALID_ARG, "%s: x null or not 16-byte aligned", fn);
+    if (!weight || !aligned(weight, 16)) return fail(LQ_ERR_INVALID_ARG, "%s: weight null or not 16-byte aligned", fn);
+    if (!aligned(residual, 16) || !aligned(residual_out, 16))
+        return fail(LQ_ERR_INVALID_ARG, "%s: residual or residual_out not 16-byte aligned", fn);
+    if (!qx || !aligned(qx, 16)) return fail(LQ_ERR_INVALID_ARG, "%s: qx null or not 16-byte aligned", fn);
+    if (!sx || !aligned(sx, 4)) return fail(LQ_ERR_INVALID_ARG, "%s: sx null or misaligned", fn);
+    const int64_t rbytes = residual ? t * k * dtype_bytes(residual_type) : 0;
+    const Range rx{x, t * k * dtype_bytes(x_type)}, rw{weight, k * dtype_bytes(weight_type)}, rr{residual, rbytes};
+    const Range ro{residual_out, residual_out ? rbytes : 0};
+    if (any_overlap({{qx, t * k}, {sx, t * 4}, ro}, {rx, rw}) || any_overlap({{qx, t * k}, {sx, t * 4}}, {rr}) ||
+        (residual_out != residual && overlap(ro, rr)))
+        return fail(LQ_ERR_INVALID_ARG, "%s: an output overlaps an input or another output", fn);
+    lq_status st;
+    if ((st = need_device()) != LQ_OK) return st;
+    lq::NormArgs a{x, x_type == LQ_FP32, residual, residual_type == LQ_FP32, weight, weight_type == LQ_FP32, t, k, eps,
+                   residual_out, qx, sx};
+    return launched(lq::launch_rms_norm_int8(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+lq_status kv_cache_write(const lq_kv_cache *cache, const void *k, const void *v, lq_dtype type, int64_t rows,
+                         int64_t k_stride, int64_t v_stride, const int32_t *block_table, int64_t max_pages,
+                         const int32_t *kv_lens, const int32_t *row_starts, int64_t b, int64_t max_rows,
+                         void *stream) {
+    const char *fn = "kv_cache_write";
+    lq::KvWriteArgs a{};
+    lq_status st = check_kv(fn, cache, rows, block_table, max_pages, kv_lens, row_starts, b, max_rows, &a.c, &a.batch);
+    if (st != LQ_OK) return st;
+    if (!is_dtype(type)) return fail(LQ_ERR_INVALID_ARG, "%s: unknown element type", fn);
+    const int64_t width = cache->heads * cache->head_dim;
+    if (rows == 0 || b == 0 || max_pages == 0) return LQ_OK;
+    if (k_stride < width || v_stride < width || k_stride % 8 || v_stride % 8)
+        return fail(LQ_ERR_INVALID_ARG, "%s: strides must be multiples of 8 and at least heads * head_dim", fn);
+    if (k_stride > kMaxElems / rows || v_stride > kMaxElems / rows)
+        return fail(LQ_ERR_UNSUPPORTED, "%s: strides too large", fn);
+    if (!k || !aligned(k, 16) || !v || !aligned(v, 16))
+        return fail(LQ_ERR_INVALID_ARG, "%s: k or v null or not 16-byte aligned", fn);
+    const int64_t el = dtype_bytes(type), codes = kv_code_bytes(cache), meta = kv_meta_bytes(cache);
+    const int64_t zeros = cache->symmetric ? 0 : meta;
+    if (any_overlap({{cache->k_codes, codes}, {cache->v_codes, codes}, {cache->k_scales, meta}, {cache->v_scales, meta},
+                     {cache->k_zeros, zeros}, {cache->v_zeros, zeros}},
+                    {{k, ((rows - 1) * k_stride + width) * el}, {v, ((rows - 1) * v_stride + width) * el},
+                     {block_table, b * max_pages * 4}, {kv_lens, b * 4}, {row_starts, (b + 1) * 4}}))
+        return fail(LQ_ERR_INVALID_ARG, "%s: an output overlaps an input or another output", fn);
+    if ((st = need_device()) != LQ_OK) return st;
+    a.k = k;
+    a.v = v;
+    a.f32 = type == LQ_FP32;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.max_rows = max_rows;
+    return launched(lq::launch_kv_write(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+lq_status kv_cache_read(const lq_kv_cache *cache, void *k, void *v, lq_dtype type, int64_t rows,
+                        const int32_t *block_table, int64_t max_pages, const int32_t *kv_lens,
+                        const int32_t *row_starts, int64_t b, int64_t max_rows, void *stream) {
+    const char *fn = "kv_cache_read";
+    lq::KvReadArgs a{};
+    lq_status st = check_kv(fn, cache, rows, block_table, max_pages, kv_lens, row_starts, b, max_rows, &a.c, &a.batch);
+    if (st != LQ_OK) return st;
+    if (!is_dtype(type)) return fail(LQ_ERR_INVALID_ARG, "%s: unknown element type", fn);
+    if (rows == 0 || b == 0) return LQ_OK;
+    if (!k && !v) return fail(LQ_ERR_INVALID_ARG, "%s: k and v both null", fn);
+    if (!aligned(k, 16) || !aligned(v, 16)) return fail(LQ_ERR_INVALID_ARG, "%s: k or v not 16-byte aligned", fn);
+    const int64_t out = rows * cache->heads * cache->head_dim * dtype_bytes(type);
+    const int64_t codes = kv_code_bytes(cache), meta = kv_meta_bytes(cache), zeros = cache->symmetric ? 0 : meta;
+    if (any_overlap({{k, k ? out : 0}, {v, v ? out : 0}},
+                    {{cache->k_codes, codes}, {cache->v_codes, codes}, {cache->k_scales, meta}, {cache->v_scales, meta},
+                     {cache->k_zeros, zeros}, {cache->v_zeros, zeros}, {block_table, b * max_pages * 4},
+                     {kv_lens, b * 4}, {row_starts, (b + 1) * 4}}))
+        return fail(LQ_ERR_INVALID_ARG, "%s: an output overlaps an input or another output", fn);
+    if ((st = need_device()) != LQ_OK) return st;
+    a.k = k;
+    a.v = v;
+    a.f32 = type == LQ_FP32;
+    a.max_rows = max_rows;
+    return launched(lq::launch_kv_read(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+int64_t paged_attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b,
+                                        int64_t max_pages, int64_t page_size, int64_t max_rows, int64_t max_kv) {
+    if (rows < 0 || b < 0 || max_pages < 0 || max_rows < 0 || max_kv < 0 || q_heads <= 0 || heads <= 0 ||
+        q_heads % heads || q_heads > 65536 || head_dim <= 0 || head_dim > 256 || page_size <= 0 || rows > kMaxDim ||
+        b > 65535 || max_pages > kMaxDim / page_size || rows > kMaxElems / (q_heads * head_dim))
+        return -1;
+    if (rows == 0 || b == 0) return 0;
+    return lq::attention_workspace_bytes(rows, q_heads, heads, head_dim, b, max_pages, page_size, max_rows, max_kv);
+}
+
+lq_status paged_attention(const lq_kv_cache *cache, const void *q_bf16, int64_t rows, int64_t q_heads,
+                          int64_t q_stride, float scale, const int32_t *block_table, int64_t max_pages,
+                          const int32_t *kv_lens, const int32_t *row_starts, int64_t b, int64_t max_rows,
+                          int64_t max_kv, void *workspace, int64_t workspace_bytes, void *out_bf16, float *lse,
+                          void *stream) {
+    const char *fn = "paged_attention";
+    lq::AttnArgs a{};
+    lq_status st = check_kv(fn, cache, rows, block_table, max_pages, kv_lens, row_starts, b, max_rows, &a.c, &a.batch);
+    if (st != LQ_OK) return st;
+    if (max_kv < 0) return fail(LQ_ERR_INVALID_ARG, "%s: negative size", fn);
+    if (q_heads <= 0 || q_heads % cache->heads)
+        return fail(LQ_ERR_INVALID_ARG, "%s: q_heads (%lld) is not a multiple of heads (%lld)", fn, (long long)q_heads,
+                    (long long)cache->heads);
+    if (!(scale > -1e30f && scale < 1e30f)) return fail(LQ_ERR_INVALID_ARG, "%s: scale not finite", fn);
+    if (rows == 0 || b == 0) return LQ_OK;
+    const int64_t d = cache->head_dim, width = q_heads * d;
+    if (q_heads > 65536 || rows > kMaxElems / width) return fail(LQ_ERR_UNSUPPORTED, "%s: q too large", fn);
+    if (q_stride < width || q_stride % 8)
+        return fail(LQ_ERR_INVALID_ARG, "%s: q_stride must be a multiple of 8 and at least q_heads * head_dim", fn);
+    if (q_stride > kMaxElems / rows) return fail(LQ_ERR_UNSUPPORTED, "%s: q_stride too large", fn);
+    if (!q_bf16 || !aligned(q_bf16, 16)) return fail(LQ_ERR_INVALID_ARG, "%s: q null or not 16-byte aligned", fn);
+    if (!out_bf16 || !aligned(out_bf16, 16)) return fail(LQ_ERR_INVALID_ARG, "%s: out null or not 16-byte aligned", fn);
+    if (!aligned(lse, 4)) return fail(LQ_ERR_INVALID_ARG, "%s: lse misaligned", fn);
+    const int64_t need = lq::attention_workspace_bytes(rows, q_heads, cache->heads, d, b, max_pages, cache->page_size,
+                                                       max_rows, max_kv);
+    if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
+        return fail(LQ_ERR_INVALID_ARG, "%s: workspace null, not 256-byte aligned or smaller than %lld bytes", fn,
+                    (long long)need);
+    const int64_t codes = kv_code_bytes(cache), meta = kv_meta_bytes(cache), zeros = cache->symmetric ? 0 : meta;
+    if (any_overlap({{out_bf16, rows * width * 2}, {lse, lse ? rows * q_heads * 4 : 0}, {workspace, need}},
+                    {{q_bf16, ((rows - 1) * q_stride + width) * 2}, {cache->k_codes, codes}, {cache->v_codes, codes},
+                     {cache->k_scales, meta}, {cache->v_scales, meta}, {cache->k_zeros, zeros}, {cache->v_zeros, zeros},
+                     {block_table, b * max_pages * 4}, {kv_lens, b * 4}, {row_starts, (b + 1) * 4}}))
+        return fail(LQ_ERR_INVALID_ARG, "%s: an output overlaps an input or another output", fn);
+    if ((st = need_device()) != LQ_OK) return st;
+    a.q = static_cast<const uint16_t *>(q_bf16);
+    a.q_stride = q_stride;
+    a.q_heads = (int)q_heads;
+    a.scale = scale;
+    a.max_rows = max_rows;
+    a.max_kv = max_kv;
+    a.workspace = workspace;
+    a.out = static_cast<uint16_t *>(out_bf16);
+    a.lse = lse;
+    return launched(lq::launch_paged_attention(a, static_cast<hipStream_t>(stream)), fn);
+}
 
 int64_t lq_read_probe_sink_words(void) { return lq::read_probe_sink_words(); }
 

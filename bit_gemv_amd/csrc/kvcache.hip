@@ -1,0 +1,308 @@
+// kvcache.hip -- quantizing keys and values into the paged cache as they are
+// written (kv_cache_write) and reading them back (kv_cache_read).
+//
+// A team of D / 8 lanes takes one head of four neighbouring tokens (an aligned
+// quad of positions, the unit in which the cache stores values), 8 elements a
+// lane: statistics by a butterfly over the team, then codes. Keys leave as
+// one run of bytes per token and lane, values as whole words of four tokens
+// (single bytes where only some of the quad's tokens are new). Both kernels
+// are bound by HBM on chunks and by latency on a decode batch.
+#include "common.hpp"
+#include "kv.hpp"
+
+namespace lq {
+
+namespace {
+
+constexpr int kTpb = 256;
+
+template <bool F32>
+LQ_DEVICE void load_row8(const void *p, int64_t e, float *f) {
+    if constexpr (F32) {
+        const f32x4 *q = reinterpret_cast<const f32x4 *>(static_cast<const float *>(p) + e);
+        const f32x4 a = q[0], b = q[1];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[j] = a[j];
+            f[4 + j] = b[j];
+        }
+    } else {
+        const u32x4 a = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p) + e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[2 * j] = bf16_lo(a[j]);
+            f[2 * j + 1] = bf16_hi(a[j]);
+        }
+    }
+}
+
+// quantize_groupwise's scale, zero and codes (stored unsigned) of the team's
+// D elements, 8 in this lane
+template <int D, int BITS, bool SYM>
+LQ_DEVICE void encode8(const float *x, float &s, float &z, uint32_t *c) {
+    constexpr int W = D / 8;
+    if constexpr (SYM) {
+        constexpr float qmax = (float)((1 << (BITS - 1)) - 1);
+        float a = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(x[j]));
+        a = team_max<W>(a);
+        s = (a < kFloor ? kFloor : a) / qmax;
+        z = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            c[j] = (uint32_t)(int)(clamp_code(rintf(x[j] / s), -qmax, qmax) + (float)(1 << (BITS - 1)));
+    } else {
+        constexpr float levels = (float)((1 << BITS) - 1);
+        float lo = x[0], hi = x[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) {
+            lo = fminf(lo, x[j]);
+            hi = fmaxf(hi, x[j]);
+        }
+        lo = team_min<W>(lo);
+        hi = team_max<W>(hi);
+        const float range = hi - lo;
+        s = (range < kFloor ? kFloor : range) / levels;
+        z = rintf(-lo / s) + 0.0f;  // -0 -> +0
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c[j] = (uint32_t)(int)clamp_code(rintf(x[j] / s) + z, 0.0f, levels);
+    }
+}
+
+// which sequence, quad of positions, head and side (key or value) a team has
+struct Item {
+    int64_t quad;
+    int head, side;
+};
+
+template <int D>
+LQ_DEVICE Item item_of(int64_t i, int heads, int64_t quad0) {
+    Item it;
+    it.head = (int)(i % heads);
+    const int64_t j = i / heads;
+    it.side = (int)(j & 1);
+    it.quad = quad0 + (j >> 1);
+    return it;
+}
+
+template <int D, int BITS, bool SYM, bool F32>
+__global__ __launch_bounds__(kTpb) void kv_write_kernel(KvWriteArgs a) {
+    constexpr int W = D / 8;                 // lanes of a team
+    constexpr int kRow = D * BITS / 8;       // bytes of a token's codes
+    constexpr int kLane = BITS;              // of them, this lane's 8 elements
+    const int lane = threadIdx.x % W, team = threadIdx.x / W;
+    for (int64_t seq = blockIdx.y; seq < a.batch.b; seq += gridDim.y) {
+        const KvRows rows = kv_rows(a.batch, seq, a.c.page_shift);
+        if (rows.n == 0 || rows.first + rows.n <= 0) continue;
+        const int64_t quad0 = (rows.first < 0 ? 0 : rows.first) >> 2;
+        const int64_t items = (((rows.first + rows.n - 1) >> 2) - quad0 + 1) * 2 * a.c.heads;
+        for (int64_t i = (int64_t)blockIdx.x * (kTpb / W) + team; i < items; i += (int64_t)gridDim.x * (kTpb / W)) {
+            const Item it = item_of<D>(i, a.c.heads, quad0);
+            const int64_t page = kv_page(a.batch, seq, it.quad * 4, a.c.page_shift, a.c.pages);
+            if (page < 0) continue;
+            const void *src = it.side ? a.v : a.k;
+            const int64_t stride = it.side ? a.v_stride : a.k_stride;
+            uint32_t code[4][8];
+            float s[4], z[4];
+            bool in[4];
+            float x[4][8];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int64_t row = it.quad * 4 + u - rows.first;
+                in[u] = row >= 0 && row < rows.n;
+                if (in[u])
+                    load_row8<F32>(src, (rows.begin + row) * stride + (int64_t)it.head * D + lane * 8, x[u]);
+                else
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[u][j] = 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) encode8<D, BITS, SYM>(x[u], s[u], z[u], code[u]);
+            const int64_t slot = ((page * a.c.heads + it.head) << a.c.page_shift) +
+                                 ((it.quad * 4) & ((1 << a.c.page_shift) - 1));
+            // bytes of this lane: 8 (bits 8) or 4 (bits 4) per token
+            if (BITS == 4) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) code[u][j] = code[u][2 * j] | (code[u][2 * j + 1] << 4);
+            }
+            float *scales = it.side ? a.c.v_scales : a.c.k_scales;
+            float *zeros = it.side ? a.c.v_zeros : a.c.k_zeros;
+            if (lane == 0) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (in[u]) {
+                        scales[slot + u] = s[u];
+                        if (!SYM) zeros[slot + u] = z[u];
+                    }
+            }
+            if (it.side == 0) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (!in[u]) continue;
+                    uint32_t w[kLane / 4];
+#pragma unroll
+                    for (int j = 0; j < kLane / 4; ++j)
+                        w[j] = code[u][4 * j] | (code[u][4 * j + 1] << 8) | (code[u][4 * j + 2] << 16) |
+                               (code[u][4 * j + 3] << 24);
+                    uint32_t *p = reinterpret_cast<uint32_t *>(a.c.k_codes + (slot + u) * kRow + lane * kLane);
+#pragma unroll
+                    for (int j = 0; j < kLane / 4; ++j) p[j] = w[j];
+                }
+            } else {
+                uint8_t *p = a.c.v_codes + slot * kRow + (int64_t)lane * kLane * 4;
+                if (in[0] && in[1] && in[2] && in[3]) {
+                    u32x4 w[kLane / 4];
+#pragma unroll
+                    for (int j = 0; j < kLane; ++j)
+                        w[j / 4][j % 4] = code[0][j] | (code[1][j] << 8) | (code[2][j] << 16) | (code[3][j] << 24);
+#pragma unroll
+                    for (int j = 0; j < kLane / 4; ++j) reinterpret_cast<u32x4 *>(p)[j] = w[j];
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (in[u])
+#pragma unroll
+                            for (int j = 0; j < kLane; ++j) p[j * 4 + u] = (uint8_t)code[u][j];
+                }
+            }
+        }
+    }
+}
+
+template <int D, int BITS, bool SYM, bool F32>
+__global__ __launch_bounds__(kTpb) void kv_read_kernel(KvReadArgs a) {
+    constexpr int W = D / 8;
+    constexpr int kRow = D * BITS / 8;
+    constexpr int kLane = BITS;
+    const int lane = threadIdx.x % W, team = threadIdx.x / W;
+    for (int64_t seq = blockIdx.y; seq < a.batch.b; seq += gridDim.y) {
+        const KvRows rows = kv_rows(a.batch, seq, a.c.page_shift);
+        if (rows.n == 0) continue;
+        const int64_t quad0 = rows.first >> 2;  // floor: positions below zero are rows too
+        const int64_t items = (((rows.first + rows.n - 1) >> 2) - quad0 + 1) * 2 * a.c.heads;
+        for (int64_t i = (int64_t)blockIdx.x * (kTpb / W) + team; i < items; i += (int64_t)gridDim.x * (kTpb / W)) {
+            const Item it = item_of<D>(i, a.c.heads, quad0);
+            void *dst = it.side ? a.v : a.k;
+            if (!dst) continue;
+            const int64_t page = kv_page(a.batch, seq, it.quad * 4, a.c.page_shift, a.c.pages);
+            const int64_t slot = page < 0 ? 0
+                                          : ((page * a.c.heads + it.head) << a.c.page_shift) +
+                                                ((it.quad * 4) & ((1 << a.c.page_shift) - 1));
+            const float *scales = it.side ? a.c.v_scales : a.c.k_scales;
+            const float *zeros = it.side ? a.c.v_zeros : a.c.k_zeros;
+            uint32_t w[4][kLane / 4];  // this lane's code bytes of each token
+            float s[4], z[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                s[u] = 0.0f;
+                z[u] = SYM ? (float)(1 << (BITS - 1)) : 0.0f;
+#pragma unroll
+                for (int j = 0; j < kLane / 4; ++j) w[u][j] = 0;
+            }
+            if (page >= 0) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    s[u] = scales[slot + u];
+                    if (!SYM) z[u] = zeros[slot + u];
+                }
+                if (it.side == 0) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const uint32_t *p =
+                            reinterpret_cast<const uint32_t *>(a.c.k_codes + (slot + u) * kRow + lane * kLane);
+#pragma unroll
+                        for (int j = 0; j < kLane / 4; ++j) w[u][j] = p[j];
+                    }
+                } else {
+                    const u32x4 *p =
+                        reinterpret_cast<const u32x4 *>(a.c.v_codes + slot * kRow + (int64_t)lane * kLane * 4);
+#pragma unroll
+                    for (int j = 0; j < kLane / 4; ++j) {
+                        const u32x4 q = p[j];  // four elements' words of four tokens
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            w[u][j] = ((q[0] >> (8 * u)) & 255u) | (((q[1] >> (8 * u)) & 255u) << 8) |
+                                      (((q[2] >> (8 * u)) & 255u) << 16) | (((q[3] >> (8 * u)) & 255u) << 24);
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int64_t row = it.quad * 4 + u - rows.first;
+                if (row < 0 || row >= rows.n) continue;
+                const bool live = page >= 0 && it.quad * 4 + u >= 0;
+                float f[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t c = BITS == 8 ? (w[u][j / 4] >> (8 * (j % 4))) & 255u : (w[u][0] >> (4 * j)) & 15u;
+                    f[j] = live ? ((float)c - z[u]) * s[u] : 0.0f;
+                }
+                const int64_t e = ((rows.begin + row) * a.c.heads + it.head) * D + lane * 8;
+                if constexpr (F32) {
+                    f32x4 *p = reinterpret_cast<f32x4 *>(static_cast<float *>(dst) + e);
+                    p[0] = f32x4{f[0], f[1], f[2], f[3]};
+                    p[1] = f32x4{f[4], f[5], f[6], f[7]};
+                } else {
+                    u32x4 v;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const bf16x2_t b{(__bf16)f[2 * j], (__bf16)f[2 * j + 1]};
+                        v[j] = __builtin_bit_cast(uint32_t, b);
+                    }
+                    *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(dst) + e) = v;
+                }
+            }
+        }
+    }
+}
+
+// Blocks in x cover max_rows rows of a sequence (one more quad where they are
+// not aligned), blocks in y the sequences; both kernels stride over what a
+// smaller grid leaves.
+dim3 kv_grid(const KvCache &c, const KvBatch &bt, int64_t max_rows) {
+    int64_t n = max_rows <= 0 || max_rows > bt.rows ? bt.rows : max_rows;
+    const int64_t items = ((n + 2) / 4 + 1) * 2 * c.heads;
+    const int64_t teams = kTpb / (c.head_dim / 8);
+    int64_t x = (items + teams - 1) / teams;
+    const int64_t y = bt.b < 32768 ? bt.b : 32768;
+    if (x > 65536) x = 65536;
+    return dim3((uint32_t)x, (uint32_t)y);
+}
+
+}  // namespace
+
+#define LQ_KV(D, BITS, SYM, F32) \
+    if (a.c.head_dim == D && a.c.bits == BITS && (a.c.symmetric != 0) == SYM && (a.f32 != 0) == F32) LQ_KV_DO(D, BITS, SYM, F32)
+#define LQ_KV_TYPES(D, BITS, SYM) LQ_KV(D, BITS, SYM, false) LQ_KV(D, BITS, SYM, true)
+#define LQ_KV_FORMATS(D) \
+    LQ_KV_TYPES(D, 4, false) LQ_KV_TYPES(D, 4, true) LQ_KV_TYPES(D, 8, false) LQ_KV_TYPES(D, 8, true)
+#define LQ_KV_ALL LQ_KV_FORMATS(64) LQ_KV_FORMATS(128) LQ_KV_FORMATS(256)
+
+hipError_t launch_kv_write(const KvWriteArgs &a, hipStream_t st) {
+    const dim3 grid = kv_grid(a.c, a.batch, a.max_rows);
+#define LQ_KV_DO(D, BITS, SYM, F32)                                                                        \
+    {                                                                                                      \
+        hipLaunchKernelGGL((kv_write_kernel<D, BITS, SYM, F32>), grid, dim3(kTpb), 0, st, a);               \
+        return hipGetLastError();                                                                          \
+    }
+    LQ_KV_ALL
+#undef LQ_KV_DO
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_kv_read(const KvReadArgs &a, hipStream_t st) {
+    const dim3 grid = kv_grid(a.c, a.batch, a.max_rows);
+#define LQ_KV_DO(D, BITS, SYM, F32)                                                                        \
+    {                                                                                                      \
+        hipLaunchKernelGGL((kv_read_kernel<D, BITS, SYM, F32>), grid, dim3(kTpb), 0, st, a);                \
+        return hipGetLastError();                                                                          \
+    }
+    LQ_KV_ALL
+#undef LQ_KV_DO
+    return hipErrorInvalidValue;
+}
+
+}  // namespace lq

@@ -110,6 +110,21 @@ struct AwqArgs {
     float *scales, *zeros;
 };
 
+// Residual addition, RMS norm and per-token INT8; *_f32: fp32, else bf16.
+struct NormArgs {
+    const void *x;
+    int x_f32;
+    const void *residual;  // or null
+    int residual_f32;
+    const void *weight;
+    int weight_f32;
+    int64_t t, k;
+    double eps;
+    void *residual_out;  // or null
+    int8_t *qx;
+    float *sx;
+};
+
 // Decode GEMV at batch 4..16 on large matrices (gemv_shared.hip), for the
 // three weight formats. scales: fp32 [n][k / group] for INT4 and INT8,
 // E8M0 bytes [n][k / 32] for MXFP4 (group and zeros unused there).
@@ -142,6 +157,7 @@ hipError_t launch_w8a16_gemv(const WoArgs &a, hipStream_t st);
 hipError_t launch_smooth_scale(const SmoothArgs &a, hipStream_t st);
 hipError_t launch_quant_per_token(const TokenQuantArgs &a, hipStream_t st);
 hipError_t launch_w8a8_gemm(const W8Args &a, hipStream_t st);
+hipError_t launch_rms_norm_int8(const NormArgs &a, hipStream_t st);
 hipError_t launch_mx_quantize(const uint16_t *w, int64_t n, int64_t k, uint8_t *codes, uint8_t *scales,
                               hipStream_t st);
 hipError_t launch_mx_gemv(const MxArgs &a, hipStream_t st);

@@ -395,6 +395,125 @@ lq_status awq_search(const void *x_bf16, int64_t t, const void *w_bf16, int64_t 
                      int64_t workspace_bytes, float *s_best, double *losses, int32_t *best, void *codes,
                      float *scales, float *zeros, void *stream);
 
+/* Element types of the activations that the entry points below take. */
+typedef enum { LQ_BF16 = 0, LQ_FP32 = 1 } lq_dtype;
+
+/*
+ * rms_norm_int8 -- the residual's addition, root-mean-square norm and dynamic
+ * per-token INT8 in one pass over the row: what lies between two W8A8
+ * products of a decoder layer. Per row, with every product and quotient
+ * rounded to fp32:
+ *   h[j]  = x[j] + residual[j]                  (fp32; h = x without residual)
+ *   r     = fp32((sum_j h[j]^2 / k + eps)^-1/2) (fp64 up to that rounding)
+ *   y[j]  = (h[j] * r) * weight[j]
+ *   sx    = max(max_j |y[j]|, 1e-8) / 127
+ *   qx[j] = clamp(round(y[j] / sx), -127, 127)
+ *   residual_out[j] = h[j] rounded to residual's type
+ * The codes come from the unrounded h. A SmoothQuant factor is folded into
+ * weight (weight[j] / s[j]), which is why weight may be fp32.
+ * x [t][k] of x_type (fp32 takes a product's output as it is); residual
+ * nullable [t][k] of residual_type; weight [k] of weight_type; eps >= 0;
+ * residual_out nullable, [t][k] of residual_type, and may be residual itself
+ * (otherwise it must not overlap any input); without residual it must be
+ * NULL. qx out int8 [t][k]; sx out fp32 [t]: w8a8_gemm's input. k a
+ * multiple of 128. x, residual, weight, qx, residual_out 16-byte aligned.
+ */
+lq_status rms_norm_int8(const void *x, lq_dtype x_type, const void *residual, lq_dtype residual_type,
+                        const void *weight, lq_dtype weight_type, int64_t t, int64_t k, double eps,
+                        void *residual_out, int8_t *qx, float *sx, void *stream);
+
+/*
+ * The quantized paged KV cache of kv_cache_write, kv_cache_read and
+ * paged_attention (W/A/KV notation: KV8 and KV4). A pool of `pages` pages
+ * holds page_size tokens each for `heads` key/value heads of head_dim
+ * elements. Each token and head has one scale (and one zero point when
+ * asymmetric) for its key and one for its value: quantize_groupwise's
+ * formulas with the head as the group. Codes are stored unsigned, symmetric
+ * ones as q + 2^(bits - 1). With D = head_dim, e = element, o = token in page
+ * and row = D bytes (bits 8) or D / 2 (bits 4):
+ *   k_codes [pages][heads][page_size][row]         bits 8: byte e;
+ *           bits 4: byte e / 2, even elements in the low nibble
+ *   v_codes [pages][heads][page_size / 4][row][4]  byte of (o, e): the same
+ *           byte index in the row, then o % 4: four tokens of one element
+ *           side by side, the operand order of the product that reads them
+ *   k_scales, k_zeros, v_scales, v_zeros fp32 [pages][heads][page_size];
+ *           zeros NULL iff symmetric
+ * bits 4 or 8; head_dim 64, 128 or 256; page_size a power of two, 16 to 256;
+ * codes, scales and zeros 16-byte aligned. All of it is the caller's memory.
+ * Slots that were never written may hold anything.
+ */
+typedef struct {
+    void *k_codes, *v_codes;
+    float *k_scales, *k_zeros, *v_scales, *v_zeros;
+    int64_t pages, page_size, heads, head_dim;
+    int bits, symmetric;
+} lq_kv_cache;
+
+/*
+ * Arguments that the three calls share. Sequence i of b holds kv_lens[i]
+ * tokens, the new ones included, in the pages block_table[i][0],
+ * block_table[i][1], ...; rows row_starts[i] .. row_starts[i + 1] - 1 of the
+ * call's row tensors are its last tokens: row r is at position
+ * kv_lens[i] - (row_starts[i + 1] - r).
+ * block_table int32 [b][max_pages], kv_lens int32 [b], row_starts int32
+ * [b + 1] (ascending), all in device memory, 4-byte aligned, so their
+ * values are not checked on the host. The kernels read or write nothing
+ * outside the tensors for any values: rows with a position below zero or in
+ * a page that is not in the pool are not written to the cache, read back as
+ * zeros, and not attended to. Rows before row_starts[0] or from
+ * row_starts[b] on are left as they were.
+ * rows is the number of rows of the row tensors. max_rows (and max_kv) bound
+ * the rows (the tokens held) of any one sequence; they size the launch and
+ * choose the kernel, no result depends on their being exact or right (0:
+ * not known).
+ *
+ * kv_cache_write -- quantize the rows k, v [rows][heads][head_dim] of `type`
+ * into their slots. k_stride and v_stride: elements from one row to the
+ * next, at least heads * head_dim and a multiple of 8 (a slice of a fused
+ * q|k|v product's rows). Two sequences may share pages only where neither
+ * writes. k and v 16-byte aligned and finite.
+ */
+lq_status kv_cache_write(const lq_kv_cache *cache, const void *k, const void *v, lq_dtype type, int64_t rows,
+                         int64_t k_stride, int64_t v_stride, const int32_t *block_table, int64_t max_pages,
+                         const int32_t *kv_lens, const int32_t *row_starts, int64_t b, int64_t max_rows,
+                         void *stream);
+
+/*
+ * kv_cache_read -- the rows' keys and values back from the cache: x_hat =
+ * s (q - z), rounded once to `type`, into k, v [rows][heads][head_dim]
+ * (16-byte aligned; either may be NULL).
+ */
+lq_status kv_cache_read(const lq_kv_cache *cache, void *k, void *v, lq_dtype type, int64_t rows,
+                        const int32_t *block_table, int64_t max_pages, const int32_t *kv_lens,
+                        const int32_t *row_starts, int64_t b, int64_t max_rows, void *stream);
+
+/*
+ * paged_attention -- causal attention of new tokens (a decode batch's single
+ * tokens, chunks of prompts, or both in one batch) over the cache, their own
+ * keys and values already written:
+ *   out[r][h] = sum_j p_j v_hat[j][h / g],  p = softmax_j(scale q[r][h] . k_hat[j][h / g])
+ * over the positions j of r's sequence up to r's own; g = q_heads / heads.
+ * A row that sees no position gets zeros (lse -inf).
+ * q bf16 [rows][q_heads][head_dim], q_stride elements from row to row (at
+ * least q_heads * head_dim, a multiple of 8); q_heads a multiple of heads;
+ * out bf16 [rows][q_heads][head_dim]; lse nullable fp32 [rows][q_heads]:
+ * log sum_j exp(scale q . k_hat). q and out 16-byte aligned.
+ * Products run on fp16 MFMA with exact integer codes, exact q (scaled by a
+ * power of two) and weights p rounded to fp16; scales, sums and softmax
+ * statistics are fp32. Finite q, |scale q . k_hat| below 1e30.
+ * workspace: at least paged_attention_workspace_bytes(...) bytes for the same
+ * arguments (may be 0: then NULL is fine), 256-byte aligned, scratch: calls
+ * that may overlap need one each.
+ * Sums are in a fixed order: equal calls give equal bits.
+ */
+int64_t paged_attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b,
+                                        int64_t max_pages, int64_t page_size, int64_t max_rows, int64_t max_kv);
+lq_status paged_attention(const lq_kv_cache *cache, const void *q_bf16, int64_t rows, int64_t q_heads,
+                          int64_t q_stride, float scale, const int32_t *block_table, int64_t max_pages,
+                          const int32_t *kv_lens, const int32_t *row_starts, int64_t b, int64_t max_rows,
+                          int64_t max_kv, void *workspace, int64_t workspace_bytes, void *out_bf16, float *lse,
+                          void *stream);
+
 /*
  * Measurement helper (not a step of the method).
  *
