@@ -49,6 +49,7 @@ constexpr int kDppXor1 = 0xB1;         // quad_perm [1, 0, 3, 2]
 constexpr int kDppXor2 = 0x4E;         // quad_perm [2, 3, 0, 1]
 constexpr int kDppHalfMirror = 0x141;  // lane i <-> 7 - i within 8 lanes
 constexpr int kDppMirror = 0x140;      // lane i <-> 15 - i within 16 lanes
+constexpr int kDppRowRor8 = 0x128;     // lane i <-> i ^ 8 within 16 lanes (rotation by 8)
 
 template <int CTRL>
 LQ_DEVICE float dpp_move(float v) {

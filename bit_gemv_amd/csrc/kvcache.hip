@@ -36,8 +36,10 @@ LQ_DEVICE void load_row8(const void *p, int64_t e, float *f) {
     }
 }
 
-// quantize_groupwise's scale, zero and codes (stored unsigned) of the team's
-// D elements, 8 in this lane
+// Scale, zero and codes (stored unsigned) of the team's D elements, 8 in this
+// lane: quantize_groupwise's formulas, except that the scale is the range
+// times the fp32 reciprocal of the level count, a multiplication (at most one
+// ulp from the quotient) in place of a division
 template <int D, int BITS, bool SYM>
 LQ_DEVICE void encode8(const float *x, float &s, float &z, uint32_t *c) {
     constexpr int W = D / 8;
@@ -47,7 +49,7 @@ LQ_DEVICE void encode8(const float *x, float &s, float &z, uint32_t *c) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(x[j]));
         a = team_max<W>(a);
-        s = (a < kFloor ? kFloor : a) / qmax;
+        s = (a < kFloor ? kFloor : a) * (1.0f / qmax);
         z = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -63,7 +65,7 @@ LQ_DEVICE void encode8(const float *x, float &s, float &z, uint32_t *c) {
         lo = team_min<W>(lo);
         hi = team_max<W>(hi);
         const float range = hi - lo;
-        s = (range < kFloor ? kFloor : range) / levels;
+        s = (range < kFloor ? kFloor : range) * (1.0f / levels);
         z = rintf(-lo / s) + 0.0f;  // -0 -> +0
 #pragma unroll
         for (int j = 0; j < 8; ++j) c[j] = (uint32_t)(int)clamp_code(rintf(x[j] / s) + z, 0.0f, levels);

