@@ -25,6 +25,7 @@ namespace {
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.44269504088896341f;
@@ -164,6 +165,7 @@ struct Schedule {
     };
     const KvBatch &bt;
     const int shift, group, row_tile, lane;
+    const bool by_unit;  // every unit counts as one step: blocks take whole units
     Lane first;
 
     LQ_DEVICE Lane load(int64_t seq, int64_t before) const {
@@ -174,14 +176,15 @@ struct Schedule {
             if (x.rows.n > 0) {
                 int64_t keys = x.rows.first + x.rows.n < x.rows.len ? x.rows.first + x.rows.n : x.rows.len;
                 keys = keys < 1 ? 1 : keys;  // a unit without keys is still written
-                x.steps = (int)((keys + STEP - 1) / STEP);
+                x.steps = by_unit ? 1 : (int)((keys + STEP - 1) / STEP);
                 x.all = (int64_t)(((uint32_t)x.rows.n * (uint32_t)group + row_tile - 1) / (uint32_t)row_tile) * x.steps;
             }
         }
         x.upto = before + scan64(x.all);
         return x;
     }
-    LQ_DEVICE Schedule(const KvBatch &b, int sh, int g, int rt, int l) : bt(b), shift(sh), group(g), row_tile(rt), lane(l) {
+    LQ_DEVICE Schedule(const KvBatch &b, int sh, int g, int rt, int l, bool unit = false)
+        : bt(b), shift(sh), group(g), row_tile(rt), lane(l), by_unit(unit) {
         first = load(lane, 0);
     }
     LQ_DEVICE int64_t total() const {
@@ -200,8 +203,12 @@ struct Schedule {
                 p.seq = s0 + src;
                 p.steps = __builtin_amdgcn_readlane(x.steps, src);
                 const int64_t start = readlane64(x.upto - x.all, src);
-                p.tile = (uint32_t)uniform_div(pos - start, p.steps);
-                p.start = start + (int64_t)p.tile * p.steps;
+                const uint32_t j = (uint32_t)uniform_div(pos - start, p.steps);
+                p.start = start + (int64_t)j * p.steps;
+                // tiles from both ends in turn: early rows see fewer keys, so
+                // neighbouring units together have about the same to do
+                const uint32_t tiles = (uint32_t)uniform_div(readlane64(x.all, src), p.steps);
+                p.tile = j & 1 ? tiles - 1 - (j >> 1) : j >> 1;
                 p.rows.begin = readlane64(x.rows.begin, src);
                 p.rows.n = readlane64(x.rows.n, src);
                 p.rows.first = readlane64(x.rows.first, src);
@@ -262,6 +269,44 @@ LQ_DEVICE void load_words(uint32_t *dst, const uint8_t *p) {
         const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
         dst[0] = v[0]; dst[1] = v[1];
     }
+}
+
+// The wave's query rows in fp16, scaled by a power of two that is common to them
+// (the largest element to [2^14, 2^15)); the sign of the softmax's scale goes to
+// q, so that larger products are larger scores. Returns what a product is to be
+// multiplied by to be a score in log2; qsum: the sum of this lane's elements.
+template <int STEPS, int BITS, bool SYM>
+LQ_DEVICE float q_to_fp16(const u32x4 *raw, float scale, f16x8 *qf, float &qsum) {
+    // magnitudes of bf16 order as their bits do, two to a word
+    u16x2 top2 = {0, 0};
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            top2 = __builtin_elementwise_max(top2, __builtin_bit_cast(u16x2, raw[s][j] & 0x7FFF7FFFu));
+    const float amax = max_halves16(
+        max_halves32(row_max(__uint_as_float((uint32_t)(top2[0] > top2[1] ? top2[0] : top2[1]) << 16))));
+    int sh = 141 - (int)(__float_as_uint(amax) >> 23);
+    sh = sh < -100 ? -100 : sh > 100 ? 100 : sh;
+    const float up = scale == 0.0f ? 0.0f : copysignf(__uint_as_float((uint32_t)(sh + 127) << 23), scale);
+    const float unscale = __uint_as_float((uint32_t)(127 - sh) << 23);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[2 * j] = bf16_lo(raw[s][j]) * up;
+            f[2 * j + 1] = bf16_hi(raw[s][j]) * up;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            // the order in which a word's codes come out: nibbles 0 4 1 5 2 6 3 7
+            const int src = BITS == 8 ? e : (e >> 1) + 4 * (e & 1);
+            qf[s][e] = (_Float16)f[src];
+            if (!SYM) qsum += (float)qf[s][e];
+        }
+    }
+    return scale == 0.0f ? 1.0f : fmaxf(fabsf(scale) * kLog2e * unscale, 1e-37f);
 }
 
 template <int D, int BITS, bool SYM, int ROWS, int WAVES>
@@ -367,9 +412,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_few_kernel(AttnArgs a, Spa
         typename C::Tile buf[C::NB];
         if (its > 0) load_pages(0);
 
-        // q in fp16, scaled by a power of two that is common to the tile (the
-        // largest element to [2^14, 2^15)); the sign of the softmax's scale goes
-        // to q, so that larger products are larger scores
         f16x8 qf[C::STEPS];
         float c1, qsum = 0.0f;
         {
@@ -385,36 +427,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_few_kernel(AttnArgs a, Spa
             #pragma unroll
             for (int i = 0; i < C::NB - 1; ++i)
                 if (i < its) load_tile(buf[i], i);  // in flight while q is made ready
-            // magnitudes of bf16 order as their bits do, two to a word
-            u16x2 top2 = {0, 0};
-#pragma unroll
-            for (int s = 0; s < C::STEPS; ++s)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    top2 = __builtin_elementwise_max(top2, __builtin_bit_cast(u16x2, raw[s][j] & 0x7FFF7FFFu));
-            const float amax =
-                max_halves16(max_halves32(row_max(__uint_as_float((uint32_t)(top2[0] > top2[1] ? top2[0] : top2[1]) << 16))));
-            int sh = 141 - (int)(__float_as_uint(amax) >> 23);
-            sh = sh < -100 ? -100 : sh > 100 ? 100 : sh;
-            const float up = a.scale == 0.0f ? 0.0f : copysignf(__uint_as_float((uint32_t)(sh + 127) << 23), a.scale);
-            const float unscale = __uint_as_float((uint32_t)(127 - sh) << 23);
-            c1 = a.scale == 0.0f ? 1.0f : fmaxf(fabsf(a.scale) * kLog2e * unscale, 1e-37f);
-#pragma unroll
-            for (int s = 0; s < C::STEPS; ++s) {
-                float f[8];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    f[2 * j] = bf16_lo(raw[s][j]) * up;
-                    f[2 * j + 1] = bf16_hi(raw[s][j]) * up;
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    // the order in which a word's codes come out: nibbles 0 4 1 5 2 6 3 7
-                    const int src = BITS == 8 ? e : (e >> 1) + 4 * (e & 1);
-                    qf[s][e] = (_Float16)f[src];
-                    if (!SYM) qsum += (float)qf[s][e];
-                }
-            }
+            c1 = q_to_fp16<C::STEPS, BITS, SYM>(raw, a.scale, qf, qsum);
             if (!SYM) qsum = add_halves16(add_halves32(qsum));
         }
 
@@ -633,6 +646,411 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_few_kernel(AttnArgs a, Spa
     }
 }
 
+// ---- many rows: 128 query rows share each key tile through LDS ----
+//
+// Four waves of 32 rows. Each key tile's codes are loaded once by the block
+// (the next tile's while this one is used), turned into fp16 once and laid out
+// in LDS as the 32 x 32 x 16 matrix instruction reads them, so the conversion
+// costs a 128th of an operation per row and code. Two blocks a CU (64 KB of LDS
+// each): one's softmax runs beside the other's products.
+template <int D, int BITS>
+struct Many {
+    static constexpr int ROWS = 128;
+    static constexpr int KT = D == 64 ? 64 : 32;   // keys of a tile
+    static constexpr int RING = 3;                 // tiles in LDS: in use, next, being written
+    static constexpr int kRow = D * BITS / 8;
+    static constexpr int KB = kRow * KT / 256;     // key code bytes a thread
+    static constexpr int TPK = 256 / KT;           // threads a key
+    static constexpr int TP = 256 / (KT / 8);      // threads a pair of value quads
+    static constexpr int VW = kRow / TP;           // value words a thread and quad
+    static constexpr int DW = VW * 8 / BITS;       // value elements a thread
+    static constexpr int STEPS = D / 16;           // score MFMAs per 32 keys
+    static constexpr int JT = D / 32;              // output tiles
+    static constexpr int CHUNKS = D / 8;           // 16-byte chunks of a key's fp16 row
+    static constexpr float kMid = (float)(1 << (BITS - 1));
+
+    static constexpr int KC = KB / BITS;           // 8-code chunks a thread brings of a key
+    // Keys lie chunk by chunk ([chunk][key][8 elements]), each chunk's run a
+    // little longer than its keys so that the threads of one key write to
+    // different banks; values [16 keys][half][position][8 keys], position p
+    // holding element (p % TP) DW + p / TP. Reads are runs of 16 bytes a lane.
+    static constexpr int KPAD = KT + (KT == 64 ? 2 : 1);
+    struct Buf {
+        f16x8 k[CHUNKS * KPAD], v[KT / 8 * D];
+        float meta[4][KT];   // key scales, value scales, key zeros, value zeros
+        float stat[4][4];    // [1]: the largest value scale of each 16 keys
+        int bad[4];          // whether they lie outside the pool
+    };
+    struct Load {
+        uint32_t k[KB / 4], v0[VW], v1[VW];
+        float meta;
+        int bad, dead;
+    };
+};
+
+template <int N>
+LQ_DEVICE void load_any(uint32_t *dst, const uint8_t *p) {
+    if constexpr (N >= 4) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) load_words<4>(dst + i, p + 4 * i);
+    } else if constexpr (N == 2) {
+        load_words<2>(dst, p);
+    } else {
+        dst[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+}
+
+template <int D, int BITS, bool SYM>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_many_kernel(AttnArgs a, Span span, int by_unit) {
+    using C = Many<D, BITS>;
+    __shared__ typename C::Buf lds[C::RING];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 31, half = lane >> 5;
+    const int h = blockIdx.x % a.c.heads;
+    const int block = blockIdx.x / a.c.heads;
+    const int group = a.q_heads / a.c.heads;
+    const int shift = a.c.page_shift, ps_mask = (1 << shift) - 1;
+    const int pages = (int)a.c.pages;
+    const uint32_t magic = fp16_magic();
+    // what this thread brings of a tile: all its keys are of one group of 16
+    const int my_key = threadIdx.x / C::TPK, my_part = threadIdx.x % C::TPK;  // in the tile
+    const int my_group = C::KT == 64 ? wave : wave >> 1;
+    const int my_pair = threadIdx.x / C::TP, my_t = threadIdx.x % C::TP;      // 16-key step and half, position
+    const uint32_t k_off = (my_key & 15) * C::kRow + my_part * C::KB;
+    const uint32_t v_off = (my_pair & 1) * 4 * C::kRow + my_t * C::VW * 4;    // its second quad is 2 quads on
+    // lanes 0-15 bring the key scales, 16-31 the value scales, then the zeros
+    const float *const meta_src = (lane < 16             ? a.c.k_scales
+                                   : SYM || lane < 32    ? a.c.v_scales
+                                   : lane < 48           ? a.c.k_zeros
+                                                         : a.c.v_zeros) + (lane & 15);
+
+    // looked up anew for each piece: its registers are wanted inside
+    const auto schedule = [&]() { return Schedule<C::KT>(a.batch, shift, group, C::ROWS, lane, by_unit); };
+    int64_t begin, end;
+    {
+        const int64_t all_steps = schedule().total(), share = uniform_div(all_steps + span.cap - 1, span.cap);
+        begin = block * share;
+        end = begin + share < all_steps ? begin + share : all_steps;
+    }
+    for (int64_t pos = begin; pos < end;) {
+        const Piece piece = schedule().at(pos);
+        const KvRows &rows = piece.rows;
+        int step0 = (int)(pos - piece.start);
+        int step1 = end - piece.start < piece.steps ? (int)(end - piece.start) : piece.steps;
+        const bool whole = step0 == 0 && step1 == piece.steps;
+        const int64_t slot_of = ((int64_t)(2 * block + (pos > begin)) * a.c.heads + h) * C::ROWS;
+        pos = piece.start + step1;
+        const uint32_t tile = piece.tile;
+        const int32_t *const table = a.batch.table + piece.seq * a.batch.max_pages;
+        const uint32_t total = (uint32_t)rows.n * (uint32_t)group;
+
+        // this lane's query row, and the wave's first and last
+        const uint32_t wave_row = tile * C::ROWS + wave * 32, rr = wave_row + n;
+        const bool live = rr < total;
+        const uint32_t tok = live ? rr / (uint32_t)group : 0;
+        const int qh = h * group + (int)(live ? rr - tok * (uint32_t)group : 0);
+        const uint32_t block_last = (tile * C::ROWS + C::ROWS - 1 < total ? tile * C::ROWS + C::ROWS - 1 : total - 1) / (uint32_t)group;
+        const uint32_t wave_last = (wave_row + 31 < total ? wave_row + 31 : total - 1) / (uint32_t)group;
+        const int row_pos = live ? (int)(rows.first + tok) : -1;
+        const int safe = (int)(rows.first + wave_row / (uint32_t)group);
+        const int reach = wave_row < total ? (int)(rows.first + wave_last) : -1;  // last key any row of the wave sees
+        int64_t kend64 = rows.first + block_last + 1;
+        kend64 = kend64 > rows.len ? rows.len : kend64;
+        const int kend = kend64 < 0 ? 0 : (int)kend64;
+        if (by_unit) step1 = (kend + C::KT - 1) / C::KT;
+        const int kbeg = step0 * C::KT < kend ? step0 * C::KT : kend;
+        const int kstop = (int64_t)step1 * C::KT < kend ? step1 * C::KT : kend;
+        const int its = (kstop - kbeg + C::KT - 1) / C::KT;
+        const int top = (kstop - 1) & ~15;
+
+        // pages of 64 groups of 16 keys ahead, a lane each
+        int pid = 0;
+        auto load_pages = [&](int it) {
+            int k0 = kbeg + C::KT * it + 16 * lane;
+            k0 = k0 < top ? k0 : top;
+            pid = table[k0 >> shift];
+        };
+        constexpr int kAhead = 64 * 16 / C::KT;  // tiles of one such read
+        auto load = [&](typename C::Load &x, int it) {
+            if (it % kAhead == 0 && it > 0) {
+                load_pages(it);
+                asm volatile("" : "+v"(pid));
+            }
+            const int key0 = kbeg + C::KT * it + 16 * my_group;
+            int page = __builtin_amdgcn_readlane(pid, (it % kAhead) * (C::KT / 16) + my_group);
+            x.bad = (uint32_t)page >= (uint32_t)pages;
+            page = x.bad ? 0 : page;
+            const int kc = key0 < top ? key0 : top;
+            const int64_t slot = (((int64_t)page * a.c.heads + h) << shift) + (kc & ps_mask);
+            load_any<C::KB / 4>(x.k, a.c.k_codes + slot * C::kRow + k_off);
+            const uint8_t *vp = a.c.v_codes + slot * C::kRow;
+            load_any<C::VW>(x.v0, vp + v_off);
+            load_any<C::VW>(x.v1, vp + 8 * C::kRow + v_off);
+            x.dead = x.bad | (key0 + (lane & 15) >= kstop);
+            x.meta = meta_src[slot];
+        };
+        auto store = [&](const typename C::Load &x, typename C::Buf &b) {
+#pragma unroll
+            for (int c = 0; c < C::KC; ++c) {
+                f16x2 f[4];
+                if constexpr (BITS == 8) {
+                    int8_row(x.k[2 * c], f);
+                    int8_row(x.k[2 * c + 1], f + 2);
+                } else {
+                    const uint32_t w = x.k[c], w8 = w >> 8;
+                    f[0] = int4_low(w, magic); f[1] = int4_high(w, magic);
+                    f[2] = int4_low(w8, magic); f[3] = int4_high(w8, magic);
+                }
+                b.k[(my_part * C::KC + c) * C::KPAD + my_key] = join(f);
+            }
+            f16x8 *vp = &b.v[my_pair * D + my_t];
+#pragma unroll
+            for (int w = 0; w < C::VW; ++w) {
+                f16x2 f[4];
+                if constexpr (BITS == 8) {
+                    int8_quad(x.v0[w], f);
+                    int8_quad(x.v1[w], f + 2);
+                    vp[w * C::TP] = join(f);
+                } else {
+                    const uint32_t v0 = x.v0[w], v1 = x.v1[w], v08 = v0 >> 8, v18 = v1 >> 8;
+                    f[0] = int4_low(v0, magic); f[1] = int4_low(v08, magic);
+                    f[2] = int4_low(v1, magic); f[3] = int4_low(v18, magic);
+                    vp[2 * w * C::TP] = join(f);
+                    f[0] = int4_high(v0, magic); f[1] = int4_high(v08, magic);
+                    f[2] = int4_high(v1, magic); f[3] = int4_high(v18, magic);
+                    vp[(2 * w + 1) * C::TP] = join(f);
+                }
+            }
+            // slots that hold nothing count as zeros
+            const float meta = x.dead ? (lane < 32 ? 0.0f : C::kMid) : x.meta;
+            b.meta[lane >> 4][16 * my_group + (lane & 15)] = meta;
+            b.stat[lane >> 4][my_group] = row_max(meta);
+            b.bad[my_group] = x.bad;
+        };
+
+        typename C::Load x;
+        if (its > 0) load_pages(0);
+        // q as in the other kernel: fp16, a power of two common to the wave's rows
+        f16x8 qf[C::STEPS];
+        float c1, qsum = 0.0f;
+        {
+            u32x4 raw[C::STEPS];
+            const uint16_t *qp = a.q + (rows.begin + tok) * a.q_stride + (int64_t)qh * D + 8 * half;
+#pragma unroll
+            for (int s = 0; s < C::STEPS; ++s)
+                raw[s] = live ? *reinterpret_cast<const u32x4 *>(qp + 16 * s) : u32x4{0u, 0u, 0u, 0u};
+            asm volatile("" : "+v"(pid));
+            if (its > 0) load(x, 0);
+            c1 = q_to_fp16<C::STEPS, BITS, SYM>(raw, a.scale, qf, qsum);
+            if (!SYM) qsum = add_halves32(qsum);
+        }
+        if (its > 0) store(x, lds[0]);
+        if (its > 1) {
+            load(x, 1);
+            store(x, lds[1]);
+        }
+        if (its > 2) load(x, 2);
+        lds_barrier();
+
+        f32x16 o[C::JT];
+#pragma unroll
+        for (int j = 0; j < C::JT; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[j][i] = 0.0f;
+        float m = -1e30f, l = 0.0f, vz = 0.0f, sref = 0.0f, mm = -1e30f;
+        constexpr int KBLK = C::KT / 32;
+
+        // keys of block kb as the matrix instruction's operand, half of the steps
+        auto key_operands = [&](const typename C::Buf &b, int kb, int from, f16x8 *kr) {
+#pragma unroll
+            for (int s = from; s < from + C::STEPS / 2; ++s) kr[s] = b.k[(2 * s + half) * C::KPAD + kb * 32 + n];
+        };
+        // scale, mask and reference of the scores t of block kb of tile b:
+        // register i of the lane is key 8 (i / 4) + 4 half + i % 4 of row n
+        auto settle = [&](const typename C::Buf &b, int kb, int key0, f32x16 &t) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int at = kb * 32 + 8 * r + 4 * half;
+                const f32x4 sk = *reinterpret_cast<const f32x4 *>(&b.meta[0][at]);
+                f32x4 zk;
+                if (!SYM) zk = *reinterpret_cast<const f32x4 *>(&b.meta[2][at]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float v = t[4 * r + i];
+                    if (!SYM) v = __builtin_fmaf(C::kMid - zk[i], qsum, v);
+                    t[4 * r + i] = v * sk[i];
+                }
+            }
+            const float sm = fmaxf(b.stat[1][2 * kb], b.stat[1][2 * kb + 1]);
+            const int bad0 = __builtin_amdgcn_readfirstlane(b.bad[2 * kb]);
+            const int bad1 = __builtin_amdgcn_readfirstlane(b.bad[2 * kb + 1]);
+            const int first = key0 + 32 * kb;
+            if (first + 31 > safe || first + 32 > kstop || (bad0 | bad1)) {
+                const int last = (row_pos < kstop ? row_pos : kstop - 1) - first - 4 * half;
+                const int last0 = bad0 ? -1 : last, last1 = bad1 ? -1 : last;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    t[i] = 8 * (i / 4) + i % 4 > (i < 8 ? last0 : last1) ? -__builtin_inff() : t[i];
+            }
+            float tm = t[0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) tm = fmaxf(tm, t[i]);
+            tm *= c1;
+            if (__any(tm > m + kSlack || sm > sref * kScaleSlack)) {
+                tm = max_halves32(tm);
+                const float mn = fmaxf(m, tm);
+                const float sn = fmaxf(fmaxf(sref, kScaleMin), pow2_floor(sm));
+                const float both = __builtin_amdgcn_exp2f(m - mn) * (sref / sn);  // 0 before the first keys
+                l *= both;
+                vz *= both;
+#pragma unroll
+                for (int j = 0; j < C::JT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[j][i] *= both;
+                m = mn;
+                sref = sn;
+                mm = m + (__builtin_amdgcn_logf(sn) - kHeadLog2);
+            }
+        };
+        // The weights of t (block kb of tile b) and their product with the
+        // values, beside the next block's scores u = keys kr . q. The order is
+        // written out: a matrix instruction, then vector work beside it.
+        auto weigh = [&](const typename C::Buf &b, int kb, const f32x16 &t, const typename C::Buf &bn, int kn, f16x8 *kr,
+                         f32x16 &u) {
+            key_operands(bn, kn, C::STEPS / 2, kr);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) u[i] = 0.0f;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {  // 16 keys
+                f16x2 pb[4];
+                f16x8 vr[C::JT];
+#pragma unroll
+                for (int j = 0; j < C::JT; ++j) vr[j] = b.v[((kb * 2 + s) * 2 + half) * D + 32 * j + n];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int at = kb * 32 + 16 * s + 8 * r + 4 * half;
+                    const f32x4 sv = *reinterpret_cast<const f32x4 *>(&b.meta[1][at]);
+                    f32x4 zv;
+                    if (!SYM) zv = *reinterpret_cast<const f32x4 *>(&b.meta[3][at]);
+                    float pv[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        // STEPS / 16 matrix instructions a weight
+                        constexpr int kEvery = C::STEPS >= 16 ? 1 : 16 / C::STEPS;
+                        const int at_i = 8 * s + 4 * r + i;
+                        if (at_i % kEvery == 0) {
+                            u = __builtin_amdgcn_mfma_f32_32x32x16_f16(kr[at_i / kEvery], qf[at_i / kEvery], u, 0, 0, 0);
+                        }
+                        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(t[at_i], c1, -mm));
+                        l += p;
+                        pv[i] = p * sv[i];
+                        if (at_i % kEvery == kEvery - 1) __builtin_amdgcn_sched_barrier(0);
+                    }
+                    pb[2 * r] = f16x2{(_Float16)pv[0], (_Float16)pv[2]};
+                    pb[2 * r + 1] = f16x2{(_Float16)pv[1], (_Float16)pv[3]};
+                    if (!SYM) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            vz = __builtin_fmaf((float)pb[2 * r + (i & 1)][i >> 1], zv[i] - C::kMid, vz);
+                    }
+                }
+                const f16x8 pf = join(pb);
+#pragma unroll
+                for (int j = 0; j < C::JT; ++j)
+                    o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vr[j], pf, o[j], 0, 0, 0);
+            }
+        };
+
+        // One tile: its first block's products are in t already. While a block's
+        // weights are formed the next block's products run (the next tile's first
+        // at the end; past the last tile whatever LDS holds, not used), and the
+        // tile after that goes to LDS. A slot is written one barrier after its
+        // last reader has passed and read one barrier after it is written.
+        int now = 0;  // ring slot of the tile in use
+        auto step = [&](int it, f32x16 &t, f32x16 &u) {
+            const typename C::Buf &b = lds[now], &next = lds[now + 1 < C::RING ? now + 1 : now + 1 - C::RING];
+            const int key0 = kbeg + C::KT * it;
+            if (key0 <= reach) {
+                f16x8 kr[C::STEPS];
+                if constexpr (KBLK == 2) {
+                    key_operands(b, 1, 0, kr);
+                    settle(b, 0, key0, t);
+                    weigh(b, 0, t, b, 1, kr, u);
+                    key_operands(next, 0, 0, kr);
+                    settle(b, 1, key0, u);
+                    weigh(b, 1, u, next, 0, kr, t);
+                } else {
+                    key_operands(next, 0, 0, kr);
+                    settle(b, 0, key0, t);
+                    weigh(b, 0, t, next, 0, kr, u);
+                }
+            }
+            if (it + 2 < its) store(x, lds[now + 2 < C::RING ? now + 2 : now + 2 - C::RING]);
+            if (it + 3 < its) load(x, it + 3);
+            lds_barrier();
+            now = now + 1 < C::RING ? now + 1 : 0;
+        };
+        f32x16 ta, tb;
+        {
+            f16x8 kr[C::STEPS];
+            key_operands(lds[0], 0, 0, kr);
+            key_operands(lds[0], 0, C::STEPS / 2, kr);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) ta[i] = 0.0f;
+#pragma unroll
+            for (int s = 0; s < C::STEPS; ++s) ta = __builtin_amdgcn_mfma_f32_32x32x16_f16(kr[s], qf[s], ta, 0, 0, 0);
+        }
+        for (int it = 0; it < its; ++it) {
+            step(it, ta, tb);
+            if constexpr (KBLK == 1) {
+                if (++it >= its) break;
+                step(it, tb, ta);
+            }
+        }
+        lds_barrier();  // nobody reads the ring any more when the next piece fills it
+        l = add_halves32(l);
+        if (!SYM) vz = add_halves32(vz);
+        if (live) {
+            const int64_t at = (rows.begin + tok) * a.q_heads + qh;
+            const int64_t part = slot_of + wave * 32 + n;
+            l *= sref * (1.0f / kHead);
+            const float f = (whole ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f) * (sref * (1.0f / kHead));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int mrow = 8 * (i / 4) + 4 * half + i % 4;
+#pragma unroll
+                for (int g = 0; g < C::TP / 32; ++g) {
+                    // output tiles j = g, g + TP / 32, ...: DW neighbouring elements
+                    float v[C::DW];
+#pragma unroll
+                    for (int e = 0; e < C::DW; ++e) v[e] = (o[e * (C::TP / 32) + g][i] - vz) * f;
+                    const int d = (g * 32 + mrow) * C::DW;
+                    if (!whole) {
+#pragma unroll
+                        for (int e = 0; e < C::DW; e += 2)
+                            *reinterpret_cast<float2 *>(span.o + part * D + d + e) = float2{v[e], v[e + 1]};
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < C::DW; e += 2) {
+                            const bf16x2_t b{(__bf16)v[e], (__bf16)v[e + 1]};
+                            *reinterpret_cast<uint32_t *>(a.out + at * D + d + e) = __builtin_bit_cast(uint32_t, b);
+                        }
+                    }
+                }
+            }
+            if (half == 0) {
+                if (!whole) {
+                    span.ml[part * 2] = l > 0.0f ? m : -__builtin_inff();
+                    span.ml[part * 2 + 1] = l;
+                } else if (a.lse) {
+                    a.lse[at] = l > 0.0f ? m * kLn2 + logf(l) : -__builtin_inff();
+                }
+            }
+        }
+    }
+}
+
 // Joins the parts of the units that were cut: one block for each border between
 // two spans and key head, which takes the unit that lies across it if this is
 // the unit's first border. D / 4 lanes a row, four parts' loads in flight.
@@ -655,7 +1073,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Span span) {
     const KvRows &rows = p.rows;
     const uint32_t total = (uint32_t)rows.n * (uint32_t)group;
     const int c = threadIdx.x % W;
-    for (int r = threadIdx.x / W; r < ROWS; r += kTeams) {
+    for (int r = blockIdx.y * kTeams + threadIdx.x / W; r < ROWS; r += kTeams * gridDim.y) {
         const uint32_t wr = p.tile * ROWS + r;
         if (wr >= total) break;
         auto slot = [&](int i) { return ((i == 0 ? slot0 : slot1 + 2 * (i - 1)) * a.c.heads + h) * ROWS + r; };
@@ -687,28 +1105,33 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Span span) {
 }
 
 struct Plan {
-    int row_tile, cap;
+    int row_tile, cap, by_unit;
     int64_t bytes;
 };
 constexpr int kFewWaves = 4, kFewStep = 32 * kFewWaves;
 
 Plan plan_of(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b, int64_t room, int64_t max_rows,
              int64_t max_kv) {
-    Plan p;
+    Plan p{};
     const int64_t n = max_rows <= 0 || max_rows > rows ? rows : max_rows;
     const int64_t kv = max_kv <= 0 || max_kv > room ? room : max_kv;
     const int64_t group = q_heads / heads;
-    p.row_tile = n * group <= 8 ? 8 : 16;
-    // no more blocks than steps of work
-    const int64_t tiles = (n * group + p.row_tile - 1) / p.row_tile;
-    const int64_t steps = (kv + kFewStep - 1) / kFewStep;
+    p.row_tile = n * group <= 8 ? 8 : n * group <= 16 ? 16 : 128;
+    const int64_t units = (rows * group + p.row_tile - 1) / p.row_tile + b;  // at most
+    const int64_t step = p.row_tile < 128 ? kFewStep : head_dim == 64 ? 64 : 32;
     // two blocks a CU, what their registers allow: all run at once, and more
     // spans only repeat the fixed part (INT4 decode of 16 sequences with
     // 256, 512, 768, 1024 blocks: 37.6, 32.3, 39.2, 38.7 us)
     int64_t cap = (512 + heads - 1) / heads;
-    if (cap > b * tiles * (steps < 1 ? 1 : steps)) cap = b * tiles * (steps < 1 ? 1 : steps);
+    // many units: blocks take whole ones, and nothing is joined
+    p.by_unit = p.row_tile == 128 && units * heads >= 2048;
+    if (p.by_unit) cap = units;
+    // no more blocks than steps of work
+    const int64_t steps = units * ((kv + step - 1) / step < 1 ? 1 : (kv + step - 1) / step);
+    if (cap > steps) cap = steps;
+    if (cap * heads > (int64_t(1) << 30)) cap = (int64_t(1) << 30) / heads;
     p.cap = (int)cap;
-    p.bytes = cap > 1 ? 2 * cap * heads * p.row_tile * (head_dim + 2) * 4 : 0;
+    p.bytes = cap > 1 && !p.by_unit ? 2 * cap * heads * p.row_tile * (head_dim + 2) * 4 : 0;
     return p;
 }
 
@@ -720,24 +1143,30 @@ int64_t attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, 
 }
 
 template <int D, int BITS, bool SYM, int ROWS>
-static hipError_t launch_few(const AttnArgs &a, const Plan &p, hipStream_t st) {
+static hipError_t launch_tiles(const AttnArgs &a, const Plan &p, hipStream_t st) {
     Span span{static_cast<float *>(a.workspace), nullptr, p.cap};
     span.ml = span.o + (int64_t)2 * p.cap * a.c.heads * ROWS * D;
-    hipLaunchKernelGGL((attn_few_kernel<D, BITS, SYM, ROWS, kFewWaves>), dim3((uint32_t)(p.cap * a.c.heads)),
-                       dim3(64 * kFewWaves), 0, st, a, span);
+    const dim3 grid((uint32_t)(p.cap * a.c.heads));
+    constexpr int step = ROWS < 128 ? kFewStep : Many<D, BITS>::KT;
+    if constexpr (ROWS < 128)
+        hipLaunchKernelGGL((attn_few_kernel<D, BITS, SYM, ROWS, kFewWaves>), grid, dim3(64 * kFewWaves), 0, st, a, span);
+    else
+        hipLaunchKernelGGL((attn_many_kernel<D, BITS, SYM>), grid, dim3(256), 0, st, a, span, p.by_unit);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.cap == 1) return e;
-    hipLaunchKernelGGL((attn_join_kernel<D, ROWS, kFewStep>), dim3((uint32_t)((p.cap - 1) * a.c.heads)), dim3(256), 0, st,
-                       a, span);
+    if (e != hipSuccess || p.cap == 1 || p.by_unit) return e;
+    hipLaunchKernelGGL((attn_join_kernel<D, ROWS, step>), dim3((uint32_t)((p.cap - 1) * a.c.heads), ROWS < 128 ? 1 : 8),
+                       dim3(256), 0, st, a, span);
     return hipGetLastError();
 }
 
 hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st) {
     const Plan p = plan_of(a.batch.rows, a.q_heads, a.c.heads, a.c.head_dim, a.batch.b,
                            a.batch.max_pages << a.c.page_shift, a.max_rows, a.max_kv);
-#define LQ_ATTN(D, BITS, SYM)                                                              \
-    if (a.c.head_dim == D && a.c.bits == BITS && (a.c.symmetric != 0) == SYM)              \
-        return p.row_tile == 8 ? launch_few<D, BITS, SYM, 8>(a, p, st) : launch_few<D, BITS, SYM, 16>(a, p, st);
+#define LQ_ATTN(D, BITS, SYM)                                                                                   \
+    if (a.c.head_dim == D && a.c.bits == BITS && (a.c.symmetric != 0) == SYM)                                   \
+        return p.row_tile == 8    ? launch_tiles<D, BITS, SYM, 8>(a, p, st)                                     \
+               : p.row_tile == 16 ? launch_tiles<D, BITS, SYM, 16>(a, p, st)                                    \
+                                  : launch_tiles<D, BITS, SYM, 128>(a, p, st);
 #define LQ_ATTN_D(D) LQ_ATTN(D, 4, false) LQ_ATTN(D, 4, true) LQ_ATTN(D, 8, false) LQ_ATTN(D, 8, true)
     LQ_ATTN_D(64) LQ_ATTN_D(128) LQ_ATTN_D(256)
 #undef LQ_ATTN_D
