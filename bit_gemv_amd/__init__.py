@@ -448,6 +448,7 @@ def gptq_quantize_noalloc(w: torch.Tensor, u: torch.Tensor, bits: int = 4, symme
 
 
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}  # lq_dtype
+_BF16, _F32, _I32, _I8, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int8, torch.uint8
 
 
 def _dtype(t: torch.Tensor, name: str) -> int:
@@ -457,26 +458,27 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return d
 
 
-def _launch(name: str, device: torch.device, *args) -> None:
-    """The call on the current stream of the tensors' own device."""
+def _launch(name: str, index: int, *args) -> None:
+    """The call on the current stream of the tensors' own device. (A decode
+    step's kernels run for microseconds: this path keeps to a few lookups.)"""
     lib = _lib or load_library()
-    index = device.index
-    if index == torch.cuda.current_device():
-        st = getattr(lib, name)(*args, torch.cuda.current_stream(index).cuda_stream)
+    if index == torch._C._cuda_getDevice():
+        st = getattr(lib, name)(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
-            st = getattr(lib, name)(*args, torch.cuda.current_stream(index).cuda_stream)
+            st = getattr(lib, name)(*args, torch._C._cuda_getCurrentRawStream(index))
     if st != LQ_OK:
         detail = lib.lq_last_error().decode() or lib.lq_status_string(st).decode()
         raise LibquantError(st, name, detail)
 
 
-def _on(device: torch.device, t: torch.Tensor, name: str, dtype, shape):
+def _on(index: int, t: torch.Tensor, name: str, dtype, shape) -> None:
     """_need, on the device of the call's first tensor."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return
     _need(t, name, dtype, shape)
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's first tensor on {device}")
-    return t
+    raise ValueError(f"{name} is on {t.device}, the call's first tensor on cuda:{index}")
 
 
 def rms_norm_int8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, residual: Optional[torch.Tensor] = None,
@@ -485,27 +487,39 @@ def rms_norm_int8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, resi
     """h = x + residual, RMS norm of h times weight, dynamic per-token INT8 of
     that -> (qx int8 [t][k], sx fp32 [t], residual_out or None). x, residual and
     weight bf16 or fp32; residual_out has residual's type and may be residual."""
-    _need(x, "x", x.dtype if isinstance(x, torch.Tensor) else None)
-    xt, dev = _dtype(x, "x"), x.device
-    t, k = x.shape
-    _on(dev, weight, "weight", weight.dtype, (k,))
-    wt, rt = _dtype(weight, "weight"), 0
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    xt, dev, index = _dtype(x, "x"), x.device, x.get_device()
+    if index < 0 or not x.is_contiguous() or x.dim() != 2:
+        _need(x, "x", x.dtype)
+        raise ValueError(f"x must be [t][k], got {tuple(x.shape)}")
+    shape = x.shape
+    t, k = shape
+    if not isinstance(weight, torch.Tensor):
+        raise TypeError("weight must be a torch.Tensor")
+    wt, rt, res_ptr, out_ptr = _dtype(weight, "weight"), 0, None, None
+    _on(index, weight, "weight", weight.dtype, (k,))
     if residual is not None:
-        _on(dev, residual, "residual", residual.dtype, (t, k))
+        if not isinstance(residual, torch.Tensor):
+            raise TypeError("residual must be a torch.Tensor")
         rt = _dtype(residual, "residual")
+        _on(index, residual, "residual", residual.dtype, shape)
         if residual_out is None:
             residual_out = torch.empty_like(residual)
-        _on(dev, residual_out, "residual_out", residual.dtype, (t, k))
+        else:
+            _on(index, residual_out, "residual_out", residual.dtype, shape)
+        res_ptr, out_ptr = residual.data_ptr(), residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out needs residual")
     if qx is None:
-        qx = torch.empty((t, k), dtype=torch.int8, device=dev)
+        qx = torch.empty(shape, dtype=_I8, device=dev)
+    else:
+        _on(index, qx, "qx", _I8, shape)
     if sx is None:
-        sx = torch.empty(t, dtype=torch.float32, device=dev)
-    _on(dev, qx, "qx", torch.int8, (t, k))
-    _on(dev, sx, "sx", torch.float32, (t,))
-    _launch("rms_norm_int8", dev, x.data_ptr(), xt, None if residual is None else residual.data_ptr(), rt,
-            weight.data_ptr(), wt, t, k, float(eps), None if residual is None else residual_out.data_ptr(),
+        sx = torch.empty((t,), dtype=_F32, device=dev)
+    else:
+        _on(index, sx, "sx", _F32, (t,))
+    _launch("rms_norm_int8", index, x.data_ptr(), xt, res_ptr, rt, weight.data_ptr(), wt, t, k, eps, out_ptr,
             qx.data_ptr(), sx.data_ptr())
     return qx, sx, residual_out
 
@@ -532,19 +546,20 @@ class KVCache:
         if not isinstance(k_codes, torch.Tensor) or k_codes.dim() != 4:
             raise ValueError("k_codes must be a tensor [pages][heads][page_size][row]")
         row, dev = head_dim * bits // 8, k_codes.device
-        pages, heads, page_size = k_codes.shape[:3]
+        pages, heads, page_size, _ = k_codes.shape
         meta = (pages, heads, page_size)
-        _need(k_codes, "k_codes", torch.uint8, (*meta, row))
-        _on(dev, v_codes, "v_codes", torch.uint8, (pages, heads, page_size // 4, row, 4))
-        _on(dev, k_scales, "k_scales", torch.float32, meta)
-        _on(dev, v_scales, "v_scales", torch.float32, meta)
+        _need(k_codes, "k_codes", _U8, (*meta, row))
+        index = k_codes.get_device()
+        _on(index, v_codes, "v_codes", _U8, (pages, heads, page_size // 4, row, 4))
+        _on(index, k_scales, "k_scales", _F32, meta)
+        _on(index, v_scales, "v_scales", _F32, meta)
         if k_zeros is not None:
-            _on(dev, k_zeros, "k_zeros", torch.float32, meta)
-            _on(dev, v_zeros, "v_zeros", torch.float32, meta)
+            _on(index, k_zeros, "k_zeros", _F32, meta)
+            _on(index, v_zeros, "v_zeros", _F32, meta)
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.k_zeros, self.v_zeros = k_zeros, v_zeros
         self.pages, self.heads, self.page_size, self.head_dim = pages, heads, page_size, head_dim
-        self.bits, self.symmetric, self.device = bits, k_zeros is None, dev
+        self.bits, self.symmetric, self.device, self._index = bits, k_zeros is None, dev, index
         self._record = _KvCacheRecord(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
                                       None if k_zeros is None else k_zeros.data_ptr(), v_scales.data_ptr(),
                                       None if v_zeros is None else v_zeros.data_ptr(), pages, page_size, heads,
@@ -568,14 +583,14 @@ class KVCache:
         return self.k_codes.numel() * 2 + self.k_scales.numel() * (8 if self.symmetric else 16)
 
 
-def _batch(cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor, row_starts: torch.Tensor):
+def _batch(index: int, block_table: torch.Tensor, kv_lens: torch.Tensor, row_starts: torch.Tensor):
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be a tensor [b][max_pages]")
-    b, dev = block_table.shape[0], cache.device
-    _on(dev, block_table, "block_table", torch.int32, None)
-    _on(dev, kv_lens, "kv_lens", torch.int32, (b,))
-    _on(dev, row_starts, "row_starts", torch.int32, (b + 1,))
-    return block_table.data_ptr(), block_table.shape[1], kv_lens.data_ptr(), row_starts.data_ptr(), b
+    b, max_pages = block_table.shape
+    _on(index, block_table, "block_table", _I32, None)
+    _on(index, kv_lens, "kv_lens", _I32, (b,))
+    _on(index, row_starts, "row_starts", _I32, (b + 1,))
+    return block_table.data_ptr(), max_pages, kv_lens.data_ptr(), row_starts.data_ptr(), b
 
 
 def _rows(cache: KVCache, t: torch.Tensor, name: str, heads: Optional[int]) -> int:
@@ -583,12 +598,12 @@ def _rows(cache: KVCache, t: torch.Tensor, name: str, heads: Optional[int]) -> i
     fused product's output); the step from row to row."""
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
         raise ValueError(f"{name} must be a tensor [rows][heads][head_dim]")
-    if t.device != cache.device:
+    if t.get_device() != cache._index:
         raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
     d = cache.head_dim
-    if t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+    rows, h, width = t.shape
+    if width != d or (heads is not None and h != heads):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, the cache {cache.heads} heads of {d}")
-    rows, h, _ = t.shape
     step = t.stride()
     if step[2] != 1 or (h > 1 and step[1] != d):
         raise ValueError(f"{name}: a row's heads must be contiguous")
@@ -604,8 +619,8 @@ def kv_cache_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, block_table
     ks, vs = _rows(cache, k, "k", cache.heads), _rows(cache, v, "v", cache.heads)
     if v.shape != k.shape or v.dtype != k.dtype:
         raise ValueError("k and v must share shape and type")
-    _launch("kv_cache_write", cache.device, cache._ref, k.data_ptr(), v.data_ptr(), _dtype(k, "k"), k.shape[0], ks, vs,
-            *_batch(cache, block_table, kv_lens, row_starts), int(max_rows))
+    _launch("kv_cache_write", cache._index, cache._ref, k.data_ptr(), v.data_ptr(), _dtype(k, "k"), k.shape[0], ks, vs,
+            *_batch(cache._index, block_table, kv_lens, row_starts), max_rows)
 
 
 def kv_cache_read(cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor, row_starts: torch.Tensor,
@@ -614,15 +629,17 @@ def kv_cache_read(cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tens
     """The values (q - z) s of the rows' keys and values, [rows][heads][head_dim]
     of dtype (bf16 or fp32) -> (k, v). Rows that belong to no sequence are left
     as they were in k and v."""
-    shape = (rows, cache.heads, cache.head_dim)
+    shape, index = (rows, cache.heads, cache.head_dim), cache._index
     if k is None:
         k = torch.empty(shape, dtype=dtype, device=cache.device)
+    else:
+        _on(index, k, "k", dtype, shape)
     if v is None:
         v = torch.empty(shape, dtype=dtype, device=cache.device)
-    _on(cache.device, k, "k", dtype, shape)
-    _on(cache.device, v, "v", dtype, shape)
-    _launch("kv_cache_read", cache.device, cache._ref, k.data_ptr(), v.data_ptr(), _dtype(k, "k"), rows,
-            *_batch(cache, block_table, kv_lens, row_starts), int(max_rows))
+    else:
+        _on(index, v, "v", dtype, shape)
+    _launch("kv_cache_read", index, cache._ref, k.data_ptr(), v.data_ptr(), _dtype(k, "k"), rows,
+            *_batch(index, block_table, kv_lens, row_starts), max_rows)
     return k, v
 
 
@@ -637,28 +654,30 @@ def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     max_rows and max_kv bound any one sequence's rows and tokens, if known;
     workspace: uint8, of at least paged_attention_workspace(...) bytes."""
     qs = _rows(cache, q, "q", None)
-    if q.dtype != torch.bfloat16:
-        raise TypeError(f"q must be {torch.bfloat16}, got {q.dtype}")
-    rows, q_heads, d = q.shape
-    dev = cache.device
-    table, max_pages, lens, starts, b = _batch(cache, block_table, kv_lens, row_starts)
+    if q.dtype is not _BF16:
+        raise TypeError(f"q must be {_BF16}, got {q.dtype}")
+    shape = rows, q_heads, d = q.shape
+    index = cache._index
+    table, max_pages, lens, starts, b = _batch(index, block_table, kv_lens, row_starts)
     if out is None:
-        out = torch.empty((rows, q_heads, d), dtype=torch.bfloat16, device=dev)
+        out = torch.empty(shape, dtype=_BF16, device=cache.device)
     else:
-        _on(dev, out, "out", torch.bfloat16, (rows, q_heads, d))
+        _on(index, out, "out", _BF16, shape)
     if lse is not None:
-        _on(dev, lse, "lse", torch.float32, (rows, q_heads))
+        _on(index, lse, "lse", _F32, (rows, q_heads))
+    ws_ptr, ws_bytes = None, 0
     if workspace is None:
-        need = (_lib or load_library()).paged_attention_workspace_bytes(rows, q_heads, cache.heads, d, b, max_pages,
-                                                                        cache.page_size, max_rows, max_kv)
-        if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws_bytes = (_lib or load_library()).paged_attention_workspace_bytes(rows, q_heads, cache.heads, d, b, max_pages,
+                                                                            cache.page_size, max_rows, max_kv)
+        if ws_bytes > 0:
+            workspace = torch.empty((ws_bytes,), dtype=_U8, device=cache.device)
+            ws_ptr = workspace.data_ptr()
     else:
-        _on(dev, workspace, "workspace", torch.uint8, None)
-    _launch("paged_attention", dev, cache._ref, q.data_ptr(), rows, q_heads, qs,
-            d ** -0.5 if scale is None else float(scale), table, max_pages, lens, starts, b, int(max_rows), int(max_kv),
-            None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
-            out.data_ptr(), None if lse is None else lse.data_ptr())
+        _on(index, workspace, "workspace", _U8, None)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
+    _launch("paged_attention", index, cache._ref, q.data_ptr(), rows, q_heads, qs, d ** -0.5 if scale is None else scale,
+            table, max_pages, lens, starts, b, max_rows, max_kv, ws_ptr, ws_bytes, out.data_ptr(),
+            None if lse is None else lse.data_ptr())
     return out
 
 
