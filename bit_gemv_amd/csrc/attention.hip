@@ -310,7 +310,7 @@ LQ_DEVICE float q_to_fp16(const u32x4 *raw, float scale, f16x8 *qf, float &qsum)
 }
 
 template <int D, int BITS, bool SYM, int ROWS, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, 2) void attn_few_kernel(AttnArgs a, Span span) {
+__global__ __launch_bounds__(64 * WAVES, 2) void attn_few_kernel(AttnArgs a, Span span, int by_unit) {
     using C = Few<D, BITS, SYM, ROWS>;
     constexpr int LDO = D + 4;
     constexpr int kStride = 32 * WAVES;  // keys from one of a wave's tiles to its next
@@ -331,7 +331,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_few_kernel(AttnArgs a, Spa
 
     const uint32_t magic = fp16_magic();
 
-    const Schedule<kStride> sched(a.batch, shift, group, ROWS, lane);
+    const Schedule<kStride> sched(a.batch, shift, group, ROWS, lane, by_unit);
     const int64_t all_steps = sched.total(), share = uniform_div(all_steps + span.cap - 1, span.cap);
     const int64_t begin = block * share, end = begin + share < all_steps ? begin + share : all_steps;
     for (int64_t pos = begin; pos < end;) {
@@ -339,7 +339,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_few_kernel(AttnArgs a, Spa
         const int64_t seq = piece.seq;
         const uint32_t tile = piece.tile;
         const int step0 = (int)(pos - piece.start);
-        const int step1 = end - piece.start < piece.steps ? (int)(end - piece.start) : piece.steps;
+        int step1 = end - piece.start < piece.steps ? (int)(end - piece.start) : piece.steps;
         const bool whole = step0 == 0 && step1 == piece.steps;
         const int64_t slot_of = ((int64_t)(2 * block + (pos > begin)) * a.c.heads + h) * ROWS;
         pos = piece.start + step1;
@@ -357,6 +357,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_few_kernel(AttnArgs a, Spa
         int64_t kend64 = rows.first + last_row + 1;
         kend64 = kend64 > rows.len ? rows.len : kend64;
         const int kend = kend64 < 0 ? 0 : (int)kend64;
+        if (by_unit) step1 = (kend + kStride - 1) / kStride;
         const int kbeg = step0 * kStride < kend ? step0 * kStride : kend;
         const int kstop = (int64_t)step1 * kStride < kend ? step1 * kStride : kend;
         const int top = (kstop - 1) & ~15;  // the piece's last 16 keys
@@ -1118,14 +1119,20 @@ Plan plan_of(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int
     const int64_t group = q_heads / heads;
     p.row_tile = n * group <= 8 ? 8 : n * group <= 16 ? 16 : 128;
     const int64_t units = (rows * group + p.row_tile - 1) / p.row_tile + b;  // at most
+    const int64_t tiles = (n * group + p.row_tile - 1) / p.row_tile;         // of a sequence
     const int64_t step = p.row_tile < 128 ? kFewStep : head_dim == 64 ? 64 : 32;
     // two blocks a CU, what their registers allow: all run at once, and more
     // spans only repeat the fixed part (INT4 decode of 16 sequences with
     // 256, 512, 768, 1024 blocks: 37.6, 32.3, 39.2, 38.7 us)
     int64_t cap = (512 + heads - 1) / heads;
-    // many units: blocks take whole ones, and nothing is joined
-    p.by_unit = p.row_tile == 128 && units * heads >= 2048;
-    if (p.by_unit) cap = units;
+    // Blocks take whole units, and nothing is joined: chunks of many units, and
+    // decode batches of short contexts, which would spend longer on the second
+    // launch (a pass over spans and over units: 1 x 1003 tokens on one head 16.3
+    // and 12.1 us, 64 x 500 on 8 heads 20.9 and 13.7, 16 x 2000 on 8 heads 20.4
+    // and 17.7; 4 x 2000 on 8 heads 15.8 and 17.5).
+    const int64_t likely = b * tiles < units ? b * tiles : units;
+    p.by_unit = p.row_tile == 128 ? units * heads >= 2048 : kv <= 1024 || (kv <= 2048 && likely * heads >= 128);
+    if (p.by_unit) cap = p.row_tile == 128 ? units : likely;
     // no more blocks than steps of work
     const int64_t steps = units * ((kv + step - 1) / step < 1 ? 1 : (kv + step - 1) / step);
     if (cap > steps) cap = steps;
@@ -1149,7 +1156,8 @@ static hipError_t launch_tiles(const AttnArgs &a, const Plan &p, hipStream_t st)
     const dim3 grid((uint32_t)(p.cap * a.c.heads));
     constexpr int step = ROWS < 128 ? kFewStep : Many<D, BITS>::KT;
     if constexpr (ROWS < 128)
-        hipLaunchKernelGGL((attn_few_kernel<D, BITS, SYM, ROWS, kFewWaves>), grid, dim3(64 * kFewWaves), 0, st, a, span);
+        hipLaunchKernelGGL((attn_few_kernel<D, BITS, SYM, ROWS, kFewWaves>), grid, dim3(64 * kFewWaves), 0, st, a, span,
+                           p.by_unit);
     else
         hipLaunchKernelGGL((attn_many_kernel<D, BITS, SYM>), grid, dim3(256), 0, st, a, span, p.by_unit);
     const hipError_t e = hipGetLastError();
