@@ -16,24 +16,45 @@ namespace {
 
 constexpr int kTpb = 256;
 
+// 8 elements as they lie, and as fp32
 template <bool F32>
-LQ_DEVICE void load_row8(const void *p, int64_t e, float *f) {
-    if constexpr (F32) {
-        const f32x4 *q = reinterpret_cast<const f32x4 *>(static_cast<const float *>(p) + e);
-        const f32x4 a = q[0], b = q[1];
+struct Raw {
+    u32x4 a[F32 ? 2 : 1];
+};
+template <bool F32>
+LQ_DEVICE Raw<F32> load_row8(const void *p, int64_t e) {
+    Raw<F32> r;
+    const u32x4 *q = reinterpret_cast<const u32x4 *>(static_cast<const char *>(p) + e * (F32 ? 4 : 2));
+    r.a[0] = q[0];
+    if constexpr (F32) r.a[1] = q[1];
+    return r;
+}
+template <bool F32>
+LQ_DEVICE void widen_row8(const Raw<F32> &r, bool in, float *f) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[j] = a[j];
-            f[4 + j] = b[j];
-        }
-    } else {
-        const u32x4 a = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p) + e);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[2 * j] = bf16_lo(a[j]);
-            f[2 * j + 1] = bf16_hi(a[j]);
-        }
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t w = F32 ? r.a[F32 ? j / 4 : 0][j % 4] : r.a[0][j / 2];
+        const float v = F32 ? __uint_as_float(w) : j % 2 ? bf16_hi(w) : bf16_lo(w);
+        f[j] = in ? v : 0.0f;
     }
+}
+
+// Maximum over the team's W (8, 16 or 32) lanes.
+template <int CTRL>
+LQ_DEVICE float dpp_f32(float v) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+template <int W>
+LQ_DEVICE float lanes_max(float v) {
+    v = fmaxf(v, dpp_f32<kDppXor1>(v));
+    v = fmaxf(v, dpp_f32<kDppXor2>(v));
+    v = fmaxf(v, dpp_f32<kDppHalfMirror>(v));
+    if constexpr (W >= 16) v = fmaxf(v, dpp_f32<kDppMirror>(v));
+    if constexpr (W >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    }
+    return v;
 }
 
 // Scale, zero and codes (stored unsigned) of the team's D elements, 8 in this
@@ -72,7 +93,7 @@ LQ_DEVICE void encode8(const float *x, float &s, float &z, uint32_t *c) {
         float a = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(x[j]));
-        top = team_max<W>(a);
+        top = lanes_max<W>(a);
         s = (top < kFloor ? kFloor : top) * (1.0f / qmax);
         z = 0.0f;
     } else {
@@ -83,8 +104,8 @@ LQ_DEVICE void encode8(const float *x, float &s, float &z, uint32_t *c) {
             lo = fminf(lo, x[j]);
             hi = fmaxf(hi, x[j]);
         }
-        lo = team_min<W>(lo);
-        hi = team_max<W>(hi);
+        lo = -lanes_max<W>(-lo);
+        hi = lanes_max<W>(hi);
         const float range = hi - lo;
         s = (range < kFloor ? kFloor : range) * (1.0f / levels);
         z = rintf(-lo / s) + 0.0f;  // -0 -> +0
@@ -143,17 +164,19 @@ __global__ __launch_bounds__(kTpb) void kv_write_kernel(KvWriteArgs a) {
             uint32_t code[4][8];
             float s[4], z[4];
             bool in[4];
-            float x[4][8];
+            // all four rows' loads at once: rows that are not the call's read a
+            // neighbour instead
+            Raw<F32> raw[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int64_t row = it.quad * 4 + u - rows.first;
+                int64_t row = it.quad * 4 + u - rows.first;
                 in[u] = row >= 0 && row < rows.n;
-                if (in[u])
-                    load_row8<F32>(src, (rows.begin + row) * stride + (int64_t)it.head * D + lane * 8, x[u]);
-                else
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[u][j] = 0.0f;
+                row = row < 0 ? 0 : row < rows.n ? row : rows.n - 1;
+                raw[u] = load_row8<F32>(src, (rows.begin + row) * stride + (int64_t)it.head * D + lane * 8);
             }
+            float x[4][8];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) widen_row8<F32>(raw[u], in[u], x[u]);
 #pragma unroll
             for (int u = 0; u < 4; ++u) encode8<D, BITS, SYM>(x[u], s[u], z[u], code[u]);
             const int64_t slot = ((page * a.c.heads + it.head) << a.c.page_shift) +
