@@ -752,10 +752,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_many_kernel(AttnAr
         const uint32_t tok = live ? rr / (uint32_t)group : 0;
         const int qh = h * group + (int)(live ? rr - tok * (uint32_t)group : 0);
         const uint32_t block_last = (tile * C::ROWS + C::ROWS - 1 < total ? tile * C::ROWS + C::ROWS - 1 : total - 1) / (uint32_t)group;
-        const uint32_t wave_last = (wave_row + 31 < total ? wave_row + 31 : total - 1) / (uint32_t)group;
         const int row_pos = live ? (int)(rows.first + tok) : -1;
         const int safe = (int)(rows.first + wave_row / (uint32_t)group);
-        const int reach = wave_row < total ? (int)(rows.first + wave_last) : -1;  // last key any row of the wave sees
         int64_t kend64 = rows.first + block_last + 1;
         kend64 = kend64 > rows.len ? rows.len : kend64;
         const int kend = kend64 < 0 ? 0 : (int)kend64;
@@ -791,43 +789,49 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_many_kernel(AttnAr
             x.dead = x.bad | (key0 + (lane & 15) >= kstop);
             x.meta = meta_src[slot];
         };
-        auto store = [&](const typename C::Load &x, typename C::Buf &b) {
-#pragma unroll
-            for (int c = 0; c < C::KC; ++c) {
-                f16x2 f[4];
+        // one 16-byte write of the tile: i below KC a chunk of keys, then values
+        auto store_part = [&](const typename C::Load &x, typename C::Buf &b, int i) {
+            f16x2 f[4];
+            if (i < C::KC) {
                 if constexpr (BITS == 8) {
-                    int8_row(x.k[2 * c], f);
-                    int8_row(x.k[2 * c + 1], f + 2);
+                    int8_row(x.k[(2 * i) % (C::KB / 4)], f);
+                    int8_row(x.k[(2 * i + 1) % (C::KB / 4)], f + 2);
                 } else {
-                    const uint32_t w = x.k[c], w8 = w >> 8;
+                    const uint32_t w = x.k[i % (C::KB / 4)], w8 = w >> 8;
                     f[0] = int4_low(w, magic); f[1] = int4_high(w, magic);
                     f[2] = int4_low(w8, magic); f[3] = int4_high(w8, magic);
                 }
-                b.k[(my_part * C::KC + c) * C::KPAD + my_key] = join(f);
-            }
-            f16x8 *vp = &b.v[my_pair * D + my_t];
-#pragma unroll
-            for (int w = 0; w < C::VW; ++w) {
-                f16x2 f[4];
+                b.k[(my_part * C::KC + i) * C::KPAD + my_key] = join(f);
+            } else {
+                const int e = i - C::KC;  // which of the thread's elements
                 if constexpr (BITS == 8) {
-                    int8_quad(x.v0[w], f);
-                    int8_quad(x.v1[w], f + 2);
-                    vp[w * C::TP] = join(f);
+                    int8_quad(x.v0[e % C::VW], f);
+                    int8_quad(x.v1[e % C::VW], f + 2);
                 } else {
-                    const uint32_t v0 = x.v0[w], v1 = x.v1[w], v08 = v0 >> 8, v18 = v1 >> 8;
-                    f[0] = int4_low(v0, magic); f[1] = int4_low(v08, magic);
-                    f[2] = int4_low(v1, magic); f[3] = int4_low(v18, magic);
-                    vp[2 * w * C::TP] = join(f);
-                    f[0] = int4_high(v0, magic); f[1] = int4_high(v08, magic);
-                    f[2] = int4_high(v1, magic); f[3] = int4_high(v18, magic);
-                    vp[(2 * w + 1) * C::TP] = join(f);
+                    const uint32_t v0 = x.v0[(e >> 1) % C::VW], v1 = x.v1[(e >> 1) % C::VW];
+                    if (e & 1) {
+                        f[0] = int4_high(v0, magic); f[1] = int4_high(v0 >> 8, magic);
+                        f[2] = int4_high(v1, magic); f[3] = int4_high(v1 >> 8, magic);
+                    } else {
+                        f[0] = int4_low(v0, magic); f[1] = int4_low(v0 >> 8, magic);
+                        f[2] = int4_low(v1, magic); f[3] = int4_low(v1 >> 8, magic);
+                    }
                 }
+                b.v[my_pair * D + my_t + e * C::TP] = join(f);
             }
+        };
+        constexpr int kParts = C::KC + C::DW;
+        auto store_meta = [&](const typename C::Load &x, typename C::Buf &b) {
             // slots that hold nothing count as zeros
             const float meta = x.dead ? (lane < 32 ? 0.0f : C::kMid) : x.meta;
             b.meta[lane >> 4][16 * my_group + (lane & 15)] = meta;
             b.stat[lane >> 4][my_group] = row_max(meta);
             b.bad[my_group] = x.bad;
+        };
+        auto store = [&](const typename C::Load &x, typename C::Buf &b) {
+            store_meta(x, b);
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) store_part(x, b, i);
         };
 
         typename C::Load x;
@@ -847,11 +851,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_many_kernel(AttnAr
             if (!SYM) qsum = add_halves32(qsum);
         }
         if (its > 0) store(x, lds[0]);
-        if (its > 1) {
+        if (its > 0) {
             load(x, 1);
             store(x, lds[1]);
+            load(x, 2);
         }
-        if (its > 2) load(x, 2);
         lds_barrier();
 
         f32x16 o[C::JT];
@@ -914,52 +918,71 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_many_kernel(AttnAr
                 mm = m + (__builtin_amdgcn_logf(sn) - kHeadLog2);
             }
         };
-        // The weights of t (block kb of tile b) and their product with the
-        // values, beside the next block's scores u = keys kr . q. The order is
-        // written out: a matrix instruction, then vector work beside it.
+        // value scales (and zeros) of a lane's keys of block kb
+        auto value_meta = [&](const typename C::Buf &b, int kb, int s, f32x4 *sv, f32x4 *zv) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int at = kb * 32 + 16 * s + 8 * r + 4 * half;
+                sv[r] = *reinterpret_cast<const f32x4 *>(&b.meta[1][at]);
+                if (!SYM) zv[r] = *reinterpret_cast<const f32x4 *>(&b.meta[3][at]);
+            }
+        };
+        // The weights of t (block kb of tile b), their product with the values,
+        // the next block's scores u = keys kr . q, and (STORE) the tile x on its
+        // way to LDS. The order is written out, so that no matrix instruction
+        // stands alone: JT groups of the first 16 keys' weights, each beside a
+        // score instruction; JT groups of the others', each beside a score and a
+        // value instruction; then the other value instructions beside the
+        // conversion of x. Without it each wave did one kind of work after the
+        // other and the two waves of a SIMD rarely met in different kinds.
         auto weigh = [&](const typename C::Buf &b, int kb, const f32x16 &t, const typename C::Buf &bn, int kn, f16x8 *kr,
-                         f32x16 &u) {
+                         f32x4 *sv, f32x4 *zv, f32x16 &u, bool with_store, typename C::Buf &to) {
+            constexpr int EG = 8 / C::JT;  // weights of a group
             key_operands(bn, kn, C::STEPS / 2, kr);
+            f16x8 vr[C::JT], pf[2];
+#pragma unroll
+            for (int j = 0; j < C::JT; ++j) vr[j] = b.v[(kb * 4 + half) * D + 32 * j + n];
 #pragma unroll
             for (int i = 0; i < 16; ++i) u[i] = 0.0f;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {  // 16 keys
-                f16x2 pb[4];
-                f16x8 vr[C::JT];
+                float pv[8];
 #pragma unroll
-                for (int j = 0; j < C::JT; ++j) vr[j] = b.v[((kb * 2 + s) * 2 + half) * D + 32 * j + n];
+                for (int g = 0; g < C::JT; ++g) {
+                    u = __builtin_amdgcn_mfma_f32_32x32x16_f16(kr[s * C::JT + g], qf[s * C::JT + g], u, 0, 0, 0);
+                    if (s == 1) o[g] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vr[g], pf[0], o[g], 0, 0, 0);
+#pragma unroll
+                    for (int i = g * EG; i < (g + 1) * EG; ++i) {
+                        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(t[8 * s + i], c1, -mm));
+                        l += p;
+                        pv[i] = p * sv[i / 4][i % 4];
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (s == 1) vr[g] = b.v[(kb * 4 + 2 + half) * D + 32 * g + n];
+                }
+                f16x2 pb[4];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const int at = kb * 32 + 16 * s + 8 * r + 4 * half;
-                    const f32x4 sv = *reinterpret_cast<const f32x4 *>(&b.meta[1][at]);
-                    f32x4 zv;
-                    if (!SYM) zv = *reinterpret_cast<const f32x4 *>(&b.meta[3][at]);
-                    float pv[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        // STEPS / 16 matrix instructions a weight
-                        constexpr int kEvery = C::STEPS >= 16 ? 1 : 16 / C::STEPS;
-                        const int at_i = 8 * s + 4 * r + i;
-                        if (at_i % kEvery == 0) {
-                            u = __builtin_amdgcn_mfma_f32_32x32x16_f16(kr[at_i / kEvery], qf[at_i / kEvery], u, 0, 0, 0);
-                        }
-                        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(t[at_i], c1, -mm));
-                        l += p;
-                        pv[i] = p * sv[i];
-                        if (at_i % kEvery == kEvery - 1) __builtin_amdgcn_sched_barrier(0);
-                    }
-                    pb[2 * r] = f16x2{(_Float16)pv[0], (_Float16)pv[2]};
-                    pb[2 * r + 1] = f16x2{(_Float16)pv[1], (_Float16)pv[3]};
+                    pb[2 * r] = f16x2{(_Float16)pv[4 * r], (_Float16)pv[4 * r + 2]};
+                    pb[2 * r + 1] = f16x2{(_Float16)pv[4 * r + 1], (_Float16)pv[4 * r + 3]};
                     if (!SYM) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            vz = __builtin_fmaf((float)pb[2 * r + (i & 1)][i >> 1], zv[i] - C::kMid, vz);
+                            vz = __builtin_fmaf((float)pb[2 * r + (i & 1)][i >> 1], zv[r][i] - C::kMid, vz);
                     }
                 }
-                const f16x8 pf = join(pb);
+                pf[s] = join(pb);
+                if (s == 0) value_meta(b, kb, 1, sv, zv);
+            }
+            if (with_store) store_meta(x, to);
 #pragma unroll
-                for (int j = 0; j < C::JT; ++j)
-                    o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vr[j], pf, o[j], 0, 0, 0);
+            for (int g = 0; g < C::JT; ++g) {
+                o[g] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vr[g], pf[1], o[g], 0, 0, 0);
+                if (with_store) {
+#pragma unroll
+                    for (int i = g * kParts / C::JT; i < (g + 1) * kParts / C::JT; ++i) store_part(x, to, i);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
         };
 
@@ -972,28 +995,37 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_many_kernel(AttnAr
         auto step = [&](int it, f32x16 &t, f32x16 &u) {
             const typename C::Buf &b = lds[now], &next = lds[now + 1 < C::RING ? now + 1 : now + 1 - C::RING];
             const int key0 = kbeg + C::KT * it;
-            if (key0 <= reach) {
-                f16x8 kr[C::STEPS];
-                if constexpr (KBLK == 2) {
-                    key_operands(b, 1, 0, kr);
-                    settle(b, 0, key0, t);
-                    weigh(b, 0, t, b, 1, kr, u);
-                    key_operands(next, 0, 0, kr);
-                    settle(b, 1, key0, u);
-                    weigh(b, 1, u, next, 0, kr, t);
-                } else {
-                    key_operands(next, 0, 0, kr);
-                    settle(b, 0, key0, t);
-                    weigh(b, 0, t, next, 0, kr, u);
-                }
+            typename C::Buf &to = lds[now + 2 < C::RING ? now + 2 : now + 2 - C::RING];
+            f16x8 kr[C::STEPS];
+            f32x4 sv[2], zv[2];
+            if constexpr (KBLK == 2) {
+                key_operands(b, 1, 0, kr);
+                value_meta(b, 0, 0, sv, zv);
+                settle(b, 0, key0, t);
+                weigh(b, 0, t, b, 1, kr, sv, zv, u, false, to);
+                key_operands(next, 0, 0, kr);
+                value_meta(b, 1, 0, sv, zv);
+                settle(b, 1, key0, u);
+                weigh(b, 1, u, next, 0, kr, sv, zv, t, true, to);
+            } else {
+                key_operands(next, 0, 0, kr);
+                value_meta(b, 0, 0, sv, zv);
+                settle(b, 0, key0, t);
+                weigh(b, 0, t, next, 0, kr, sv, zv, u, true, to);
             }
-            if (it + 2 < its) store(x, lds[now + 2 < C::RING ? now + 2 : now + 2 - C::RING]);
             if (it + 3 < its) load(x, it + 3);
             lds_barrier();
             now = now + 1 < C::RING ? now + 1 : 0;
         };
-        f32x16 ta, tb;
-        {
+        if (wave_row >= total) {  // no rows of its own: it only brings its part of the tiles
+            for (int it = 0; it < its; ++it) {
+                store(x, lds[now + 2 < C::RING ? now + 2 : now + 2 - C::RING]);
+                if (it + 3 < its) load(x, it + 3);
+                lds_barrier();
+                now = now + 1 < C::RING ? now + 1 : 0;
+            }
+        } else if (its > 0) {
+            f32x16 ta, tb;
             f16x8 kr[C::STEPS];
             key_operands(lds[0], 0, 0, kr);
             key_operands(lds[0], 0, C::STEPS / 2, kr);
@@ -1001,12 +1033,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_many_kernel(AttnAr
             for (int i = 0; i < 16; ++i) ta[i] = 0.0f;
 #pragma unroll
             for (int s = 0; s < C::STEPS; ++s) ta = __builtin_amdgcn_mfma_f32_32x32x16_f16(kr[s], qf[s], ta, 0, 0, 0);
-        }
-        for (int it = 0; it < its; ++it) {
-            step(it, ta, tb);
-            if constexpr (KBLK == 1) {
-                if (++it >= its) break;
-                step(it, tb, ta);
+            for (int it = 0; it < its; ++it) {
+                step(it, ta, tb);
+                if constexpr (KBLK == 1) {
+                    if (++it >= its) break;
+                    step(it, tb, ta);
+                }
             }
         }
         lds_barrier();  // nobody reads the ring any more when the next piece fills it
