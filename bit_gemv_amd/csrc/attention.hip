@@ -117,6 +117,8 @@ struct Span {
     float *o;   // [2 cap][heads][rows of a tile][D], relative to the part's maximum
     float *ml;  // [2 cap][heads][rows of a tile][2]: maximum (log2) and sum
     int cap;
+    int by_unit;           // every unit counts as one step: blocks take whole units
+    uint32_t least, most;  // sequences of another number of query rows (all heads of a group) are not looked at
 };
 
 struct Piece {
@@ -164,8 +166,8 @@ struct Schedule {
         int64_t all, upto;  // of all of them, and of the sequences up to this one
     };
     const KvBatch &bt;
+    const Span &span;
     const int shift, group, row_tile, lane;
-    const bool by_unit;  // every unit counts as one step: blocks take whole units
     Lane first;
 
     LQ_DEVICE Lane load(int64_t seq, int64_t before) const {
@@ -173,18 +175,19 @@ struct Schedule {
         x.steps = 1;
         if (seq < bt.b) {
             x.rows = kv_rows(bt, seq, shift);
-            if (x.rows.n > 0) {
+            const uint32_t all_rows = (uint32_t)x.rows.n * (uint32_t)group;
+            if (all_rows >= span.least && all_rows <= span.most) {
                 int64_t keys = x.rows.first + x.rows.n < x.rows.len ? x.rows.first + x.rows.n : x.rows.len;
                 keys = keys < 1 ? 1 : keys;  // a unit without keys is still written
-                x.steps = by_unit ? 1 : (int)((keys + STEP - 1) / STEP);
-                x.all = (int64_t)(((uint32_t)x.rows.n * (uint32_t)group + row_tile - 1) / (uint32_t)row_tile) * x.steps;
+                x.steps = span.by_unit ? 1 : (int)((keys + STEP - 1) / STEP);
+                x.all = (int64_t)((all_rows + row_tile - 1) / (uint32_t)row_tile) * x.steps;
             }
         }
         x.upto = before + scan64(x.all);
         return x;
     }
-    LQ_DEVICE Schedule(const KvBatch &b, int sh, int g, int rt, int l, bool unit = false)
-        : bt(b), shift(sh), group(g), row_tile(rt), lane(l), by_unit(unit) {
+    LQ_DEVICE Schedule(const KvBatch &b, const Span &sp, int sh, int g, int rt, int l)
+        : bt(b), span(sp), shift(sh), group(g), row_tile(rt), lane(l) {
         first = load(lane, 0);
     }
     LQ_DEVICE int64_t total() const {
@@ -310,7 +313,7 @@ LQ_DEVICE float q_to_fp16(const u32x4 *raw, float scale, f16x8 *qf, float &qsum)
 }
 
 template <int D, int BITS, bool SYM, int ROWS, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, 2) void attn_few_kernel(AttnArgs a, Span span, int by_unit) {
+__global__ __launch_bounds__(64 * WAVES, 2) void attn_few_kernel(AttnArgs a, Span span) {
     using C = Few<D, BITS, SYM, ROWS>;
     constexpr int LDO = D + 4;
     constexpr int kStride = 32 * WAVES;  // keys from one of a wave's tiles to its next
@@ -331,7 +334,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_few_kernel(AttnArgs a, Spa
 
     const uint32_t magic = fp16_magic();
 
-    const Schedule<kStride> sched(a.batch, shift, group, ROWS, lane, by_unit);
+    const Schedule<kStride> sched(a.batch, span, shift, group, ROWS, lane);
     const int64_t all_steps = sched.total(), share = uniform_div(all_steps + span.cap - 1, span.cap);
     const int64_t begin = block * share, end = begin + share < all_steps ? begin + share : all_steps;
     for (int64_t pos = begin; pos < end;) {
@@ -357,7 +360,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_few_kernel(AttnArgs a, Spa
         int64_t kend64 = rows.first + last_row + 1;
         kend64 = kend64 > rows.len ? rows.len : kend64;
         const int kend = kend64 < 0 ? 0 : (int)kend64;
-        if (by_unit) step1 = (kend + kStride - 1) / kStride;
+        if (span.by_unit) step1 = (kend + kStride - 1) / kStride;
         const int kbeg = step0 * kStride < kend ? step0 * kStride : kend;
         const int kstop = (int64_t)step1 * kStride < kend ? step1 * kStride : kend;
         const int top = (kstop - 1) & ~15;  // the piece's last 16 keys
@@ -649,20 +652,20 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_few_kernel(AttnArgs a, Spa
 
 // ---- many rows: 128 query rows share each key tile through LDS ----
 //
-// Four waves of 32 rows. Each key tile's codes are loaded once by the block
-// (the next tile's while this one is used), turned into fp16 once and laid out
-// in LDS as the 32 x 32 x 16 matrix instruction reads them, so the conversion
-// costs a 128th of an operation per row and code. Two blocks a CU (64 KB of LDS
+// W waves of 32 rows. Each key tile's codes are loaded once by the block (ahead
+// of their use), turned into fp16 once and laid out in LDS as the 32 x 32 x 16
+// matrix instruction reads them, so the conversion costs a 32 W-th of an
+// operation per row and code. Two blocks a CU (64 KB of LDS
 // each): one's softmax runs beside the other's products.
-template <int D, int BITS>
+template <int D, int BITS, int W>
 struct Many {
-    static constexpr int ROWS = 128;
-    static constexpr int KT = D == 64 ? 64 : 32;   // keys of a tile
+    static constexpr int ROWS = 32 * W;
+    static constexpr int KT = D == 64 ? 16 * W : 8 * W;  // keys of a tile
     static constexpr int RING = 3;                 // tiles in LDS: in use, next, being written
     static constexpr int kRow = D * BITS / 8;
-    static constexpr int KB = kRow * KT / 256;     // key code bytes a thread
-    static constexpr int TPK = 256 / KT;           // threads a key
-    static constexpr int TP = 256 / (KT / 8);      // threads a pair of value quads
+    static constexpr int KB = kRow * KT / (64 * W);  // key code bytes a thread
+    static constexpr int TPK = 64 * W / KT;        // threads a key
+    static constexpr int TP = 64 * W / (KT / 8);   // threads a pair of value quads
     static constexpr int VW = kRow / TP;           // value words a thread and quad
     static constexpr int DW = VW * 8 / BITS;       // value elements a thread
     static constexpr int STEPS = D / 16;           // score MFMAs per 32 keys
@@ -675,12 +678,12 @@ struct Many {
     // little longer than its keys so that the threads of one key write to
     // different banks; values [16 keys][half][position][8 keys], position p
     // holding element (p % TP) DW + p / TP. Reads are runs of 16 bytes a lane.
-    static constexpr int KPAD = KT + (KT == 64 ? 2 : 1);
+    static constexpr int KPAD = KT + (D == 64 ? 2 : 1);
     struct Buf {
         f16x8 k[CHUNKS * KPAD], v[KT / 8 * D];
         float meta[4][KT];   // key scales, value scales, key zeros, value zeros
-        float stat[4][4];    // [1]: the largest value scale of each 16 keys
-        int bad[4];          // whether they lie outside the pool
+        float stat[4][KT / 16];  // [1]: the largest value scale of each 16 keys
+        int bad[KT / 16];        // whether they lie outside the pool
     };
     struct Load {
         uint32_t k[KB / 4], v0[VW], v1[VW];
@@ -701,9 +704,9 @@ LQ_DEVICE void load_any(uint32_t *dst, const uint8_t *p) {
     }
 }
 
-template <int D, int BITS, bool SYM>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_many_kernel(AttnArgs a, Span span, int by_unit) {
-    using C = Many<D, BITS>;
+template <int D, int BITS, bool SYM, int W>
+__global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(AttnArgs a, Span span) {
+    using C = Many<D, BITS, W>;
     __shared__ typename C::Buf lds[C::RING];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -716,7 +719,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_many_kernel(AttnAr
     const uint32_t magic = fp16_magic();
     // what this thread brings of a tile: all its keys are of one group of 16
     const int my_key = threadIdx.x / C::TPK, my_part = threadIdx.x % C::TPK;  // in the tile
-    const int my_group = C::KT == 64 ? wave : wave >> 1;
+    const int my_group = D == 64 ? wave : wave >> 1;
     const int my_pair = threadIdx.x / C::TP, my_t = threadIdx.x % C::TP;      // 16-key step and half, position
     const uint32_t k_off = (my_key & 15) * C::kRow + my_part * C::KB;
     const uint32_t v_off = (my_pair & 1) * 4 * C::kRow + my_t * C::VW * 4;    // its second quad is 2 quads on
@@ -727,7 +730,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_many_kernel(AttnAr
                                                          : a.c.v_zeros) + (lane & 15);
 
     // looked up anew for each piece: its registers are wanted inside
-    const auto schedule = [&]() { return Schedule<C::KT>(a.batch, shift, group, C::ROWS, lane, by_unit); };
+    const auto schedule = [&]() { return Schedule<C::KT>(a.batch, span, shift, group, C::ROWS, lane); };
     int64_t begin, end;
     {
         const int64_t all_steps = schedule().total(), share = uniform_div(all_steps + span.cap - 1, span.cap);
@@ -757,7 +760,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_many_kernel(AttnAr
         int64_t kend64 = rows.first + block_last + 1;
         kend64 = kend64 > rows.len ? rows.len : kend64;
         const int kend = kend64 < 0 ? 0 : (int)kend64;
-        if (by_unit) step1 = (kend + C::KT - 1) / C::KT;
+        if (span.by_unit) step1 = (kend + C::KT - 1) / C::KT;
         const int kbeg = step0 * C::KT < kend ? step0 * C::KT : kend;
         const int kstop = (int64_t)step1 * C::KT < kend ? step1 * C::KT : kend;
         const int its = (kstop - kbeg + C::KT - 1) / C::KT;
@@ -998,20 +1001,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_many_kernel(AttnAr
             typename C::Buf &to = lds[now + 2 < C::RING ? now + 2 : now + 2 - C::RING];
             f16x8 kr[C::STEPS];
             f32x4 sv[2], zv[2];
-            if constexpr (KBLK == 2) {
-                key_operands(b, 1, 0, kr);
-                value_meta(b, 0, 0, sv, zv);
-                settle(b, 0, key0, t);
-                weigh(b, 0, t, b, 1, kr, sv, zv, u, false, to);
-                key_operands(next, 0, 0, kr);
-                value_meta(b, 1, 0, sv, zv);
-                settle(b, 1, key0, u);
-                weigh(b, 1, u, next, 0, kr, sv, zv, t, true, to);
-            } else {
-                key_operands(next, 0, 0, kr);
-                value_meta(b, 0, 0, sv, zv);
-                settle(b, 0, key0, t);
-                weigh(b, 0, t, next, 0, kr, sv, zv, u, true, to);
+#pragma unroll
+            for (int kb = 0; kb < KBLK; ++kb) {
+                const bool last = kb == KBLK - 1;
+                f32x16 &cur = kb & 1 ? u : t, &then = kb & 1 ? t : u;
+                key_operands(last ? next : b, last ? 0 : kb + 1, 0, kr);
+                value_meta(b, kb, 0, sv, zv);
+                settle(b, kb, key0, cur);
+                weigh(b, kb, cur, last ? next : b, last ? 0 : kb + 1, kr, sv, zv, then, last, to);
             }
             if (it + 3 < its) load(x, it + 3);
             lds_barrier();
@@ -1094,7 +1091,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Span span) {
     const int h = blockIdx.x % a.c.heads;
     const int64_t border = blockIdx.x / a.c.heads + 1;
     const int group = a.q_heads / a.c.heads;
-    const Schedule<STEP> sched(a.batch, a.c.page_shift, group, ROWS, lane);
+    const Schedule<STEP> sched(a.batch, span, a.c.page_shift, group, ROWS, lane);
     const int64_t all_steps = sched.total(), share = uniform_div(all_steps + span.cap - 1, span.cap);
     if (border * share >= all_steps) return;
     const Piece p = sched.at(border * share);
@@ -1137,11 +1134,49 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Span span) {
     }
 }
 
-struct Plan {
+// One launch of a kernel (and of the join): the sequences it takes, its tile's
+// rows, blocks a key head and workspace.
+struct Pass {
     int row_tile, cap, by_unit;
+    uint32_t least, most;
+    int64_t bytes;
+};
+struct Plan {
+    Pass pass[2];
+    int passes;
     int64_t bytes;
 };
 constexpr int kFewWaves = 4, kFewStep = 32 * kFewWaves;
+
+Pass pass_of(int row_tile, int64_t rows, int64_t group, int64_t heads, int64_t head_dim, int64_t b, int64_t kv, int64_t n) {
+    Pass p{};
+    p.row_tile = row_tile;
+    p.least = 1;
+    p.most = 0xFFFFFFFFu;
+    const int64_t units = (rows * group + row_tile - 1) / row_tile + b;  // at most
+    const int64_t tiles = (n * group + row_tile - 1) / row_tile;         // of a sequence
+    const int64_t step = row_tile < 128 ? kFewStep : row_tile / (head_dim == 64 ? 2 : 4);
+    // what the kernels' registers allow on 256 CUs: all blocks run at once, and
+    // more spans only repeat the fixed part (INT4 decode of 16 sequences with
+    // 256, 512, 768, 1024 blocks: 37.6, 32.3, 39.2, 38.7 us)
+    int64_t cap = ((row_tile == 256 ? 256 : 512) + heads - 1) / heads;
+    // Blocks take whole units, and nothing is joined: chunks of many units, and
+    // decode batches of short contexts, which would spend longer on the second
+    // launch (a pass over spans and over units: 1 x 1003 tokens on one head 16.3
+    // and 12.1 us, 64 x 500 on 8 heads 20.9 and 13.7, 16 x 2000 on 8 heads 20.4
+    // and 17.7; 4 x 2000 on 8 heads 15.8 and 17.5).
+    const int64_t likely = b * tiles < units ? b * tiles : units;
+    p.by_unit = row_tile >= 128 ? units * heads >= (row_tile == 128 ? 2048 : 1024)
+                                : kv <= 1024 || (kv <= 2048 && likely * heads >= 128);
+    if (p.by_unit) cap = row_tile >= 128 ? units : likely;
+    // no more blocks than steps of work
+    const int64_t steps = units * ((kv + step - 1) / step < 1 ? 1 : (kv + step - 1) / step);
+    if (cap > steps) cap = steps;
+    if (cap * heads > (int64_t(1) << 30)) cap = (int64_t(1) << 30) / heads;
+    p.cap = (int)cap;
+    p.bytes = cap > 1 && !p.by_unit ? (2 * cap * heads * row_tile * (head_dim + 2) * 4 + 255) / 256 * 256 : 0;
+    return p;
+}
 
 Plan plan_of(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b, int64_t room, int64_t max_rows,
              int64_t max_kv) {
@@ -1149,28 +1184,25 @@ Plan plan_of(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int
     const int64_t n = max_rows <= 0 || max_rows > rows ? rows : max_rows;
     const int64_t kv = max_kv <= 0 || max_kv > room ? room : max_kv;
     const int64_t group = q_heads / heads;
-    p.row_tile = n * group <= 8 ? 8 : n * group <= 16 ? 16 : 128;
-    const int64_t units = (rows * group + p.row_tile - 1) / p.row_tile + b;  // at most
-    const int64_t tiles = (n * group + p.row_tile - 1) / p.row_tile;         // of a sequence
-    const int64_t step = p.row_tile < 128 ? kFewStep : head_dim == 64 ? 64 : 32;
-    // two blocks a CU, what their registers allow: all run at once, and more
-    // spans only repeat the fixed part (INT4 decode of 16 sequences with
-    // 256, 512, 768, 1024 blocks: 37.6, 32.3, 39.2, 38.7 us)
-    int64_t cap = (512 + heads - 1) / heads;
-    // Blocks take whole units, and nothing is joined: chunks of many units, and
-    // decode batches of short contexts, which would spend longer on the second
-    // launch (a pass over spans and over units: 1 x 1003 tokens on one head 16.3
-    // and 12.1 us, 64 x 500 on 8 heads 20.9 and 13.7, 16 x 2000 on 8 heads 20.4
-    // and 17.7; 4 x 2000 on 8 heads 15.8 and 17.5).
-    const int64_t likely = b * tiles < units ? b * tiles : units;
-    p.by_unit = p.row_tile == 128 ? units * heads >= 2048 : kv <= 1024 || (kv <= 2048 && likely * heads >= 128);
-    if (p.by_unit) cap = p.row_tile == 128 ? units : likely;
-    // no more blocks than steps of work
-    const int64_t steps = units * ((kv + step - 1) / step < 1 ? 1 : (kv + step - 1) / step);
-    if (cap > steps) cap = steps;
-    if (cap * heads > (int64_t(1) << 30)) cap = (int64_t(1) << 30) / heads;
-    p.cap = (int)cap;
-    p.bytes = cap > 1 && !p.by_unit ? 2 * cap * heads * p.row_tile * (head_dim + 2) * 4 : 0;
+    auto pass = [&](int row_tile) { return pass_of(row_tile, rows, group, heads, head_dim, b, kv, n); };
+    p.passes = 1;
+    if (n * group <= 16) {
+        p.pass[0] = pass(n * group <= 8 ? 8 : 16);
+    } else {
+        // Tiles of 256 rows where a sequence fills them on the average (a
+        // 2048-token chunk of the 70B heads in tiles of 128: 646 us, of 256:
+        // 567), of 128 otherwise. In a batch of single tokens beside few chunks
+        // (the others than the longest have few rows) the sequences of up to 16
+        // rows go to the kernel for few rows in a launch of their own.
+        p.pass[0] = pass(rows * group >= 256 * b && head_dim != 256 ? 256 : 128);
+        if (b >= 4 && (rows - n) * group <= 64 * (b - 1)) {
+            p.pass[0].least = 17;
+            p.pass[1] = pass(16);
+            p.pass[1].most = 16;
+            p.passes = 2;
+        }
+    }
+    p.bytes = p.pass[0].bytes + p.pass[1].bytes;
     return p;
 }
 
@@ -1182,16 +1214,15 @@ int64_t attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, 
 }
 
 template <int D, int BITS, bool SYM, int ROWS>
-static hipError_t launch_tiles(const AttnArgs &a, const Plan &p, hipStream_t st) {
-    Span span{static_cast<float *>(a.workspace), nullptr, p.cap};
+static hipError_t launch_tiles(const AttnArgs &a, const Pass &p, char *workspace, hipStream_t st) {
+    Span span{reinterpret_cast<float *>(workspace), nullptr, p.cap, p.by_unit, p.least, p.most};
     span.ml = span.o + (int64_t)2 * p.cap * a.c.heads * ROWS * D;
     const dim3 grid((uint32_t)(p.cap * a.c.heads));
-    constexpr int step = ROWS < 128 ? kFewStep : Many<D, BITS>::KT;
+    constexpr int step = ROWS < 128 ? kFewStep : Many<D, BITS, ROWS / 32>::KT;
     if constexpr (ROWS < 128)
-        hipLaunchKernelGGL((attn_few_kernel<D, BITS, SYM, ROWS, kFewWaves>), grid, dim3(64 * kFewWaves), 0, st, a, span,
-                           p.by_unit);
+        hipLaunchKernelGGL((attn_few_kernel<D, BITS, SYM, ROWS, kFewWaves>), grid, dim3(64 * kFewWaves), 0, st, a, span);
     else
-        hipLaunchKernelGGL((attn_many_kernel<D, BITS, SYM>), grid, dim3(256), 0, st, a, span, p.by_unit);
+        hipLaunchKernelGGL((attn_many_kernel<D, BITS, SYM, ROWS / 32>), grid, dim3(2 * ROWS), 0, st, a, span);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.cap == 1 || p.by_unit) return e;
     hipLaunchKernelGGL((attn_join_kernel<D, ROWS, step>), dim3((uint32_t)((p.cap - 1) * a.c.heads), ROWS < 128 ? 1 : 8),
@@ -1199,14 +1230,31 @@ static hipError_t launch_tiles(const AttnArgs &a, const Plan &p, hipStream_t st)
     return hipGetLastError();
 }
 
+template <int D, int BITS, bool SYM>
+static hipError_t launch_plan(const AttnArgs &a, const Plan &p, hipStream_t st) {
+    char *ws = static_cast<char *>(a.workspace);
+    for (int i = 0; i < p.passes; ++i) {
+        const Pass &q = p.pass[i];
+        hipError_t e;
+        if (q.row_tile == 8)
+            e = launch_tiles<D, BITS, SYM, 8>(a, q, ws, st);
+        else if (q.row_tile == 16)
+            e = launch_tiles<D, BITS, SYM, 16>(a, q, ws, st);
+        else if (D == 256 || q.row_tile == 128)
+            e = launch_tiles<D, BITS, SYM, 128>(a, q, ws, st);
+        else
+            e = launch_tiles<D, BITS, SYM, D == 256 ? 128 : 256>(a, q, ws, st);
+        if (e != hipSuccess) return e;
+        ws += q.bytes;
+    }
+    return hipSuccess;
+}
+
 hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st) {
     const Plan p = plan_of(a.batch.rows, a.q_heads, a.c.heads, a.c.head_dim, a.batch.b,
                            a.batch.max_pages << a.c.page_shift, a.max_rows, a.max_kv);
-#define LQ_ATTN(D, BITS, SYM)                                                                                   \
-    if (a.c.head_dim == D && a.c.bits == BITS && (a.c.symmetric != 0) == SYM)                                   \
-        return p.row_tile == 8    ? launch_tiles<D, BITS, SYM, 8>(a, p, st)                                     \
-               : p.row_tile == 16 ? launch_tiles<D, BITS, SYM, 16>(a, p, st)                                    \
-                                  : launch_tiles<D, BITS, SYM, 128>(a, p, st);
+#define LQ_ATTN(D, BITS, SYM) \
+    if (a.c.head_dim == D && a.c.bits == BITS && (a.c.symmetric != 0) == SYM) return launch_plan<D, BITS, SYM>(a, p, st);
 #define LQ_ATTN_D(D) LQ_ATTN(D, 4, false) LQ_ATTN(D, 4, true) LQ_ATTN(D, 8, false) LQ_ATTN(D, 8, true)
     LQ_ATTN_D(64) LQ_ATTN_D(128) LQ_ATTN_D(256)
 #undef LQ_ATTN_D

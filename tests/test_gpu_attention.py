@@ -45,7 +45,8 @@ def _run(seqs, d, bits, sym, page=16, heads=2, group=4, seed=0, q_scale=1.0, k_s
 @pytest.mark.parametrize("bits,sym", FORMATS)
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_formats(d, bits, sym):
-    _run(SEQS, d, bits, sym, seed=d + bits)
+    # bounds that choose each kernel: 256, 128, 16 and 8 rows a tile
+    _run(SEQS, d, bits, sym, seed=d + bits, hints=((0, 0), (20, 0), (4, 261), (2, 0)))
 
 
 @pytest.mark.parametrize("bits,sym", FORMATS)
@@ -84,6 +85,15 @@ def test_long_single_sequence(held, bits, sym):
 def test_long_chunk():
     _run([(1500, 130), (900, 64)], 128, 8, True, page=64, heads=1, group=2, seed=5)
     _run([(1500, 130), (900, 64)], 128, 4, False, page=16, heads=1, group=2, seed=6)
+
+
+@pytest.mark.parametrize("bits,sym", FORMATS)
+@pytest.mark.parametrize("group", [1, 4, 5])
+def test_single_tokens_beside_a_chunk(bits, sym, group):
+    """A batch whose single tokens go to a launch of their own, whole and split."""
+    seqs = [(150, 100)] + [(n, 1) for n in (1, 40, 257, 600, 33)] + [(9, 9), (3, 4)]
+    _run(seqs, 64, bits, sym, heads=2, group=group, seed=group, hints=((100, 600), (100, 5000)))
+    _run(seqs, 64, bits, sym, page=256, heads=1, group=group, seed=group, hints=((100, 0),))
 
 
 def test_rows_apart_and_leading_rows():
