@@ -229,8 +229,11 @@ struct Schedule {
 // ---- few rows: one wave per run of 32 keys, no sharing between waves ----
 //
 // A tile's rows are the heads of the group, token by token. Wave w of a block
-// walks a piece's 32-key tiles w, w + WAVES, ... with the next tile's codes and
-// scales in flight; the waves' results are joined in LDS.
+// walks a piece's 32-key tiles w, w + WAVES, ...; the next tile's keys are asked
+// for as soon as this one's have been multiplied, its values after the second
+// product, into the registers that just fell free. That leaves room for three
+// waves a SIMD: a wave alone issues an instruction every 5-12 cycles, so the
+// rate goes with the waves. The waves' results are joined in LDS.
 //
 // ROWS is 16, the width of the matrix instruction, or 8: then columns 0-7 and
 // 8-15 hold the same rows, the first half of the lanes takes the softmax of
@@ -240,9 +243,6 @@ struct Schedule {
 // heads) is bound by instructions, not bytes.
 template <int D, int BITS, bool SYM, int ROWS>
 struct Few {
-    // tiles in registers: the one in use and the next (a third or fourth changed
-    // nothing: 32.3-34.8 us for the INT4 decode of 16 sequences)
-    static constexpr int NB = 2;
     static constexpr int HALVES = 16 / ROWS;
     static constexpr int US = 2 / HALVES;            // 16-key groups whose softmax a lane takes
     static constexpr int kRow = D * BITS / 8;        // code bytes of a token
@@ -257,8 +257,9 @@ struct Few {
     struct Tile {
         uint32_t k[2][KW], v[2][KW];
         f32x4 sk[US], sv[US], zk[US], zv[US];
-        int key[2];  // first key of the 16, or kNoKey for a page outside the pool
     };
+    // waves a SIMD that the registers allow
+    static constexpr int OCC = D <= 128 && ROWS == 8 ? 3 : 2;
 };
 constexpr int kNoKey = 0x7FFFFF00;
 constexpr int64_t kMaxTokens = int64_t(1) << 30;  // of one sequence: keys are 32-bit
@@ -317,7 +318,7 @@ LQ_DEVICE float q_to_fp16(const u32x4 *raw, float scale, f16x8 *qf, float &qsum)
 }
 
 template <int D, int BITS, bool SYM, int ROWS, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, 2) void attn_few_kernel(AttnArgs a, Span span) {
+__global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void attn_few_kernel(AttnArgs a, Span span) {
     using C = Few<D, BITS, SYM, ROWS>;
     constexpr int LDO = D + 4;
     constexpr int kStride = 32 * WAVES;  // keys from one of a wave's tiles to its next
@@ -381,43 +382,54 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_few_kernel(AttnArgs a, Spa
         // the page numbers are waited for here, so that reading one later does
         // not wait for the loads of codes issued since
         auto settle_pages = [&]() { asm volatile("" : "+v"(pid0), "+v"(pid1)); };
-        auto load_tile = [&](typename C::Tile &x, int it) {
-            if ((it & 63) == 0 && it > 0) {
-                load_pages(it);
-                settle_pages();
-            }
+        // slots of a tile's two groups of 16 keys, and their first keys (kNoKey for
+        // a page outside the pool)
+        auto slots_of = [&](int it, int64_t *slots, int *keys) {
             const int key0 = kbeg + 32 * wave + kStride * it;
-            int64_t slots[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 int page = __builtin_amdgcn_readlane(u ? pid1 : pid0, it & 63);
                 const int key = key0 + 16 * u;
                 const bool in = (uint32_t)page < (uint32_t)pages;
-                x.key[u] = in ? key : kNoKey;
+                keys[u] = in ? key : kNoKey;
                 page = in ? page : 0;
                 const int kc = key < top ? key : top;
-                const int64_t slot = (((int64_t)page * a.c.heads + h) << shift) + (kc & ps_mask);
-                const uint8_t *kp = a.c.k_codes + slot * C::kRow, *vp = a.c.v_codes + slot * C::kRow;
+                slots[u] = (((int64_t)page * a.c.heads + h) << shift) + (kc & ps_mask);
+            }
+        };
+        auto load_keys = [&](typename C::Tile &x, const int64_t *slots) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const uint8_t *kp = a.c.k_codes + slots[u] * C::kRow;
 #pragma unroll
                 for (int j = 0; j < C::NV; ++j) load_words<C::VEC, true>(x.k[u] + j * C::VEC, kp + j * 64 + k_off);
-#pragma unroll
-                for (int j = 0; j < C::NV; ++j) load_words<C::VEC, true>(x.v[u] + j * C::VEC, vp + j * 256 + v_off);
-                slots[u] = slot;
             }
 #pragma unroll
             for (int u = 0; u < C::US; ++u) {
                 const int64_t at = (C::HALVES == 2 ? (half ? slots[1] : slots[0]) : slots[u]) + m_off;
                 x.sk[u] = *reinterpret_cast<const f32x4 *>(a.c.k_scales + at);
+                if (!SYM) x.zk[u] = *reinterpret_cast<const f32x4 *>(a.c.k_zeros + at);
+            }
+        };
+        auto load_values = [&](typename C::Tile &x, const int64_t *slots) {
+#pragma unroll
+            for (int u = 0; u < C::US; ++u) {
+                const int64_t at = (C::HALVES == 2 ? (half ? slots[1] : slots[0]) : slots[u]) + m_off;
                 x.sv[u] = *reinterpret_cast<const f32x4 *>(a.c.v_scales + at);
-                if (!SYM) {
-                    x.zk[u] = *reinterpret_cast<const f32x4 *>(a.c.k_zeros + at);
-                    x.zv[u] = *reinterpret_cast<const f32x4 *>(a.c.v_zeros + at);
-                }
+                if (!SYM) x.zv[u] = *reinterpret_cast<const f32x4 *>(a.c.v_zeros + at);
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const uint8_t *vp = a.c.v_codes + slots[u] * C::kRow;
+#pragma unroll
+                for (int j = 0; j < C::NV; ++j) load_words<C::VEC, true>(x.v[u] + j * C::VEC, vp + j * 256 + v_off);
             }
         };
         const int first_key = kbeg + 32 * wave;
         const int its = kstop > first_key ? (kstop - first_key + kStride - 1) / kStride : 0;
-        typename C::Tile buf[C::NB];
+        typename C::Tile x;
+        int64_t slots[2] = {0, 0};
+        int keys[2] = {0, 0};
         if (its > 0) load_pages(0);
 
         f16x8 qf[C::STEPS];
@@ -432,9 +444,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_few_kernel(AttnArgs a, Spa
                 raw[s] = live ? *reinterpret_cast<const u32x4 *>(qp + d0) : u32x4{0u, 0u, 0u, 0u};
             }
             settle_pages();
-            #pragma unroll
-            for (int i = 0; i < C::NB - 1; ++i)
-                if (i < its) load_tile(buf[i], i);  // in flight while q is made ready
+                        if (its > 0) {  // in flight while q is made ready
+                slots_of(0, slots, keys);
+                load_keys(x, slots);
+                load_values(x, slots);
+            }
             c1 = q_to_fp16<C::STEPS, BITS, SYM>(raw, a.scale, qf, qsum);
             if (!SYM) qsum = add_halves16(add_halves32(qsum));
         }
@@ -447,7 +461,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_few_kernel(AttnArgs a, Spa
         // sums these), and times the value scale as the product's operand.
         float m = -1e30f, l = 0.0f, vz = 0.0f, sref = 0.0f, mm = -1e30f;
 
-        auto use_tile = [&](typename C::Tile &x) {
+        for (int it = 0; it < its; ++it) {
             f32x4 t[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -468,12 +482,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_few_kernel(AttnArgs a, Spa
             }
             int key_of[C::US];
             if constexpr (C::HALVES == 2) {
-                key_of[0] = (half ? x.key[1] : x.key[0]) + 4 * g;
+                key_of[0] = (half ? keys[1] : keys[0]) + 4 * g;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) t[0][i] = half ? t[1][i] : t[0][i];
             } else {
-                key_of[0] = x.key[0] + 4 * g;
-                key_of[C::US - 1] = x.key[1] + 4 * g;
+                key_of[0] = keys[0] + 4 * g;
+                key_of[C::US - 1] = keys[1] + 4 * g;
             }
             float tm = -__builtin_inff();
             int smi = 0;  // positive floats order as their bits do
@@ -485,7 +499,17 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_few_kernel(AttnArgs a, Spa
                     t[u][i] *= x.sk[u][i];
                 }
             }
-            if (x.key[0] + 15 > safe || x.key[1] + 15 > safe || x.key[1] + 15 >= kstop) {
+            const bool masked = keys[0] + 15 > safe || keys[1] + 15 > safe || keys[1] + 15 >= kstop;
+            const bool more = it + 1 < its;
+            if (more) {
+                if (((it + 1) & 63) == 0) {
+                    load_pages(it + 1);
+                    settle_pages();
+                }
+                slots_of(it + 1, slots, keys);
+                load_keys(x, slots);
+            }
+            if (masked) {
                 // keys some row does not see, or nobody: they may hold anything
 #pragma unroll
                 for (int u = 0; u < C::US; ++u)
@@ -568,16 +592,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_few_kernel(AttnArgs a, Spa
                     o[2 * w + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(join(vf), pf, o[2 * w + 1], 0, 0, 0);
                 }
             }
-        };
-
-        for (int it = 0; it < its; it += C::NB) {
-#pragma unroll
-            for (int i = 0; i < C::NB; ++i) {
-                if (it + i < its) {
-                    if (it + i + C::NB - 1 < its) load_tile(buf[(i + C::NB - 1) % C::NB], it + i + C::NB - 1);
-                    use_tile(buf[i]);
-                }
-            }
+            if (more) load_values(x, slots);
         }
         l = add_halves16(add_halves32(l));
         if (!SYM) vz = add_halves16(add_halves32(vz));
@@ -936,12 +951,13 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
         };
         // The weights of t (block kb of tile b), their product with the values,
         // the next block's scores u = keys kr . q, and (STORE) the tile x on its
-        // way to LDS. The order is written out, so that no matrix instruction
-        // stands alone: JT groups of the first 16 keys' weights, each beside a
-        // score instruction; JT groups of the others', each beside a score and a
-        // value instruction; then the other value instructions beside the
-        // conversion of x. Without it each wave did one kind of work after the
-        // other and the two waves of a SIMD rarely met in different kinds.
+        // way to LDS, in one run of instructions without a branch, with the
+        // independent work side by side: JT groups of the first 16 keys' weights,
+        // each beside a score instruction; JT groups of the others', each beside a
+        // score and a value instruction; then the other value instructions
+        // beside the conversion of x. (Holding the compiler to this order with
+        // scheduling barriers, or raising the wave's priority over it, changed
+        // nothing beyond noise: 541-569 us for the 2048-token chunk.)
         auto weigh = [&](const typename C::Buf &b, int kb, const f32x16 &t, const typename C::Buf &bn, int kn, f16x8 *kr,
                          f32x4 *sv, f32x4 *zv, f32x16 &u, bool with_store, typename C::Buf &to) {
             constexpr int EG = 8 / C::JT;  // weights of a group
@@ -964,7 +980,6 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
                         l += p;
                         pv[i] = p * sv[i / 4][i % 4];
                     }
-                    __builtin_amdgcn_sched_barrier(0);
                     if (s == 1) vr[g] = b.v[(kb * 4 + 2 + half) * D + 32 * g + n];
                 }
                 f16x2 pb[4];
@@ -989,7 +1004,6 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
 #pragma unroll
                     for (int i = g * kParts / C::JT; i < (g + 1) * kParts / C::JT; ++i) store_part(x, to, i);
                 }
-                __builtin_amdgcn_sched_barrier(0);
             }
         };
 
@@ -1160,22 +1174,27 @@ Pass pass_of(int row_tile, int64_t rows, int64_t group, int64_t heads, int64_t h
     const int64_t units = (rows * group + row_tile - 1) / row_tile + b;  // at most
     const int64_t tiles = (n * group + row_tile - 1) / row_tile;         // of a sequence
     const int64_t step = row_tile < 128 ? kFewStep : row_tile / (head_dim == 64 ? 2 : 4);
-    // what the kernels' registers allow on 256 CUs: all blocks run at once, and
-    // more spans only repeat the fixed part (INT4 decode of 16 sequences with
-    // 256, 512, 768, 1024 blocks: 37.6, 32.3, 39.2, 38.7 us)
-    int64_t cap = ((row_tile == 256 ? 256 : 512) + heads - 1) / heads;
+    // What the kernels' registers allow on 256 CUs: all blocks run at once, and
+    // more spans only repeat the fixed part. Single tokens' kernel (row_tile 8)
+    // has room for three blocks a CU, which pays while spans are short and costs
+    // a few per cent of HBM's rate when they are long (512, 768, 1024 blocks:
+    // INT4 decode of 16 sequences up to 8192 tokens 30.6, 28.0, 33.5 us; INT8 of
+    // 64 up to 16384 215.7, 224.5, 228.8).
+    const int64_t unit_steps = (kv + step - 1) / step < 1 ? 1 : (kv + step - 1) / step;
+    const int64_t likely = b * tiles < units ? b * tiles : units;
+    const bool short_spans = likely * unit_steps * heads <= 32 * 512;
+    const int64_t blocks = row_tile == 256 ? 256 : row_tile == 8 && head_dim <= 128 && short_spans ? 768 : 512;
+    int64_t cap = (blocks + heads - 1) / heads;
     // Blocks take whole units, and nothing is joined: chunks of many units, and
     // decode batches of short contexts, which would spend longer on the second
     // launch (a pass over spans and over units: 1 x 1003 tokens on one head 16.3
     // and 12.1 us, 64 x 500 on 8 heads 20.9 and 13.7, 16 x 2000 on 8 heads 20.4
     // and 17.7; 4 x 2000 on 8 heads 15.8 and 17.5).
-    const int64_t likely = b * tiles < units ? b * tiles : units;
     p.by_unit = row_tile >= 128 ? units * heads >= (row_tile == 128 ? 2048 : 1024)
                                 : kv <= 1024 || (kv <= 2048 && likely * heads >= 128);
     if (p.by_unit) cap = row_tile >= 128 ? units : likely;
     // no more blocks than steps of work
-    const int64_t steps = units * ((kv + step - 1) / step < 1 ? 1 : (kv + step - 1) / step);
-    if (cap > steps) cap = steps;
+    if (cap > units * unit_steps) cap = units * unit_steps;
     if (cap * heads > (int64_t(1) << 30)) cap = (int64_t(1) << 30) / heads;
     p.cap = (int)cap;
     p.bytes = cap > 1 && !p.by_unit ? (2 * cap * heads * row_tile * (head_dim + 2) * 4 + 255) / 256 * 256 : 0;
