@@ -449,6 +449,8 @@ def gptq_quantize_noalloc(w: torch.Tensor, u: torch.Tensor, bits: int = 4, symme
 
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}  # lq_dtype
 _BF16, _F32, _I32, _I8, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int8, torch.uint8
+_Tensor, _empty = torch.Tensor, torch.empty_strided  # empty_strided: the cheapest of torch's allocating calls
+_device_now, _stream_now = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _dtype(t: torch.Tensor, name: str) -> int:
@@ -462,11 +464,11 @@ def _launch(name: str, index: int, *args) -> None:
     """The call on the current stream of the tensors' own device. (A decode
     step's kernels run for microseconds: this path keeps to a few lookups.)"""
     lib = _lib or load_library()
-    if index == torch._C._cuda_getDevice():
-        st = getattr(lib, name)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if index == _device_now():
+        st = getattr(lib, name)(*args, _stream_now(index))
     else:
         with torch.cuda.device(index):
-            st = getattr(lib, name)(*args, torch._C._cuda_getCurrentRawStream(index))
+            st = getattr(lib, name)(*args, _stream_now(index))
     if st != LQ_OK:
         detail = lib.lq_last_error().decode() or lib.lq_status_string(st).decode()
         raise LibquantError(st, name, detail)
@@ -474,7 +476,7 @@ def _launch(name: str, index: int, *args) -> None:
 
 def _on(index: int, t: torch.Tensor, name: str, dtype, shape) -> None:
     """_need, on the device of the call's first tensor."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous()
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous()
             and (shape is None or t.shape == shape)):
         return
     _need(t, name, dtype, shape)
@@ -512,11 +514,11 @@ def rms_norm_int8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, resi
     elif residual_out is not None:
         raise ValueError("residual_out needs residual")
     if qx is None:
-        qx = torch.empty(shape, dtype=_I8, device=dev)
+        qx = torch.empty_like(x, dtype=_I8)
     else:
         _on(index, qx, "qx", _I8, shape)
     if sx is None:
-        sx = torch.empty((t,), dtype=_F32, device=dev)
+        sx = _empty((t,), (1,), dtype=_F32, device=dev)
     else:
         _on(index, sx, "sx", _F32, (t,))
     _launch("rms_norm_int8", index, x.data_ptr(), xt, res_ptr, rt, weight.data_ptr(), wt, t, k, eps, out_ptr,
@@ -629,13 +631,14 @@ def kv_cache_read(cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tens
     """The values (q - z) s of the rows' keys and values, [rows][heads][head_dim]
     of dtype (bf16 or fp32) -> (k, v). Rows that belong to no sequence are left
     as they were in k and v."""
-    shape, index = (rows, cache.heads, cache.head_dim), cache._index
+    heads, d, index = cache.heads, cache.head_dim, cache._index
+    shape, steps = (rows, heads, d), (heads * d, d, 1)
     if k is None:
-        k = torch.empty(shape, dtype=dtype, device=cache.device)
+        k = _empty(shape, steps, dtype=dtype, device=cache.device)
     else:
         _on(index, k, "k", dtype, shape)
     if v is None:
-        v = torch.empty(shape, dtype=dtype, device=cache.device)
+        v = _empty(shape, steps, dtype=dtype, device=cache.device)
     else:
         _on(index, v, "v", dtype, shape)
     _launch("kv_cache_read", index, cache._ref, k.data_ptr(), v.data_ptr(), _dtype(k, "k"), rows,
@@ -660,7 +663,7 @@ def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     index = cache._index
     table, max_pages, lens, starts, b = _batch(index, block_table, kv_lens, row_starts)
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=cache.device)
+        out = _empty(shape, (q_heads * d, d, 1), dtype=_BF16, device=cache.device)
     else:
         _on(index, out, "out", _BF16, shape)
     if lse is not None:
@@ -670,7 +673,7 @@ def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
         ws_bytes = (_lib or load_library()).paged_attention_workspace_bytes(rows, q_heads, cache.heads, d, b, max_pages,
                                                                             cache.page_size, max_rows, max_kv)
         if ws_bytes > 0:
-            workspace = torch.empty((ws_bytes,), dtype=_U8, device=cache.device)
+            workspace = _empty((ws_bytes,), (1,), dtype=_U8, device=cache.device)
             ws_ptr = workspace.data_ptr()
     else:
         _on(index, workspace, "workspace", _U8, None)
