@@ -129,33 +129,6 @@ struct Piece {
     KvRows rows;
 };
 
-// One lane's value, and quotients, as wave-uniform numbers.
-LQ_DEVICE int64_t readlane64(int64_t v, int src) {
-    const int lo = __builtin_amdgcn_readlane((int)v, src), hi = __builtin_amdgcn_readlane((int)(v >> 32), src);
-    return ((int64_t)hi << 32) | (uint32_t)lo;
-}
-LQ_DEVICE int64_t uniform_div(int64_t a, int64_t b) {  // a >= 0, b > 0
-    if ((a | b) >> 32) return a / b;
-    return (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)a / (uint32_t)b);
-}
-
-template <int CTRL, int ROWMASK>
-LQ_DEVICE int64_t dpp_add64(int64_t v) {  // v plus the lane's source, or plus 0 where it has none
-    const int lo = __builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWMASK, 0xF, false);
-    const int hi = __builtin_amdgcn_update_dpp(0, (int)(v >> 32), CTRL, ROWMASK, 0xF, false);
-    return v + (((int64_t)hi << 32) | (uint32_t)lo);
-}
-// Inclusive sum over the wave's lanes: shifts by 1, 2, 4, 8 within rows of 16,
-// then each row's last lane to the next row and lane 31 to the upper half.
-LQ_DEVICE int64_t scan64(int64_t v) {
-    v = dpp_add64<0x111, 0xF>(v);
-    v = dpp_add64<0x112, 0xF>(v);
-    v = dpp_add64<0x114, 0xF>(v);
-    v = dpp_add64<0x118, 0xF>(v);
-    v = dpp_add64<0x142, 0xA>(v);
-    return dpp_add64<0x143, 0xC>(v);
-}
-
 // One wave's view of all units: a lane a sequence, 64 at a time; the first 64
 // are kept.
 template <int STEP>
@@ -1195,7 +1168,7 @@ Pass pass_of(int row_tile, int64_t rows, int64_t group, int64_t heads, int64_t h
     if (p.by_unit) cap = row_tile >= 128 ? units : likely;
     // no more blocks than steps of work
     if (cap > units * unit_steps) cap = units * unit_steps;
-    if (cap * heads > (int64_t(1) << 30)) cap = (int64_t(1) << 30) / heads;
+    if (cap * heads > (1 << 22)) cap = (1 << 22) / heads;  // blocks that walk on, within the launch limits
     p.cap = (int)cap;
     p.bytes = cap > 1 && !p.by_unit ? (2 * cap * heads * row_tile * (head_dim + 2) * 4 + 255) / 256 * 256 : 0;
     return p;

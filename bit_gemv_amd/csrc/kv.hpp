@@ -25,6 +25,7 @@ struct KvWriteArgs {
     const void *k, *v;
     int f32;
     int64_t k_stride, v_stride, max_rows;
+    int flat = 0;  // set by the launcher: see kv_grid
 };
 
 struct KvReadArgs {
@@ -33,6 +34,7 @@ struct KvReadArgs {
     void *k, *v;
     int f32;
     int64_t max_rows;
+    int flat = 0;
 };
 
 struct AttnArgs {
@@ -78,6 +80,33 @@ __device__ __forceinline__ int64_t kv_page(const KvBatch &bt, int64_t seq, int64
     if (pos < 0 || i >= bt.max_pages) return -1;
     const int64_t p = bt.table[seq * bt.max_pages + i];
     return p < 0 || p >= pages ? -1 : p;
+}
+
+// One lane's value, and quotients, as wave-uniform numbers.
+__device__ __forceinline__ int64_t readlane64(int64_t v, int src) {
+    const int lo = __builtin_amdgcn_readlane((int)v, src), hi = __builtin_amdgcn_readlane((int)(v >> 32), src);
+    return ((int64_t)hi << 32) | (uint32_t)lo;
+}
+__device__ __forceinline__ int64_t uniform_div(int64_t a, int64_t b) {  // a >= 0, b > 0
+    if ((a | b) >> 32) return a / b;
+    return (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)a / (uint32_t)b);
+}
+
+template <int CTRL, int ROWMASK>
+__device__ __forceinline__ int64_t dpp_add64(int64_t v) {  // v plus the lane's source, or plus 0 where it has none
+    const int lo = __builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWMASK, 0xF, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, (int)(v >> 32), CTRL, ROWMASK, 0xF, false);
+    return v + (((int64_t)hi << 32) | (uint32_t)lo);
+}
+// Inclusive sum over the wave's lanes: shifts by 1, 2, 4, 8 within rows of 16,
+// then each row's last lane to the next row and lane 31 to the upper half.
+__device__ __forceinline__ int64_t scan64(int64_t v) {
+    v = dpp_add64<0x111, 0xF>(v);
+    v = dpp_add64<0x112, 0xF>(v);
+    v = dpp_add64<0x114, 0xF>(v);
+    v = dpp_add64<0x118, 0xF>(v);
+    v = dpp_add64<0x142, 0xA>(v);
+    return dpp_add64<0x143, 0xC>(v);
 }
 
 }  // namespace lq

@@ -123,6 +123,46 @@ LQ_DEVICE uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
                                  0x05040100u);
 }
 
+// A sequence's items: aligned quads of its rows' positions (READ: those below
+// zero as well), for each two sides of every head.
+struct Items {
+    int64_t quad0, count;
+};
+template <bool READ>
+LQ_DEVICE Items items_of(const KvRows &rows, int heads) {
+    if (rows.n == 0 || (!READ && rows.first + rows.n <= 0)) return {0, 0};
+    const int64_t quad0 = (!READ && rows.first < 0 ? 0 : rows.first) >> 2;
+    return {quad0, (((rows.first + rows.n - 1) >> 2) - quad0 + 1) * 2 * heads};
+}
+
+// Where a team starts and how it goes on. In the plain grid blocks in x are a
+// sequence's items and blocks in y the sequences. In the flat one block
+// blockIdx.x is that block of all sequences' blocks of items, one after
+// another: each wave adds the sequences up, 64 at a time.
+struct Walk {
+    int64_t seq, seq_step, item, item_step;
+};
+template <bool READ>
+LQ_DEVICE Walk walk_of(const KvBatch &bt, int shift, int heads, int flat, int teams, int team) {
+    if (!flat) return {blockIdx.y, gridDim.y, (int64_t)blockIdx.x * teams + team, (int64_t)gridDim.x * teams};
+    const int lane = threadIdx.x & 63;
+    int64_t before = 0;
+    for (int64_t s0 = 0; s0 < bt.b; s0 += 64) {
+        int64_t mine = 0;
+        if (s0 + lane < bt.b)
+            mine = (items_of<READ>(kv_rows(bt, s0 + lane, shift), heads).count + teams - 1) / (uint32_t)teams;
+        const int64_t upto = before + scan64(mine);
+        const uint64_t past = __ballot(upto > (int64_t)blockIdx.x);
+        if (past) {
+            const int src = __ffsll((unsigned long long)past) - 1;
+            const int64_t first = readlane64(upto - mine, src);
+            return {s0 + src, (int64_t)1 << 60, (blockIdx.x - first) * teams + team, (int64_t)1 << 60};
+        }
+        before = readlane64(upto, 63);
+    }
+    return {bt.b, 1, 0, 1};
+}
+
 // which sequence, quad of positions, head and side (key or value) a team has
 struct Item {
     int64_t quad;
@@ -150,12 +190,12 @@ __global__ __launch_bounds__(kTpb) void kv_write_kernel(KvWriteArgs a) {
     constexpr int kRow = D * BITS / 8;       // bytes of a token's codes
     constexpr int kLane = BITS;              // of them, this lane's 8 elements
     const int lane = threadIdx.x % W, team = threadIdx.x / W;
-    for (int64_t seq = blockIdx.y; seq < a.batch.b; seq += gridDim.y) {
+    const Walk w0 = walk_of<false>(a.batch, a.c.page_shift, a.c.heads, a.flat, kTpb / W, team);
+    for (int64_t seq = w0.seq; seq < a.batch.b; seq += w0.seq_step) {
         const KvRows rows = kv_rows(a.batch, seq, a.c.page_shift);
-        if (rows.n == 0 || rows.first + rows.n <= 0) continue;
-        const int64_t quad0 = (rows.first < 0 ? 0 : rows.first) >> 2;
-        const int64_t items = (((rows.first + rows.n - 1) >> 2) - quad0 + 1) * 2 * a.c.heads;
-        for (int64_t i = (int64_t)blockIdx.x * (kTpb / W) + team; i < items; i += (int64_t)gridDim.x * (kTpb / W)) {
+        const Items mine = items_of<false>(rows, a.c.heads);
+        const int64_t quad0 = mine.quad0;
+        for (int64_t i = w0.item; i < mine.count; i += w0.item_step) {
             const Item it = item_of<D>(i, a.c.heads, quad0);
             const int64_t page = kv_page(a.batch, seq, it.quad * 4, a.c.page_shift, a.c.pages);
             if (page < 0) continue;
@@ -237,12 +277,12 @@ __global__ __launch_bounds__(kTpb) void kv_read_kernel(KvReadArgs a) {
     constexpr int kRow = D * BITS / 8;
     constexpr int kLane = BITS;
     const int lane = threadIdx.x % W, team = threadIdx.x / W;
-    for (int64_t seq = blockIdx.y; seq < a.batch.b; seq += gridDim.y) {
+    const Walk w0 = walk_of<true>(a.batch, a.c.page_shift, a.c.heads, a.flat, kTpb / W, team);
+    for (int64_t seq = w0.seq; seq < a.batch.b; seq += w0.seq_step) {
         const KvRows rows = kv_rows(a.batch, seq, a.c.page_shift);
-        if (rows.n == 0) continue;
-        const int64_t quad0 = rows.first >> 2;  // floor: positions below zero are rows too
-        const int64_t items = (((rows.first + rows.n - 1) >> 2) - quad0 + 1) * 2 * a.c.heads;
-        for (int64_t i = (int64_t)blockIdx.x * (kTpb / W) + team; i < items; i += (int64_t)gridDim.x * (kTpb / W)) {
+        const Items mine = items_of<true>(rows, a.c.heads);
+        const int64_t quad0 = mine.quad0;
+        for (int64_t i = w0.item; i < mine.count; i += w0.item_step) {
             const Item it = item_of<D>(i, a.c.heads, quad0);
             void *dst = it.side ? a.v : a.k;
             if (!dst) continue;
@@ -318,17 +358,24 @@ __global__ __launch_bounds__(kTpb) void kv_read_kernel(KvReadArgs a) {
     }
 }
 
-// Blocks in x cover max_rows rows of a sequence (one more quad where they are
-// not aligned), blocks in y the sequences; both kernels stride over what a
-// smaller grid leaves.
-dim3 kv_grid(const KvCache &c, const KvBatch &bt, int64_t max_rows) {
-    int64_t n = max_rows <= 0 || max_rows > bt.rows ? bt.rows : max_rows;
-    const int64_t items = ((n + 2) / 4 + 1) * 2 * c.heads;
+// The plain grid covers max_rows rows of every sequence. Where that is many
+// times the rows there are (one long chunk among single tokens, or no bound
+// given), the flat grid covers the rows. Measured (8 heads of 128, INT8, write):
+// 256 single tokens beside a chunk of 8192, plain 293 us, flat 22; 4 beside one
+// of 2048 (5 times the rows), plain 6.8, flat 6.1; eight chunks of 1024, plain
+// 12.0, flat 13.0; 64 single tokens, plain 4.4, flat 4.9. The plain grid walks on
+// past its limits.
+dim3 kv_grid(const KvCache &c, const KvBatch &bt, int64_t max_rows, int *flat) {
+    const int64_t n = max_rows <= 0 || max_rows > bt.rows ? bt.rows : max_rows;
     const int64_t teams = kTpb / (c.head_dim / 8);
-    int64_t x = (items + teams - 1) / teams;
-    const int64_t y = bt.b < 32768 ? bt.b : 32768;
+    auto blocks = [&](int64_t quads) { return (quads * 2 * c.heads + teams - 1) / teams; };
+    int64_t x = blocks((n + 2) / 4 + 1);
+    // at most: a quad more at each end of a sequence's rows, a block not full
+    const int64_t all = blocks(bt.rows / 4 + 2 * bt.b) + bt.b;
+    *flat = x * bt.b > 4 * all && all <= (1 << 23);
+    if (*flat) return dim3((uint32_t)all);
     if (x > 65536) x = 65536;
-    return dim3((uint32_t)x, (uint32_t)y);
+    return dim3((uint32_t)x, (uint32_t)(bt.b < 32768 ? bt.b : 32768));
 }
 
 }  // namespace
@@ -340,8 +387,9 @@ dim3 kv_grid(const KvCache &c, const KvBatch &bt, int64_t max_rows) {
     LQ_KV_TYPES(D, 4, false) LQ_KV_TYPES(D, 4, true) LQ_KV_TYPES(D, 8, false) LQ_KV_TYPES(D, 8, true)
 #define LQ_KV_ALL LQ_KV_FORMATS(64) LQ_KV_FORMATS(128) LQ_KV_FORMATS(256)
 
-hipError_t launch_kv_write(const KvWriteArgs &a, hipStream_t st) {
-    const dim3 grid = kv_grid(a.c, a.batch, a.max_rows);
+hipError_t launch_kv_write(const KvWriteArgs &args, hipStream_t st) {
+    KvWriteArgs a = args;
+    const dim3 grid = kv_grid(a.c, a.batch, a.max_rows, &a.flat);
 #define LQ_KV_DO(D, BITS, SYM, F32)                                                                        \
     {                                                                                                      \
         hipLaunchKernelGGL((kv_write_kernel<D, BITS, SYM, F32>), grid, dim3(kTpb), 0, st, a);               \
@@ -352,8 +400,9 @@ hipError_t launch_kv_write(const KvWriteArgs &a, hipStream_t st) {
     return hipErrorInvalidValue;
 }
 
-hipError_t launch_kv_read(const KvReadArgs &a, hipStream_t st) {
-    const dim3 grid = kv_grid(a.c, a.batch, a.max_rows);
+hipError_t launch_kv_read(const KvReadArgs &args, hipStream_t st) {
+    KvReadArgs a = args;
+    const dim3 grid = kv_grid(a.c, a.batch, a.max_rows, &a.flat);
 #define LQ_KV_DO(D, BITS, SYM, F32)                                                                        \
     {                                                                                                      \
         hipLaunchKernelGGL((kv_read_kernel<D, BITS, SYM, F32>), grid, dim3(kTpb), 0, st, a);                \

@@ -208,6 +208,7 @@ __global__ __launch_bounds__(TPB) void rms_norm_int8_kernel(const void *x, const
     if (t == 0) sx[blockIdx.x] = s;
 }
 
+// a.t at most 2^21: a launch's lanes in one dimension stay below 2^32
 template <int TPB, int NL, bool ONE>
 hipError_t launch_shape(const NormArgs &a, hipStream_t st) {
     const int res = !a.residual ? kNoRes : a.residual_f32 ? kResF32 : kResBf16;
@@ -225,10 +226,24 @@ hipError_t launch_shape(const NormArgs &a, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_rms_norm_int8(const NormArgs &a, hipStream_t st) {
-    if (a.k <= 8192) return launch_shape<256, 4, true>(a, st);
-    if (a.k <= 32768) return launch_shape<1024, 4, true>(a, st);
-    return launch_shape<1024, 4, false>(a, st);
+hipError_t launch_rms_norm_int8(const NormArgs &args, hipStream_t st) {
+    constexpr int64_t kSlice = int64_t(1) << 21;
+    auto at = [](const void *p, int64_t bytes) { return p ? static_cast<const char *>(p) + bytes : nullptr; };
+    for (int64_t row = 0; row < args.t; row += kSlice) {
+        NormArgs a = args;
+        const int64_t e = row * a.k;
+        a.t = args.t - row < kSlice ? args.t - row : kSlice;
+        a.x = at(args.x, e * (a.x_f32 ? 4 : 2));
+        a.residual = at(args.residual, e * (a.residual_f32 ? 4 : 2));
+        a.residual_out = const_cast<char *>(at(args.residual_out, e * (a.residual_f32 ? 4 : 2)));
+        a.qx = args.qx + e;
+        a.sx = args.sx + row;
+        const hipError_t err = a.k <= 8192    ? launch_shape<256, 4, true>(a, st)
+                               : a.k <= 32768 ? launch_shape<1024, 4, true>(a, st)
+                                              : launch_shape<1024, 4, false>(a, st);
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
 }
 
 }  // namespace lq

@@ -501,7 +501,7 @@ lq_status kv_cache_read(const lq_kv_cache *cache, void *k, void *v, lq_dtype typ
  * out bf16 [rows][q_heads][head_dim]; lse nullable fp32 [rows][q_heads]:
  * log sum_j exp(scale q . k_hat). q and out 16-byte aligned.
  * Products run on fp16 MFMA with exact integer codes, q scaled by a power of
- * two (exact down to 2^-24 of the largest element of 16 rows) and weights p
+ * two (exact down to 2^-28 of the largest element of up to 32 rows) and weights p
  * rounded to fp16; scales, sums and softmax
  * statistics are fp32. |q| up to 1e30, |scale q . k_hat| below 1e30; at most
  * 2^30 tokens in a sequence.

@@ -183,6 +183,27 @@ def test_odd_lengths_and_starts_touch_nothing_outside():
     torch.cuda.synchronize()
 
 
+def test_shared_prefix_pages():
+    """Two sequences over the same first pages, the second with more."""
+    rng = np.random.default_rng(17)
+    b = Batch([(32, 1), (50, 1)], 16, rng)
+    ref = new_cache(b, 16, 1, 64, 8, True)
+    fill(ref, b, rng)
+    b.lists[0] = b.lists[1][:2]
+    b.table[0, :2] = b.lists[0]
+    q = bf16(rng.standard_normal((2, 4, 64)))
+    want, wl, bound = serving.attention(q, ref, b.lists, b.kv, b.starts, 0.125)
+    say("paged_attention shared prefix")
+    check_attention(bg.paged_attention(dev_bf16f(q), to_gpu(ref), *b.on_gpu()), None, want, wl, bound, "shared prefix")
+
+
+@pytest.mark.parametrize("single", [True, False])
+def test_many_sequences(single):
+    """Past 64 sequences the sharing-out adds them up in several rounds."""
+    seqs = [(1 + (i * 37) % 90, 1 if single else 1 + (i % 3) * 7) for i in range(150)]
+    _run(seqs, 64, 4, True, heads=1, group=2, seed=18, hints=((0, 0), (15, 90), (15, 4000), (1, 4000)))
+
+
 def test_empty_calls():
     gpu = bg.KVCache.empty(2, 16, 1, 64)
     z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731

@@ -76,6 +76,14 @@ def test_hint_changes_nothing(max_rows):
     _run(128, 4, False, 16, 2, SEQS, "bf16", 11, max_rows=max_rows)
 
 
+@pytest.mark.parametrize("max_rows", [0, 90])
+def test_one_chunk_among_many_single_tokens(max_rows):
+    """Enough sequences for the flat grid, past 64 of them."""
+    seqs = [(5 + i, 1) for i in range(70)] + [(100, 90), (3, 5), (0, 1), (30, 0), (33, 1)] + [(7, 2)] * 60
+    _run(64, 8, True, 16, 1, seqs, "bf16", 17, max_rows=max_rows)
+    _run(64, 4, False, 32, 3, seqs, "fp32", 18, max_rows=max_rows, lead=2)
+
+
 def test_rows_apart_and_leading_rows():
     """k and v as slices of a fused product's rows; rows before the first sequence."""
     _run(128, 8, True, 16, 2, SEQS, "fp32", 12, gap=5)
@@ -169,6 +177,14 @@ def test_large_offsets():
     # half a step of the code, and the fp32 rounding of code and product
     assert bool(((k - x).abs() <= s / 127 * 0.5 + s * 2.0 ** -22).all())
     assert torch.equal(v, -k)
+    # attention over those pages: the bits of the same pages in a small pool
+    at = [pages - 1, 3, pages - 2]
+    small = bg.KVCache(*(t[at].clone() for t in (gpu.k_codes, gpu.v_codes, gpu.k_scales, gpu.v_scales)), None, None, d, 8)
+    tiny = torch.arange(3, dtype=torch.int32, device="cuda")[None]
+    q = torch.randn((130, 2 * heads, d), generator=g, device="cuda").bfloat16()
+    for n in (130, 1):
+        s1 = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        assert torch.equal(bg.paged_attention(q[:n], gpu, table, lens, s1), bg.paged_attention(q[:n], small, tiny, lens, s1))
 
 
 def test_empty_calls():

@@ -67,6 +67,20 @@ def test_magnitudes(scale):
     _case(4, 512, "fp32", "fp32", "fp32", 3, x_scale=scale)
 
 
+def test_rows_past_one_launch():
+    """More rows than a launch takes: as the same rows by themselves."""
+    t, k = (1 << 21) + 5, 128
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn((t, k), generator=g, device="cuda").bfloat16()
+    w = torch.rand(k, generator=g, device="cuda")
+    res = x.flip(0).contiguous()
+    say(f"rms_norm_int8 t={t} k={k}")
+    out = bg.rms_norm_int8(x, w, 1e-5, res)
+    for at in (0, (1 << 21) - 3, t - 8):
+        part = bg.rms_norm_int8(x[at : at + 8].clone(), w, 1e-5, res[at : at + 8].clone())
+        assert all(torch.equal(a[at : at + 8], b) for a, b in zip(out, part))
+
+
 def test_zero_rows_and_zero_eps():
     x = torch.zeros(3, 256, device="cuda")
     x[1] = 1
