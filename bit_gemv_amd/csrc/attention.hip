@@ -101,6 +101,10 @@ LQ_DEVICE float add_halves32(float v) { return swap_add32(v, v); }
 LQ_DEVICE float add_halves16(float v) { return swap_add16(v, v); }
 LQ_DEVICE float max4(f32x4 v) { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); }
 
+// A row without keys has the sum 0: zeros, and -inf for the log; a NaN goes on.
+LQ_DEVICE float inverse_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+LQ_DEVICE float log_sum(float m, float l) { return l == 0.0f ? -__builtin_inff() : m * kLn2 + logf(l); }
+
 // the power of two at or below a positive normal float
 LQ_DEVICE float pow2_floor(float v) { return __uint_as_float(__float_as_uint(v) & 0x7F800000u); }
 
@@ -252,11 +256,12 @@ LQ_DEVICE void load_words(uint32_t *dst, const uint8_t *p) {
         dst[0] = v[0]; dst[1] = v[1];
     }
 }
-// The wave's query rows in fp16, scaled by a power of two that is common to them
-// (the largest element to [2^14, 2^15)); the sign of the softmax's scale goes to
-// q, so that larger products are larger scores. Returns what a product is to be
-// multiplied by to be a score in log2; qsum: the sum of this lane's elements.
-template <int STEPS, int BITS, bool SYM>
+// The lane's query row in fp16, scaled by a power of two (the row's largest
+// element to [2^14, 2^15)); the sign of the softmax's scale goes to q, so that
+// larger products are larger scores. The row's other elements are in the lanes
+// 32 (MANY) or 16, 32 and 48 away. Returns what a product is to be multiplied
+// by to be a score in log2; qsum: the sum of this lane's elements.
+template <int STEPS, int BITS, bool SYM, bool MANY>
 LQ_DEVICE float q_to_fp16(const u32x4 *raw, float scale, f16x8 *qf, float &qsum) {
     // magnitudes of bf16 order as their bits do, two to a word
     u16x2 top2 = {0, 0};
@@ -265,8 +270,8 @@ LQ_DEVICE float q_to_fp16(const u32x4 *raw, float scale, f16x8 *qf, float &qsum)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             top2 = __builtin_elementwise_max(top2, __builtin_bit_cast(u16x2, raw[s][j] & 0x7FFF7FFFu));
-    const float amax = max_halves16(
-        max_halves32(row_max(__uint_as_float((uint32_t)(top2[0] > top2[1] ? top2[0] : top2[1]) << 16))));
+    float amax = max_halves32(__uint_as_float((uint32_t)(top2[0] > top2[1] ? top2[0] : top2[1]) << 16));
+    if (!MANY) amax = max_halves16(amax);
     int sh = 141 - (int)(__float_as_uint(amax) >> 23);
     sh = sh < -100 ? -100 : sh > 100 ? 100 : sh;
     const float up = scale == 0.0f ? 0.0f : copysignf(__uint_as_float((uint32_t)(sh + 127) << 23), scale);
@@ -417,12 +422,12 @@ __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void at
                 raw[s] = live ? *reinterpret_cast<const u32x4 *>(qp + d0) : u32x4{0u, 0u, 0u, 0u};
             }
             settle_pages();
-                        if (its > 0) {  // in flight while q is made ready
+            if (its > 0) {  // in flight while q is made ready
                 slots_of(0, slots, keys);
                 load_keys(x, slots);
                 load_values(x, slots);
             }
-            c1 = q_to_fp16<C::STEPS, BITS, SYM>(raw, a.scale, qf, qsum);
+            c1 = q_to_fp16<C::STEPS, BITS, SYM, false>(raw, a.scale, qf, qsum);
             if (!SYM) qsum = add_halves16(add_halves32(qsum));
         }
 
@@ -613,7 +618,7 @@ __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void at
             for (int w = 0; w < WAVES; ++w) lr += lds_l[w][r] * __builtin_amdgcn_exp2f(lds_m[w][r] - mr);
             const uint32_t wt = wr / (uint32_t)group;
             const int64_t at = (rows.begin + wt) * a.q_heads + h * group + (wr - wt * (uint32_t)group);
-            const float norm = !whole ? 1.0f : lr > 0.0f ? 1.0f / lr : 0.0f;
+            const float norm = !whole ? 1.0f : inverse_sum(lr);
 #pragma unroll
             for (int d = 4 * c; d < D; d += 4 * kTeam) {
                 f32x4 v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -631,10 +636,10 @@ __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void at
             if (c == 0) {
                 if (!whole) {
                     float *ml = span.ml + (slot_of + r) * 2;
-                    ml[0] = lr > 0.0f ? mr : -__builtin_inff();
+                    ml[0] = lr == 0.0f ? -__builtin_inff() : mr;
                     ml[1] = lr;
                 } else if (a.lse) {
-                    a.lse[at] = lr > 0.0f ? mr * kLn2 + logf(lr) : -__builtin_inff();
+                    a.lse[at] = log_sum(mr, lr);
                 }
             }
         }
@@ -831,7 +836,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
 
         typename C::Load x;
         if (its > 0) load_pages(0);
-        // q as in the other kernel: fp16, a power of two common to the wave's rows
+        // q as in the other kernel: fp16, scaled by a power of two
         f16x8 qf[C::STEPS];
         float c1, qsum = 0.0f;
         {
@@ -842,7 +847,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
                 raw[s] = live ? *reinterpret_cast<const u32x4 *>(qp + 16 * s) : u32x4{0u, 0u, 0u, 0u};
             asm volatile("" : "+v"(pid));
             if (its > 0) load(x, 0);
-            c1 = q_to_fp16<C::STEPS, BITS, SYM>(raw, a.scale, qf, qsum);
+            c1 = q_to_fp16<C::STEPS, BITS, SYM, true>(raw, a.scale, qf, qsum);
             if (!SYM) qsum = add_halves32(qsum);
         }
         if (its > 0) store(x, lds[0]);
@@ -1036,7 +1041,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
             const int64_t at = (rows.begin + tok) * a.q_heads + qh;
             const int64_t part = slot_of + wave * 32 + n;
             l *= sref * (1.0f / kHead);
-            const float f = (whole ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f) * (sref * (1.0f / kHead));
+            const float f = (whole ? inverse_sum(l) : 1.0f) * (sref * (1.0f / kHead));
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int mrow = 8 * (i / 4) + 4 * half + i % 4;
@@ -1062,10 +1067,10 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
             }
             if (half == 0) {
                 if (!whole) {
-                    span.ml[part * 2] = l > 0.0f ? m : -__builtin_inff();
+                    span.ml[part * 2] = l == 0.0f ? -__builtin_inff() : m;
                     span.ml[part * 2 + 1] = l;
                 } else if (a.lse) {
-                    a.lse[at] = l > 0.0f ? m * kLn2 + logf(l) : -__builtin_inff();
+                    a.lse[at] = log_sum(m, l);
                 }
             }
         }
@@ -1115,13 +1120,13 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Span span) {
             v += *reinterpret_cast<const f32x4 *>(span.o + at * D + 4 * c) *
                  __builtin_amdgcn_exp2f(span.ml[2 * at] - mall);
         }
-        v *= l > 0.0f ? 1.0f / l : 0.0f;
+        v *= inverse_sum(l);
         const uint32_t wt = wr / (uint32_t)group;
         const int64_t at = (rows.begin + wt) * a.q_heads + h * group + (wr - wt * (uint32_t)group);
         const bf16x2_t b0{(__bf16)v[0], (__bf16)v[1]}, b1{(__bf16)v[2], (__bf16)v[3]};
         *reinterpret_cast<u32x2 *>(a.out + at * D + 4 * c) =
             u32x2{__builtin_bit_cast(uint32_t, b0), __builtin_bit_cast(uint32_t, b1)};
-        if (c == 0 && a.lse) a.lse[at] = l > 0.0f ? mall * kLn2 + logf(l) : -__builtin_inff();
+        if (c == 0 && a.lse) a.lse[at] = log_sum(mall, l);
     }
 }
 

@@ -501,10 +501,10 @@ lq_status kv_cache_read(const lq_kv_cache *cache, void *k, void *v, lq_dtype typ
  * out bf16 [rows][q_heads][head_dim]; lse nullable fp32 [rows][q_heads]:
  * log sum_j exp(scale q . k_hat). q and out 16-byte aligned.
  * Products run on fp16 MFMA with exact integer codes, q scaled by a power of
- * two (exact down to 2^-28 of the largest element of up to 32 rows) and weights p
- * rounded to fp16; scales, sums and softmax
- * statistics are fp32. |q| up to 1e30, |scale q . k_hat| below 1e30; at most
- * 2^30 tokens in a sequence.
+ * two for each row and head (exact down to 2^-30 of its largest element) and
+ * weights p rounded to fp16; scales, sums and softmax statistics are fp32.
+ * |q| up to 1e30, |scale q . k_hat| below 1e30; at most 2^30 tokens in a
+ * sequence. A NaN in q makes its own row and head NaN (lse too) and no other.
  * workspace: at least paged_attention_workspace_bytes(...) bytes for the same
  * arguments (may be 0: then NULL is fine), 256-byte aligned, scratch: calls
  * that may overlap need one each.

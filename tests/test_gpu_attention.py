@@ -132,8 +132,8 @@ def test_magnitudes_of_q(q_scale, k_scale):
 
 
 def test_heads_of_different_size_in_one_tile():
-    """Rows of one 16-row tile whose q differ by 2^14: each is still within its
-    own bound plus the tile's, fp16 subnormals of the largest row's scaling."""
+    """Rows of one 16-row tile whose q differ by 2^14: each within its own
+    bound, as the power of two that scales q is the row's own."""
     rng = np.random.default_rng(13)
     b = Batch([(64, 1)], 16, rng)
     ref = new_cache(b, 16, 1, 64, 8, True)
@@ -143,6 +143,33 @@ def test_heads_of_different_size_in_one_tile():
     say("paged_attention uneven heads")
     out = bg.paged_attention(dev_bf16f(q), to_gpu(ref), *b.on_gpu())
     check_attention(out, None, want, wl, bound, "uneven heads")
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 3e38])
+@pytest.mark.parametrize("bits,sym", [(4, False), (8, True)])
+def test_a_row_that_is_not_finite_changes_no_other(bad, bits, sym):
+    """In tiles of 8, 16 and 128 rows, whole and in parts; a NaN reaches its
+    row's result, split or not."""
+    rng = np.random.default_rng(19)
+    b = Batch([(700, 3), (40, 30), (9, 1)], 16, rng)
+    ref = new_cache(b, 16, 1, 64, bits, sym)
+    fill(ref, b, rng)
+    q = bf16(rng.standard_normal((34, 4, 64)))
+    want, wl, bound = serving.attention(q, ref, b.lists, b.kv, b.starts, 0.125)
+    hit = [(0, 1), (2, 3), (7, 0), (33, 2)]
+    gq = dev_bf16f(q)
+    for i, (r, h) in enumerate(hit):
+        gq[r, h, 5 * i] = bad
+    keep = np.ones((34, 4), bool)
+    keep[tuple(np.array(hit).T)] = False
+    for hints in ((0, 0), (30, 5000), (3, 5000), (2, 5000)):
+        say(f"paged_attention q {bad} bits={bits} hints {hints}")
+        lse = torch.empty((34, 4), device="cuda")
+        out = bg.paged_attention(gq, to_gpu(ref), *b.on_gpu(), max_rows=hints[0], max_kv=hints[1], lse=lse)
+        k = torch.from_numpy(keep).cuda()
+        check_attention(out[k], lse[k], want[keep], wl[keep], bound[keep], f"{bad} {hints}")
+        if bad != bad:
+            assert bool(out[~k].isnan().all()) and bool(lse[~k].isnan().all())
 
 
 def test_pages_outside_the_pool_are_not_attended_to():
