@@ -9,7 +9,8 @@
 // subtracting; q becomes fp16 exactly after a power-of-two scaling; the key
 // scale is applied to the fp32 score and the value scale to p before it is
 // rounded to fp16 (2^-11), normalized by a running bound of the value scales
-// so that it stays in fp16's range.
+// so that it stays in fp16's range. A value zero outside the codes counts with
+// the unrounded p: its weight may vanish in fp16 while scale times zero is large.
 //
 // The first product is formed transposed, keys x rows: a lane then holds four
 // neighbouring keys of one row, which is the operand layout that the second
@@ -51,22 +52,24 @@ constexpr float kHead = 8.0f, kHeadLog2 = 3.0f;
 LQ_DEVICE f16x2 as_f16x2(uint32_t w) { return __builtin_bit_cast(f16x2, w); }
 
 template <uint32_t SEL0, uint32_t SEL1>
-LQ_DEVICE void int8_pairs(uint32_t w, f16x2 *out) {
-    const f16x2 off = {(_Float16)1152.0f, (_Float16)1152.0f};
-    out[0] = as_f16x2(__builtin_amdgcn_perm(0x64646464u, w, SEL0)) - off;
-    out[1] = as_f16x2(__builtin_amdgcn_perm(0x64646464u, w, SEL1)) - off;
+LQ_DEVICE void int8_pairs(uint32_t w, f16x2 *out, f16x2 off0, f16x2 off1) {
+    out[0] = as_f16x2(__builtin_amdgcn_perm(0x64646464u, w, SEL0)) + off0;
+    out[1] = as_f16x2(__builtin_amdgcn_perm(0x64646464u, w, SEL1)) + off1;
 }
-LQ_DEVICE void int8_row(uint32_t w, f16x2 *out) { int8_pairs<0x04010400u, 0x04030402u>(w, out); }
-LQ_DEVICE void int8_quad(uint32_t w, f16x2 *out) { int8_pairs<0x04020400u, 0x04030401u>(w, out); }
+LQ_DEVICE f16x2 both(float v) { return f16x2{(_Float16)v, (_Float16)v}; }
+LQ_DEVICE void int8_row(uint32_t w, f16x2 *out, f16x2 off = both(-1152.0f)) {
+    int8_pairs<0x04010400u, 0x04030402u>(w, out, off, off);
+}
+LQ_DEVICE void int8_quad(uint32_t w, f16x2 *out, f16x2 off0 = both(-1152.0f), f16x2 off1 = both(-1152.0f)) {
+    int8_pairs<0x04020400u, 0x04030401u>(w, out, off0, off1);
+}
 // `magic` is the fp16 pair (1024, 1024) in a vector register, so that mask and
 // merge are one v_and_or_b32
-LQ_DEVICE f16x2 int4_low(uint32_t w, uint32_t magic) {
-    const f16x2 off = {(_Float16)1032.0f, (_Float16)1032.0f};
-    return as_f16x2((w & 0x000F000Fu) | magic) - off;
+LQ_DEVICE f16x2 int4_low(uint32_t w, uint32_t magic, f16x2 off = both(-1032.0f)) {
+    return as_f16x2((w & 0x000F000Fu) | magic) + off;
 }
-LQ_DEVICE f16x2 int4_high(uint32_t w, uint32_t magic) {
-    const f16x2 sc = {(_Float16)0.0625f, (_Float16)0.0625f}, off = {(_Float16)-72.0f, (_Float16)-72.0f};
-    return __builtin_elementwise_fma(as_f16x2((w & 0x00F000F0u) | magic), sc, off);
+LQ_DEVICE f16x2 int4_high(uint32_t w, uint32_t magic, f16x2 off = both(-72.0f)) {
+    return __builtin_elementwise_fma(as_f16x2((w & 0x00F000F0u) | magic), both(0.0625f), off);
 }
 LQ_DEVICE uint32_t fp16_magic() {
     uint32_t m = 0x64006400u;
@@ -516,11 +519,11 @@ __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void at
                 if constexpr (C::HALVES == 2) sm = fmaxf(sm, dpp_f32<kDppRowRor8>(sm));
                 const float mn = fmaxf(m, tm);
                 const float sn = fmaxf(fmaxf(sref, kScaleMin), pow2_floor(sm));
-                const float both = __builtin_amdgcn_exp2f(m - mn) * (sref / sn);  // 0 before the first keys
-                l *= both;
-                vz *= both;
+                const float by = __builtin_amdgcn_exp2f(m - mn) * (sref / sn);  // 0 before the first keys
+                l *= by;
+                vz *= by;
 #pragma unroll
-                for (int q = 0; q < C::TILES; ++q) o[q] *= both;
+                for (int q = 0; q < C::TILES; ++q) o[q] *= by;
                 m = mn;
                 sref = sn;
                 mm = m + (__builtin_amdgcn_logf(sn) - kHeadLog2);
@@ -538,7 +541,20 @@ __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void at
                 pb[2 * u] = f16x2{(_Float16)pv[0], (_Float16)pv[2]};
                 pb[2 * u + 1] = f16x2{(_Float16)pv[1], (_Float16)pv[3]};
                 if (!SYM) {
-                    // the zero point's share, from the same rounded weights
+                    // The zero's share, from the same rounded weights; from the
+                    // unrounded ones what of it lies outside the codes, as they may
+                    // vanish in fp16 where a tiny scale goes with a large zero.
+                    constexpr float levels = 2.0f * C::kMid - 1.0f;
+                    const f32x4 zv = x.zv[u];
+                    const float low = fminf(fminf(zv[0], zv[1]), fminf(zv[2], zv[3]));
+                    if (__any(!(low >= 0.0f && max4(zv) <= levels))) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float near = fminf(fmaxf(zv[i], 0.0f), levels);
+                            vz = __builtin_fmaf(pv[i], zv[i] - near, vz);
+                            x.zv[u][i] = near;
+                        }
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         vz = __builtin_fmaf((float)pb[2 * u + (i & 1)][i >> 1], x.zv[u][i] - C::kMid, vz);
@@ -654,7 +670,7 @@ __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void at
 // matrix instruction reads them, so the conversion costs a 32 W-th of an
 // operation per row and code. Two blocks a CU (64 KB of LDS
 // each): one's softmax runs beside the other's products.
-template <int D, int BITS, int W>
+template <int D, int BITS, bool SYM, int W>
 struct Many {
     static constexpr int ROWS = 32 * W;
     static constexpr int KT = D == 64 ? 16 * W : 8 * W;  // keys of a tile
@@ -678,9 +694,25 @@ struct Many {
     static constexpr int KPAD = KT + (D == 64 ? 2 : 1);
     struct Buf {
         f16x8 k[CHUNKS * KPAD], v[KT / 8 * D];
-        float meta[4][KT];   // key scales, value scales, key zeros, value zeros
+        float meta[4][KT];   // key scales, value scales, what is left of key and value zeros
         float stat[4][KT / 16];  // [1]: the largest value scale of each 16 keys
-        int bad[KT / 16];        // whether they lie outside the pool
+        int flags[KT / 16];      // kBad, kWideK, kWideV of each 16 keys
+        // asymmetric: what is added to a code in the mantissa of 1024 (and, INT4,
+        // of 64) to take the zero off it: keys twice each, values by quads in the
+        // order 0 2 1 3
+        uint32_t koff[SYM ? 1 : BITS == 4 ? 2 : 1][SYM ? 1 : KT];
+        alignas(8) _Float16 voff[SYM ? 1 : BITS == 4 ? 2 : 1][SYM ? 4 : KT];
+    };
+    // Key zeros between -1024 and 1024 and value zeros among the codes (all but
+    // those of keys and values far from 0 for their range) are taken off the codes
+    // exactly in the conversion to fp16, once for all rows; what is left of others
+    // (meta's zeros) is taken off the sums, in branches that these flags choose.
+    // Scores and weights thus cost the same with zeros as without (ragged chunks
+    // of 64-wide heads, INT8: 95 us, against 112 with every zero taken off the
+    // sums).
+    enum { kBad = 1, kWideK = 2, kWideV = 4 };
+    struct Off {
+        f16x2 k[2], v[2][2][2];  // [low, high nibble]; values [quad][tokens 0 2, 1 3][nibble]
     };
     struct Load {
         uint32_t k[KB / 4], v0[VW], v1[VW];
@@ -703,7 +735,7 @@ LQ_DEVICE void load_any(uint32_t *dst, const uint8_t *p) {
 
 template <int D, int BITS, bool SYM, int W>
 __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(AttnArgs a, Span span) {
-    using C = Many<D, BITS, W>;
+    using C = Many<D, BITS, SYM, W>;
     __shared__ typename C::Buf lds[C::RING];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -790,48 +822,89 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
             x.meta = meta_src[slot];
         };
         // one 16-byte write of the tile: i below KC a chunk of keys, then values
-        auto store_part = [&](const typename C::Load &x, typename C::Buf &b, int i) {
+        auto store_part = [&](const typename C::Load &x, typename C::Buf &b, int i, const typename C::Off &off) {
             f16x2 f[4];
             if (i < C::KC) {
                 if constexpr (BITS == 8) {
-                    int8_row(x.k[(2 * i) % (C::KB / 4)], f);
-                    int8_row(x.k[(2 * i + 1) % (C::KB / 4)], f + 2);
+                    int8_row(x.k[(2 * i) % (C::KB / 4)], f, off.k[0]);
+                    int8_row(x.k[(2 * i + 1) % (C::KB / 4)], f + 2, off.k[0]);
                 } else {
                     const uint32_t w = x.k[i % (C::KB / 4)], w8 = w >> 8;
-                    f[0] = int4_low(w, magic); f[1] = int4_high(w, magic);
-                    f[2] = int4_low(w8, magic); f[3] = int4_high(w8, magic);
+                    f[0] = int4_low(w, magic, off.k[0]); f[1] = int4_high(w, magic, off.k[1]);
+                    f[2] = int4_low(w8, magic, off.k[0]); f[3] = int4_high(w8, magic, off.k[1]);
                 }
                 b.k[(my_part * C::KC + i) * C::KPAD + my_key] = join(f);
             } else {
                 const int e = i - C::KC;  // which of the thread's elements
                 if constexpr (BITS == 8) {
-                    int8_quad(x.v0[e % C::VW], f);
-                    int8_quad(x.v1[e % C::VW], f + 2);
+                    int8_quad(x.v0[e % C::VW], f, off.v[0][0][0], off.v[0][1][0]);
+                    int8_quad(x.v1[e % C::VW], f + 2, off.v[1][0][0], off.v[1][1][0]);
                 } else {
                     const uint32_t v0 = x.v0[(e >> 1) % C::VW], v1 = x.v1[(e >> 1) % C::VW];
                     if (e & 1) {
-                        f[0] = int4_high(v0, magic); f[1] = int4_high(v0 >> 8, magic);
-                        f[2] = int4_high(v1, magic); f[3] = int4_high(v1 >> 8, magic);
+                        f[0] = int4_high(v0, magic, off.v[0][0][1]); f[1] = int4_high(v0 >> 8, magic, off.v[0][1][1]);
+                        f[2] = int4_high(v1, magic, off.v[1][0][1]); f[3] = int4_high(v1 >> 8, magic, off.v[1][1][1]);
                     } else {
-                        f[0] = int4_low(v0, magic); f[1] = int4_low(v0 >> 8, magic);
-                        f[2] = int4_low(v1, magic); f[3] = int4_low(v1 >> 8, magic);
+                        f[0] = int4_low(v0, magic, off.v[0][0][0]); f[1] = int4_low(v0 >> 8, magic, off.v[0][1][0]);
+                        f[2] = int4_low(v1, magic, off.v[1][0][0]); f[3] = int4_low(v1 >> 8, magic, off.v[1][1][0]);
                     }
                 }
                 b.v[my_pair * D + my_t + e * C::TP] = join(f);
             }
         };
         constexpr int kParts = C::KC + C::DW;
+        // scales and zeros of the wave's 16 keys; returns the offsets of this
+        // thread's own keys, which the wave itself has just written
         auto store_meta = [&](const typename C::Load &x, typename C::Buf &b) {
+            typename C::Off off;
             // slots that hold nothing count as zeros
-            const float meta = x.dead ? (lane < 32 ? 0.0f : C::kMid) : x.meta;
+            float meta = x.dead ? (lane < 32 ? 0.0f : C::kMid) : x.meta;
+            int flags = x.bad ? C::kBad : 0;
+            if constexpr (SYM) {
+                off.k[0] = both(-1024.0f - C::kMid);
+                off.k[1] = both(-64.0f - C::kMid);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) off.v[i >> 2][(i >> 1) & 1][i & 1] = off.k[i & 1];
+            } else if (lane >= 32) {
+                const float near = lane < 48 ? fminf(fmaxf(rintf(meta), -1024.0f), 1024.0f)
+                                             : fminf(fmaxf(rintf(meta), 0.0f), 2.0f * C::kMid - 1.0f);
+                meta -= near;
+                const f16x2 low = both(-1024.0f - near), high = both(-64.0f - near);
+                const int key = 16 * my_group + (lane & 15), quad = (key & ~3) | ((key & 1) << 1) | ((key >> 1) & 1);
+                if (lane < 48) {
+                    b.koff[0][key] = __builtin_bit_cast(uint32_t, low);
+                    if (BITS == 4) b.koff[BITS == 4][key] = __builtin_bit_cast(uint32_t, high);
+                } else {
+                    b.voff[0][quad] = low[0];
+                    if (BITS == 4) b.voff[BITS == 4][quad] = high[0];
+                }
+            }
             b.meta[lane >> 4][16 * my_group + (lane & 15)] = meta;
             b.stat[lane >> 4][my_group] = row_max(meta);
-            b.bad[my_group] = x.bad;
+            if constexpr (!SYM) {
+                const uint64_t wide = __ballot(lane >= 32 && meta != 0.0f);
+                flags |= ((wide >> 32) & 0xFFFFu ? C::kWideK : 0) | (wide >> 48 ? C::kWideV : 0);
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+                for (int i = 0; i < (BITS == 4 ? 2 : 1); ++i) {
+                    off.k[i] = as_f16x2(b.koff[i][my_key]);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const u32x2 w = *reinterpret_cast<const u32x2 *>(&b.voff[i][16 * my_group + 8 * u + 4 * (my_pair & 1)]);
+                        off.v[u][0][i] = as_f16x2(w[0]);
+                        off.v[u][1][i] = as_f16x2(w[1]);
+                    }
+                }
+            }
+            b.flags[my_group] = flags;
+            return off;
         };
         auto store = [&](const typename C::Load &x, typename C::Buf &b) {
-            store_meta(x, b);
+            const typename C::Off off = store_meta(x, b);
 #pragma unroll
-            for (int i = 0; i < kParts; ++i) store_part(x, b, i);
+            for (int i = 0; i < kParts; ++i) store_part(x, b, i, off);
         };
 
         typename C::Load x;
@@ -874,22 +947,21 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
         // scale, mask and reference of the scores t of block kb of tile b:
         // register i of the lane is key 8 (i / 4) + 4 half + i % 4 of row n
         auto settle = [&](const typename C::Buf &b, int kb, int key0, f32x16 &t) {
+            const int flags0 = __builtin_amdgcn_readfirstlane(b.flags[2 * kb]);
+            const int flags1 = __builtin_amdgcn_readfirstlane(b.flags[2 * kb + 1]);
+            const int bad0 = flags0 & C::kBad, bad1 = flags1 & C::kBad;
+            if (!SYM && ((flags0 | flags1) & C::kWideK)) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    t[i] = __builtin_fmaf(-b.meta[2][kb * 32 + 8 * (i / 4) + 4 * half + i % 4], qsum, t[i]);
+            }
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int at = kb * 32 + 8 * r + 4 * half;
-                const f32x4 sk = *reinterpret_cast<const f32x4 *>(&b.meta[0][at]);
-                f32x4 zk;
-                if (!SYM) zk = *reinterpret_cast<const f32x4 *>(&b.meta[2][at]);
+                const f32x4 sk = *reinterpret_cast<const f32x4 *>(&b.meta[0][kb * 32 + 8 * r + 4 * half]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float v = t[4 * r + i];
-                    if (!SYM) v = __builtin_fmaf(C::kMid - zk[i], qsum, v);
-                    t[4 * r + i] = v * sk[i];
-                }
+                for (int i = 0; i < 4; ++i) t[4 * r + i] *= sk[i];
             }
             const float sm = fmaxf(b.stat[1][2 * kb], b.stat[1][2 * kb + 1]);
-            const int bad0 = __builtin_amdgcn_readfirstlane(b.bad[2 * kb]);
-            const int bad1 = __builtin_amdgcn_readfirstlane(b.bad[2 * kb + 1]);
             const int first = key0 + 32 * kb;
             if (first + 31 > safe || first + 32 > kstop || (bad0 | bad1)) {
                 const int last = (row_pos < kstop ? row_pos : kstop - 1) - first - 4 * half;
@@ -906,26 +978,33 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
                 tm = max_halves32(tm);
                 const float mn = fmaxf(m, tm);
                 const float sn = fmaxf(fmaxf(sref, kScaleMin), pow2_floor(sm));
-                const float both = __builtin_amdgcn_exp2f(m - mn) * (sref / sn);  // 0 before the first keys
-                l *= both;
-                vz *= both;
+                const float by = __builtin_amdgcn_exp2f(m - mn) * (sref / sn);  // 0 before the first keys
+                l *= by;
+                vz *= by;
 #pragma unroll
                 for (int j = 0; j < C::JT; ++j)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[j][i] *= both;
+                    for (int i = 0; i < 16; ++i) o[j][i] *= by;
                 m = mn;
                 sref = sn;
                 mm = m + (__builtin_amdgcn_logf(sn) - kHeadLog2);
             }
-        };
-        // value scales (and zeros) of a lane's keys of block kb
-        auto value_meta = [&](const typename C::Buf &b, int kb, int s, f32x4 *sv, f32x4 *zv) {
+            if (!SYM && ((flags0 | flags1) & C::kWideV)) {
+                // of the unrounded weights: they may vanish in fp16 where a tiny
+                // scale goes with a large zero
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int at = kb * 32 + 16 * s + 8 * r + 4 * half;
-                sv[r] = *reinterpret_cast<const f32x4 *>(&b.meta[1][at]);
-                if (!SYM) zv[r] = *reinterpret_cast<const f32x4 *>(&b.meta[3][at]);
+                for (int i = 0; i < 16; ++i) {
+                    const int at = kb * 32 + 8 * (i / 4) + 4 * half + i % 4;
+                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(t[i], c1, -mm));
+                    vz = __builtin_fmaf(p, b.meta[1][at] * b.meta[3][at], vz);
+                }
             }
+        };
+        // value scales of a lane's keys of block kb
+        auto value_scales = [&](const typename C::Buf &b, int kb, int s, f32x4 *sv) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                sv[r] = *reinterpret_cast<const f32x4 *>(&b.meta[1][kb * 32 + 16 * s + 8 * r + 4 * half]);
         };
         // The weights of t (block kb of tile b), their product with the values,
         // the next block's scores u = keys kr . q, and (STORE) the tile x on its
@@ -937,7 +1016,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
         // scheduling barriers, or raising the wave's priority over it, changed
         // nothing beyond noise: 541-569 us for the 2048-token chunk.)
         auto weigh = [&](const typename C::Buf &b, int kb, const f32x16 &t, const typename C::Buf &bn, int kn, f16x8 *kr,
-                         f32x4 *sv, f32x4 *zv, f32x16 &u, bool with_store, typename C::Buf &to) {
+                         f32x4 *sv, f32x16 &u, bool with_store, typename C::Buf &to) {
             constexpr int EG = 8 / C::JT;  // weights of a group
             key_operands(bn, kn, C::STEPS / 2, kr);
             f16x8 vr[C::JT], pf[2];
@@ -965,22 +1044,18 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
                 for (int r = 0; r < 2; ++r) {
                     pb[2 * r] = f16x2{(_Float16)pv[4 * r], (_Float16)pv[4 * r + 2]};
                     pb[2 * r + 1] = f16x2{(_Float16)pv[4 * r + 1], (_Float16)pv[4 * r + 3]};
-                    if (!SYM) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            vz = __builtin_fmaf((float)pb[2 * r + (i & 1)][i >> 1], zv[r][i] - C::kMid, vz);
-                    }
                 }
                 pf[s] = join(pb);
-                if (s == 0) value_meta(b, kb, 1, sv, zv);
+                if (s == 0) value_scales(b, kb, 1, sv);
             }
-            if (with_store) store_meta(x, to);
+            typename C::Off off;
+            if (with_store) off = store_meta(x, to);
 #pragma unroll
             for (int g = 0; g < C::JT; ++g) {
                 o[g] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vr[g], pf[1], o[g], 0, 0, 0);
                 if (with_store) {
 #pragma unroll
-                    for (int i = g * kParts / C::JT; i < (g + 1) * kParts / C::JT; ++i) store_part(x, to, i);
+                    for (int i = g * kParts / C::JT; i < (g + 1) * kParts / C::JT; ++i) store_part(x, to, i, off);
                 }
             }
         };
@@ -996,15 +1071,15 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
             const int key0 = kbeg + C::KT * it;
             typename C::Buf &to = lds[now + 2 < C::RING ? now + 2 : now + 2 - C::RING];
             f16x8 kr[C::STEPS];
-            f32x4 sv[2], zv[2];
+            f32x4 sv[2];
 #pragma unroll
             for (int kb = 0; kb < KBLK; ++kb) {
                 const bool last = kb == KBLK - 1;
                 f32x16 &cur = kb & 1 ? u : t, &then = kb & 1 ? t : u;
                 key_operands(last ? next : b, last ? 0 : kb + 1, 0, kr);
-                value_meta(b, kb, 0, sv, zv);
+                value_scales(b, kb, 0, sv);
                 settle(b, kb, key0, cur);
-                weigh(b, kb, cur, last ? next : b, last ? 0 : kb + 1, kr, sv, zv, then, last, to);
+                weigh(b, kb, cur, last ? next : b, last ? 0 : kb + 1, kr, sv, then, last, to);
             }
             if (it + 3 < its) load(x, it + 3);
             lds_barrier();
@@ -1219,7 +1294,7 @@ static hipError_t launch_tiles(const AttnArgs &a, const Pass &p, char *workspace
     Span span{reinterpret_cast<float *>(workspace), nullptr, p.cap, p.by_unit, p.least, p.most};
     span.ml = span.o + (int64_t)2 * p.cap * a.c.heads * ROWS * D;
     const dim3 grid((uint32_t)(p.cap * a.c.heads));
-    constexpr int step = ROWS < 128 ? kFewStep : Many<D, BITS, ROWS / 32>::KT;
+    constexpr int step = ROWS < 128 ? kFewStep : Many<D, BITS, SYM, ROWS / 32>::KT;
     if constexpr (ROWS < 128)
         hipLaunchKernelGGL((attn_few_kernel<D, BITS, SYM, ROWS, kFewWaves>), grid, dim3(64 * kFewWaves), 0, st, a, span);
     else

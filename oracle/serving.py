@@ -110,7 +110,10 @@ def attention(q, cache, table, kv_lens, row_starts, scale):
       (2^-11 + 2^-20 + 4 d) W        weights rounded to fp16, exp2, and scores
                                      off by d on both sides of the quotient
       n 2^-24 W'                     n fp32 additions per sum
-      n 2^-27 max|v|                 weights below fp16's subnormals
+      n 2^-27 max|v|                 weights below fp16's subnormals: half a step,
+                                     2^-28 of the largest scale, times a code less
+                                     a zero among the codes, at most twice max|v|
+                                     over that scale
 
     with W = sum p |v| / sum p, W' the same of s (|c - mid| + |z - mid|), and
     d = (D + 8) 2^-24 max_j scale s_j sum |q| (|c - mid| + |z - mid|), the fp32

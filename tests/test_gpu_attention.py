@@ -124,6 +124,31 @@ def test_uneven_value_scales(bits, sym):
         _run([(300, 1), (200, 20)], 64, bits, sym, seed=11, v_scale=f)
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_zeros_far_from_the_codes(bits, d):
+    """Keys and values far from zero for their range (zeros of thousands), all
+    alike (zeros of 1e8 and more) and on one side, among ordinary ones."""
+    rng = np.random.default_rng(20)
+    b = Batch([(200, 40), (90, 3), (70, 1)], 16, rng)
+    ref = new_cache(b, 16, 1, d, bits, False)
+    fill(ref, b, rng)
+    for i, (held, every) in enumerate(((200, 5), (90, 1), (70, 33))):
+        for t in range(0, held, every):
+            at = b.lists[i][t // 16], t % 16
+            kind = (t // every) % 4
+            for side in "kv":
+                x = (5 + 0.01 * rng.standard_normal((1, d)), np.full((1, d), 0.03125), -7 - rng.random((1, d)),
+                     rng.standard_normal((1, d)))[kind]
+                ref.put_rows(*at, side, x)
+    q = bf16(0.2 * rng.standard_normal((44, 5, d)))
+    want, wl, bound = serving.attention(q, ref, b.lists, b.kv, b.starts, d ** -0.5)
+    for hints in ((0, 0), (40, 5000), (3, 5000), (1, 5000)):
+        say(f"paged_attention far zeros bits={bits} d={d} hints {hints}")
+        out = bg.paged_attention(dev_bf16f(q), to_gpu(ref), *b.on_gpu(), max_rows=hints[0], max_kv=hints[1])
+        check_attention(out, None, want, wl, bound, f"far zeros {hints}")
+
+
 @pytest.mark.parametrize("q_scale,k_scale", [(1e-30, 1.0), (1e30, 1e-30), (1e-5, 1e5), (1e18, 1e-18)])
 def test_magnitudes_of_q(q_scale, k_scale):
     """q far outside fp16's range, tiny or huge."""
