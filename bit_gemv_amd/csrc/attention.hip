@@ -944,35 +944,44 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
 #pragma unroll
             for (int s = from; s < from + C::STEPS / 2; ++s) kr[s] = b.k[(2 * s + half) * C::KPAD + kb * 32 + n];
         };
-        // scale, mask and reference of the scores t of block kb of tile b:
-        // register i of the lane is key 8 (i / 4) + 4 half + i % 4 of row n
-        auto settle = [&](const typename C::Buf &b, int kb, int key0, f32x16 &t) {
+        // Scores t of block kb of tile b times the key scales, part `part` of
+        // `parts`, and their maximum: register i of the lane is key
+        // 8 (i / 4) + 4 half + i % 4 of row n.
+        auto key_scales = [&](const typename C::Buf &b, int kb, f32x4 *sk) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sk[r] = *reinterpret_cast<const f32x4 *>(&b.meta[0][kb * 32 + 8 * r + 4 * half]);
+        };
+        auto scale_scores = [&](const f32x4 *sk, f32x16 &t, float top, int part, int parts) {
+#pragma unroll
+            for (int i = part * 16 / parts; i < (part + 1) * 16 / parts; ++i) t[i] *= sk[i / 4][i % 4];
+#pragma unroll
+            for (int i = part * 16 / parts; i < (part + 1) * 16 / parts; i += 2) top = fmaxf(fmaxf(top, t[i]), t[i + 1]);
+            return top;
+        };
+        // Mask and reference of these scores, tm their maximum.
+        auto settle = [&](const typename C::Buf &b, int kb, int key0, f32x16 &t, float tm) {
             const int flags0 = __builtin_amdgcn_readfirstlane(b.flags[2 * kb]);
             const int flags1 = __builtin_amdgcn_readfirstlane(b.flags[2 * kb + 1]);
             const int bad0 = flags0 & C::kBad, bad1 = flags1 & C::kBad;
-            if (!SYM && ((flags0 | flags1) & C::kWideK)) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    t[i] = __builtin_fmaf(-b.meta[2][kb * 32 + 8 * (i / 4) + 4 * half + i % 4], qsum, t[i]);
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const f32x4 sk = *reinterpret_cast<const f32x4 *>(&b.meta[0][kb * 32 + 8 * r + 4 * half]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) t[4 * r + i] *= sk[i];
-            }
-            const float sm = fmaxf(b.stat[1][2 * kb], b.stat[1][2 * kb + 1]);
             const int first = key0 + 32 * kb;
-            if (first + 31 > safe || first + 32 > kstop || (bad0 | bad1)) {
+            const float sm = fmaxf(b.stat[1][2 * kb], b.stat[1][2 * kb + 1]);
+            if (first + 31 > safe || first + 32 > kstop || ((flags0 | flags1) & (C::kBad | C::kWideK))) {
+                if (!SYM) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int at = kb * 32 + 8 * (i / 4) + 4 * half + i % 4;
+                        t[i] = __builtin_fmaf(-b.meta[2][at] * b.meta[0][at], qsum, t[i]);
+                    }
+                }
                 const int last = (row_pos < kstop ? row_pos : kstop - 1) - first - 4 * half;
                 const int last0 = bad0 ? -1 : last, last1 = bad1 ? -1 : last;
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     t[i] = 8 * (i / 4) + i % 4 > (i < 8 ? last0 : last1) ? -__builtin_inff() : t[i];
-            }
-            float tm = t[0];
+                tm = t[0];
 #pragma unroll
-            for (int i = 1; i < 16; ++i) tm = fmaxf(tm, t[i]);
+                for (int i = 1; i < 16; ++i) tm = fmaxf(tm, t[i]);
+            }
             tm *= c1;
             if (__any(tm > m + kSlack || sm > sref * kScaleSlack)) {
                 tm = max_halves32(tm);
@@ -1012,11 +1021,13 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
         // independent work side by side: JT groups of the first 16 keys' weights,
         // each beside a score instruction; JT groups of the others', each beside a
         // score and a value instruction; then the other value instructions
-        // beside the conversion of x. (Holding the compiler to this order with
+        // beside the scaling of u (peak: its maximum) and the conversion of x. The
+        // 2048-token chunk takes 538 us so, 550 with the scaling and the sums of
+        // the weights after the run. (Holding the compiler to this order with
         // scheduling barriers, or raising the wave's priority over it, changed
-        // nothing beyond noise: 541-569 us for the 2048-token chunk.)
+        // nothing beyond noise.)
         auto weigh = [&](const typename C::Buf &b, int kb, const f32x16 &t, const typename C::Buf &bn, int kn, f16x8 *kr,
-                         f32x4 *sv, f32x16 &u, bool with_store, typename C::Buf &to) {
+                         f32x4 *sv, f32x16 &u, float &peak, bool with_store, typename C::Buf &to) {
             constexpr int EG = 8 / C::JT;  // weights of a group
             key_operands(bn, kn, C::STEPS / 2, kr);
             f16x8 vr[C::JT], pf[2];
@@ -1026,7 +1037,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
             for (int i = 0; i < 16; ++i) u[i] = 0.0f;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {  // 16 keys
-                float pv[8];
+                float pv[8], even = 0.0f;
 #pragma unroll
                 for (int g = 0; g < C::JT; ++g) {
                     u = __builtin_amdgcn_mfma_f32_32x32x16_f16(kr[s * C::JT + g], qf[s * C::JT + g], u, 0, 0, 0);
@@ -1034,7 +1045,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
 #pragma unroll
                     for (int i = g * EG; i < (g + 1) * EG; ++i) {
                         const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(t[8 * s + i], c1, -mm));
-                        l += p;
+                        if (i % 2) l += even + p;
+                        else even = p;
                         pv[i] = p * sv[i / 4][i % 4];
                     }
                     if (s == 1) vr[g] = b.v[(kb * 4 + 2 + half) * D + 32 * g + n];
@@ -1048,11 +1060,17 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
                 pf[s] = join(pb);
                 if (s == 0) value_scales(b, kb, 1, sv);
             }
+            // used here, or the compiler moves the sums behind the branch below
+            asm volatile("" : "+v"(l));
             typename C::Off off;
             if (with_store) off = store_meta(x, to);
+            f32x4 sk[4];
+            key_scales(bn, kn, sk);
+            peak = -__builtin_inff();
 #pragma unroll
             for (int g = 0; g < C::JT; ++g) {
                 o[g] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vr[g], pf[1], o[g], 0, 0, 0);
+                peak = scale_scores(sk, u, peak, g, C::JT);
                 if (with_store) {
 #pragma unroll
                     for (int i = g * kParts / C::JT; i < (g + 1) * kParts / C::JT; ++i) store_part(x, to, i, off);
@@ -1066,6 +1084,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
         // tile after that goes to LDS. A slot is written one barrier after its
         // last reader has passed and read one barrier after it is written.
         int now = 0;  // ring slot of the tile in use
+        float peak = 0.0f;
         auto step = [&](int it, f32x16 &t, f32x16 &u) {
             const typename C::Buf &b = lds[now], &next = lds[now + 1 < C::RING ? now + 1 : now + 1 - C::RING];
             const int key0 = kbeg + C::KT * it;
@@ -1078,8 +1097,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
                 f32x16 &cur = kb & 1 ? u : t, &then = kb & 1 ? t : u;
                 key_operands(last ? next : b, last ? 0 : kb + 1, 0, kr);
                 value_scales(b, kb, 0, sv);
-                settle(b, kb, key0, cur);
-                weigh(b, kb, cur, last ? next : b, last ? 0 : kb + 1, kr, sv, then, last, to);
+                settle(b, kb, key0, cur, peak);
+                weigh(b, kb, cur, last ? next : b, last ? 0 : kb + 1, kr, sv, then, peak, last, to);
             }
             if (it + 3 < its) load(x, it + 3);
             lds_barrier();
@@ -1101,6 +1120,9 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
             for (int i = 0; i < 16; ++i) ta[i] = 0.0f;
 #pragma unroll
             for (int s = 0; s < C::STEPS; ++s) ta = __builtin_amdgcn_mfma_f32_32x32x16_f16(kr[s], qf[s], ta, 0, 0, 0);
+            f32x4 sk[4];
+            key_scales(lds[0], 0, sk);
+            peak = scale_scores(sk, ta, -__builtin_inff(), 0, 1);
             for (int it = 0; it < its; ++it) {
                 step(it, ta, tb);
                 if constexpr (KBLK == 1) {
