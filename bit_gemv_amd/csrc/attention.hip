@@ -220,7 +220,8 @@ struct Schedule {
 // the tile's first 16 keys and the second half that of the others (zeros
 // elsewhere in p), and the two columns' outputs are added at the end. Half the
 // scores, exponentials and scales a lane: INT4 decode of 16 sequences (70B
-// heads) is bound by instructions, not bytes.
+// heads) is bound by instructions, not bytes (28 us; 22 for the loads alone).
+// Long contexts are bound by HBM: INT8 of 64 sequences, 1.42 GB in 216 us.
 template <int D, int BITS, bool SYM, int ROWS>
 struct Few {
     static constexpr int HALVES = 16 / ROWS;
@@ -663,13 +664,17 @@ __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void at
     }
 }
 
-// ---- many rows: 128 query rows share each key tile through LDS ----
+// ---- many rows: 128 or 256 query rows share each key tile through LDS ----
 //
 // W waves of 32 rows. Each key tile's codes are loaded once by the block (ahead
 // of their use), turned into fp16 once and laid out in LDS as the 32 x 32 x 16
 // matrix instruction reads them, so the conversion costs a 32 W-th of an
-// operation per row and code. Two blocks a CU (64 KB of LDS
-// each): one's softmax runs beside the other's products.
+// operation per row and code. Tiles of 128 rows leave room for two blocks a CU
+// (one's softmax beside the other's products), tiles of 256 for one. Two waves
+// a SIMD are what the registers allow, and a wave alone issues a vector
+// instruction every 5-12 cycles: the products (16 instructions of 32 cycles for
+// 32 keys of 32 rows) and the softmax (some 150) together are the bound, not
+// either rate: 539 us for a 2048-token chunk over 8192 (890 TFLOP/s).
 template <int D, int BITS, bool SYM, int W>
 struct Many {
     static constexpr int ROWS = 32 * W;
@@ -1288,8 +1293,8 @@ Plan plan_of(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int
         p.pass[0] = pass(n * group <= 8 ? 8 : 16);
     } else {
         // Tiles of 256 rows where a sequence fills them on the average (a
-        // 2048-token chunk of the 70B heads in tiles of 128: 646 us, of 256:
-        // 567), of 128 otherwise. In a batch of single tokens beside few chunks
+        // 2048-token chunk of the 70B heads in tiles of 128: 620 us, of 256:
+        // 539; ragged chunks of 64-wide heads 99 and 95), of 128 otherwise. In a batch of single tokens beside few chunks
         // (the others than the longest have few rows) the sequences of up to 16
         // rows go to the kernel for few rows in a launch of their own.
         p.pass[0] = pass(rows * group >= 256 * b && head_dim != 256 ? 256 : 128);

@@ -4,7 +4,8 @@
 // Per row: h = x + residual, r = (sum h^2 / k + eps)^-1/2, y = (h r) w,
 // s = max|y| / 127, q = round(y / s). The row is read once and stays in
 // registers over both reductions; the kernel is bound by HBM (2-4 bytes of x,
-// 2 x 2 of a bf16 residual and 1 of codes per element). The sum of squares is
+// 2 x 2 of a bf16 residual and 1 of codes per element; 8192 rows of 8192 from
+// fp32 107 us, 5.6 TB/s), a few rows by latency (one row 4.4 us). The sum of squares is
 // in fp64: products of fp32 values are exact there, so r is the correctly
 // rounded value whatever the order of the sum, and the codes follow the
 // definition bit for bit.
