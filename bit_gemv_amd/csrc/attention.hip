@@ -188,10 +188,12 @@ struct Schedule {
                 const int64_t start = readlane64(x.upto - x.all, src);
                 const uint32_t j = (uint32_t)uniform_div(pos - start, p.steps);
                 p.start = start + (int64_t)j * p.steps;
-                // tiles from both ends in turn: early rows see fewer keys, so
-                // neighbouring units together have about the same to do
+                // Early rows see fewer keys. Spans: tiles from both ends in turn,
+                // so that neighbouring units together have about the same to do.
+                // Whole units: the largest first, so that the last to start are
+                // short (a prompt of 4096, 501 us in turn, 398 so).
                 const uint32_t tiles = (uint32_t)uniform_div(readlane64(x.all, src), p.steps);
-                p.tile = j & 1 ? tiles - 1 - (j >> 1) : j >> 1;
+                p.tile = span.by_unit ? tiles - 1 - j : j & 1 ? tiles - 1 - (j >> 1) : j >> 1;
                 p.rows.begin = readlane64(x.rows.begin, src);
                 p.rows.n = readlane64(x.rows.n, src);
                 p.rows.first = readlane64(x.rows.first, src);
@@ -1265,14 +1267,29 @@ Pass pass_of(int row_tile, int64_t rows, int64_t group, int64_t heads, int64_t h
     const bool short_spans = likely * unit_steps * heads <= 32 * 512;
     const int64_t blocks = row_tile == 256 ? 256 : row_tile == 8 && head_dim <= 128 && short_spans ? 768 : 512;
     int64_t cap = (blocks + heads - 1) / heads;
-    // Blocks take whole units, and nothing is joined: chunks of many units, and
-    // decode batches of short contexts, which would spend longer on the second
-    // launch (a pass over spans and over units: 1 x 1003 tokens on one head 16.3
-    // and 12.1 us, 64 x 500 on 8 heads 20.9 and 13.7, 16 x 2000 on 8 heads 20.4
-    // and 17.7; 4 x 2000 on 8 heads 15.8 and 17.5).
-    p.by_unit = row_tile >= 128 ? units * heads >= (row_tile == 128 ? 2048 : 1024)
-                                : kv <= 1024 || (kv <= 2048 && likely * heads >= 128);
-    if (p.by_unit) cap = row_tile >= 128 ? units : likely;
+    // Blocks take whole units, and nothing is joined.
+    if (row_tile >= 128) {
+        // Chunks: cutting units costs about what 1200 more keys of each block do
+        // (parts written, read and joined, more first loads); whole units cost
+        // the last round's idle blocks, and at least the longest unit's time.
+        // Measured, 64 / 8 heads of 128, spans and units: prompts of 1100, 1800
+        // and 3000 83 and 55, 122 and 95, 257 and 223 us; 2048 over 8192 555 and
+        // 550; 1500 over 8192 (1.5 rounds) 462 and 505; 512 over 4096 113 and 146.
+        // Lengths other than the longest are not known here: half of it on the
+        // average, and short contexts before the rows only.
+        constexpr int64_t kCut = 1200;
+        const int64_t slots = row_tile == 256 || head_dim == 256 ? 256 : 512, load = likely * heads;
+        const int64_t mean = b == 1 ? kv - (n < kv ? n : kv) / 2 : kv / 2, prior = n < kv ? kv - n : 0;
+        const int64_t idle = (load + slots - 1) / slots * slots - load;
+        p.by_unit = load >= 4 * slots || (kv <= load * mean / slots + kCut && (b == 1 ? idle * prior <= kCut * slots : prior <= kCut));
+    } else {
+        // Decode batches of short contexts, which would spend longer on the
+        // second launch (a pass over spans and over units: 1 x 1003 tokens on one
+        // head 16.3 and 12.1 us, 64 x 500 on 8 heads 20.9 and 13.7, 16 x 2000 on
+        // 8 heads 20.4 and 17.7; 4 x 2000 on 8 heads 15.8 and 17.5).
+        p.by_unit = kv <= 1024 || (kv <= 2048 && likely * heads >= 128);
+    }
+    if (p.by_unit) cap = likely;
     // no more blocks than steps of work
     if (cap > units * unit_steps) cap = units * unit_steps;
     if (cap * heads > (1 << 22)) cap = (1 << 22) / heads;  // blocks that walk on, within the launch limits
