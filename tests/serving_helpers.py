@@ -23,7 +23,7 @@ class Batch:
     """Sequences (tokens held, new rows) over scattered pages. Table entries
     past a sequence's pages are out of the pool on purpose."""
 
-    def __init__(self, seqs, page, rng, spare=2, lead=0):
+    def __init__(self, seqs, page, rng, spare=2, lead=0, wide=0):
         self.kv = [s[0] for s in seqs]
         self.starts = [lead]
         for s in seqs:
@@ -32,7 +32,7 @@ class Batch:
         need = [(n + page - 1) // page for n in self.kv]
         self.pages = sum(need) + spare
         order, at = rng.permutation(self.pages), 0
-        wide = max(need + [1]) + 1
+        wide = max(need + [1, wide]) + 1
         self.table = np.where(rng.random((len(seqs), wide)) < 0.5, -1, 1 << 30).astype(np.int32)
         self.lists = []
         for i, n in enumerate(need):

@@ -18,9 +18,9 @@ SEQS = [(1, 1), (17, 1), (16, 16), (33, 5), (70, 70), (261, 3), (3, 6), (0, 2), 
 
 
 def _run(seqs, d, bits, sym, page=16, heads=2, group=4, seed=0, q_scale=1.0, k_scale=1.0, v_scale=1.0, gap=0, lead=0,
-         scale=None, hints=((0, 0),), what=""):
+         scale=None, hints=((0, 0),), what="", room=0):
     rng = np.random.default_rng(seed)
-    b = Batch(seqs, page, rng, lead=lead)
+    b = Batch(seqs, page, rng, lead=lead, wide=room // page)
     ref = new_cache(b, page, heads, d, bits, sym)
     fill(ref, b, rng, k_scale, v_scale)
     gpu = to_gpu(ref)
@@ -47,6 +47,16 @@ def _run(seqs, d, bits, sym, page=16, heads=2, group=4, seed=0, q_scale=1.0, k_s
 def test_formats(d, bits, sym):
     # bounds that choose each kernel: 256, 128, 16 and 8 rows a tile
     _run(SEQS, d, bits, sym, seed=d + bits, hints=((0, 0), (20, 0), (4, 261), (2, 0)))
+
+
+@pytest.mark.parametrize("bits,sym", FORMATS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_formats_cut_into_spans(d, bits, sym):
+    """A table wide enough for long contexts: every kernel cuts its work into
+    spans and joins the parts."""
+    seqs = [(40, 40), (300, 70), (3, 6), (0, 2), (500, 33), (40, 0)]
+    _run(seqs, d, bits, sym, seed=d + bits + 2, room=8192, hints=((70, 0), (4, 0), (2, 0)))
+    _run([(300, 200)], d, bits, sym, heads=1, group=8, seed=d + bits + 3, room=8192)
 
 
 @pytest.mark.parametrize("bits,sym", FORMATS)
@@ -130,7 +140,7 @@ def test_zeros_far_from_the_codes(bits, d):
     """Keys and values far from zero for their range (zeros of thousands), all
     alike (zeros of 1e8 and more) and on one side, among ordinary ones."""
     rng = np.random.default_rng(20)
-    b = Batch([(200, 40), (90, 3), (70, 1)], 16, rng)
+    b = Batch([(200, 40), (90, 3), (70, 1)], 16, rng, wide=512)
     ref = new_cache(b, 16, 1, d, bits, False)
     fill(ref, b, rng)
     for i, (held, every) in enumerate(((200, 5), (90, 1), (70, 33))):
@@ -143,7 +153,7 @@ def test_zeros_far_from_the_codes(bits, d):
                 ref.put_rows(*at, side, x)
     q = bf16(0.2 * rng.standard_normal((44, 5, d)))
     want, wl, bound = serving.attention(q, ref, b.lists, b.kv, b.starts, d ** -0.5)
-    for hints in ((0, 0), (40, 5000), (3, 5000), (1, 5000)):
+    for hints in ((0, 0), (40, 500), (40, 5000), (3, 5000), (1, 5000)):
         say(f"paged_attention far zeros bits={bits} d={d} hints {hints}")
         out = bg.paged_attention(dev_bf16f(q), to_gpu(ref), *b.on_gpu(), max_rows=hints[0], max_kv=hints[1])
         check_attention(out, None, want, wl, bound, f"far zeros {hints}")
@@ -176,7 +186,7 @@ def test_a_row_that_is_not_finite_changes_no_other(bad, bits, sym):
     """In tiles of 8, 16 and 128 rows, whole and in parts; a NaN reaches its
     row's result, split or not."""
     rng = np.random.default_rng(19)
-    b = Batch([(700, 3), (40, 30), (9, 1)], 16, rng)
+    b = Batch([(700, 3), (40, 30), (9, 1)], 16, rng, wide=512)
     ref = new_cache(b, 16, 1, 64, bits, sym)
     fill(ref, b, rng)
     q = bf16(rng.standard_normal((34, 4, 64)))
@@ -187,7 +197,7 @@ def test_a_row_that_is_not_finite_changes_no_other(bad, bits, sym):
         gq[r, h, 5 * i] = bad
     keep = np.ones((34, 4), bool)
     keep[tuple(np.array(hit).T)] = False
-    for hints in ((0, 0), (30, 5000), (3, 5000), (2, 5000)):
+    for hints in ((0, 0), (30, 700), (30, 5000), (3, 5000), (2, 5000), (2, 700)):
         say(f"paged_attention q {bad} bits={bits} hints {hints}")
         lse = torch.empty((34, 4), device="cuda")
         out = bg.paged_attention(gq, to_gpu(ref), *b.on_gpu(), max_rows=hints[0], max_kv=hints[1], lse=lse)

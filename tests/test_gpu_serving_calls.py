@@ -23,10 +23,10 @@ def _gen(seed):
     return torch.Generator(device="cuda").manual_seed(seed)
 
 
-def _setup(seqs, heads=2, group=4, d=128, bits=8, sym=True, page=16, seed=0):
+def _setup(seqs, heads=2, group=4, d=128, bits=8, sym=True, page=16, seed=0, wide=0):
     """A filled GPU cache of random codes, its batch and q."""
     rng = np.random.default_rng(seed)
-    b = Batch(seqs, page, rng)
+    b = Batch(seqs, page, rng, wide=wide)
     c = bg.KVCache.empty(b.pages, page, heads, d, bits, sym)
     g = _gen(seed)
     for t in (c.k_codes, c.v_codes):
@@ -67,11 +67,13 @@ def test_cache_graph(bits, sym):
 @pytest.mark.parametrize("seqs,hints", [
     ([(900, 1), (17, 1), (300, 1)], (1, 900)),       # whole sequences per block
     ([(5000, 1), (700, 1)], (1, 5000)),              # spans, joined
-    ([(700, 130), (260, 260)], (260, 700)),          # chunks, joined
-    ([(300, 200)] + [(90, 1)] * 6, (200, 300)),      # two launches of each kind
+    ([(700, 130), (260, 260)], (260, 700)),          # chunks, whole units
+    ([(700, 130), (260, 260)], (260, 8000)),         # chunks, joined
+    ([(300, 200)] + [(90, 1)] * 6, (200, 300)),      # two launches
+    ([(300, 200)] + [(90, 1)] * 6, (200, 8000)),     # two launches of each kind
 ])
 def test_attention_graph(seqs, hints):
-    b, c, q = _setup(seqs)
+    b, c, q = _setup(seqs, wide=512)
     out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
     batch = b.on_gpu()
     need = bg.paged_attention_workspace(b.rows, q.shape[1], c, len(seqs), batch[0].shape[1], *hints)
@@ -111,7 +113,7 @@ def test_two_graphs_and_growing_lengths():
 
 def test_other_streams_side_by_side():
     """The same calls on two streams at once give the bits of calls in order."""
-    sets = [_setup([(3000, 1), (500, 1)], seed=s) for s in (1, 2)] + [_setup([(400, 70)], seed=3)]
+    sets = [_setup([(3000, 1), (500, 1)], seed=s) for s in (1, 2)] + [_setup([(400, 70)], seed=3, wide=512)]
     xs = [torch.randn(64, 2048, device="cuda") for _ in range(2)]
     w = torch.ones(2048, device="cuda")
     want = [bg.paged_attention(q, c, *b.on_gpu()) for b, c, q in sets] + [bg.rms_norm_int8(x, w)[0] for x in xs]
@@ -150,7 +152,7 @@ def test_cache_and_attention_guard(d, bits, sym):
     """Pool tensors, read outputs, attention's output, lse and workspace, each
     between canaries, over every launch form."""
     lib, page, heads = bg.load_library(), 16, 2
-    b = Batch([(300, 20), (33, 1), (1300, 1), (5, 5), (40, 1)], page, np.random.default_rng(d), spare=0)
+    b = Batch([(300, 20), (33, 1), (1300, 1), (5, 5), (40, 1)], page, np.random.default_rng(d), spare=0, wide=512)
     row = d * bits // 8
     meta = (b.pages, heads, page)
     g = {"k_codes": Guarded((*meta, row), torch.uint8),
