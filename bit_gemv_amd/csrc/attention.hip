@@ -676,7 +676,7 @@ __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void at
 // a SIMD are what the registers allow, and a wave alone issues a vector
 // instruction every 5-12 cycles: the products (16 instructions of 32 cycles for
 // 32 keys of 32 rows) and the softmax (some 150) together are the bound, not
-// either rate: 539 us for a 2048-token chunk over 8192 (890 TFLOP/s).
+// either rate: 522 us for a 2048-token chunk over 8192 (920 TFLOP/s).
 template <int D, int BITS, bool SYM, int W>
 struct Many {
     static constexpr int ROWS = 32 * W;
@@ -1311,9 +1311,11 @@ Plan plan_of(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int
     } else {
         // Tiles of 256 rows where a sequence fills them on the average (a
         // 2048-token chunk of the 70B heads in tiles of 128: 620 us, of 256:
-        // 539; ragged chunks of 64-wide heads 99 and 95), of 128 otherwise. In a batch of single tokens beside few chunks
-        // (the others than the longest have few rows) the sequences of up to 16
-        // rows go to the kernel for few rows in a launch of their own.
+        // 539; ragged chunks of 64-wide heads 99 and 95), of 128 otherwise. In a
+        // batch of single tokens beside few chunks (the others than the longest
+        // have few rows) the sequences of up to 16 rows go to the kernel for few
+        // rows in a launch of their own (10 single tokens beside 2 chunks: 150
+        // us, 170 in one).
         p.pass[0] = pass(rows * group >= 256 * b && head_dim != 256 ? 256 : 128);
         if (b >= 4 && (rows - n) * group <= 64 * (b - 1)) {
             p.pass[0].least = 17;
