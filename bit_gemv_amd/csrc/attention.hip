@@ -676,7 +676,8 @@ __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void at
 // a SIMD are what the registers allow, and a wave alone issues a vector
 // instruction every 5-12 cycles: the products (16 instructions of 32 cycles for
 // 32 keys of 32 rows) and the softmax (some 150) together are the bound, not
-// either rate: 522 us for a 2048-token chunk over 8192 (920 TFLOP/s).
+// either rate: 522 to 557 us on different cards for a 2048-token chunk over 8192
+// (860 to 920 TFLOP/s).
 template <int D, int BITS, bool SYM, int W>
 struct Many {
     static constexpr int ROWS = 32 * W;
@@ -1185,11 +1186,11 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
 // two spans and key head, which takes the unit that lies across it if this is
 // the unit's first border. D / 4 lanes a row, four parts' loads in flight.
 template <int D, int ROWS, int STEP>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Span span) {
+LQ_DEVICE void join_parts(const AttnArgs &a, const Span &span, int block, int part, int parts_of_rows) {
     constexpr int W = D / 4, kTeams = 256 / W;
     const int lane = threadIdx.x & 63;
-    const int h = blockIdx.x % a.c.heads;
-    const int64_t border = blockIdx.x / a.c.heads + 1;
+    const int h = block % a.c.heads;
+    const int64_t border = block / a.c.heads + 1;
     const int group = a.q_heads / a.c.heads;
     const Schedule<STEP> sched(a.batch, span, a.c.page_shift, group, ROWS, lane);
     const int64_t all_steps = sched.total(), share = uniform_div(all_steps + span.cap - 1, span.cap);
@@ -1203,7 +1204,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Span span) {
     const KvRows &rows = p.rows;
     const uint32_t total = (uint32_t)rows.n * (uint32_t)group;
     const int c = threadIdx.x % W;
-    for (int r = blockIdx.y * kTeams + threadIdx.x / W; r < ROWS; r += kTeams * gridDim.y) {
+    for (int r = part * kTeams + threadIdx.x / W; r < ROWS; r += kTeams * parts_of_rows) {
         const uint32_t wr = p.tile * ROWS + r;
         if (wr >= total) break;
         auto slot = [&](int i) { return ((i == 0 ? slot0 : slot1 + 2 * (i - 1)) * a.c.heads + h) * ROWS + r; };
@@ -1232,6 +1233,22 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Span span) {
             u32x2{__builtin_bit_cast(uint32_t, b0), __builtin_bit_cast(uint32_t, b1)};
         if (c == 0 && a.lse) a.lse[at] = log_sum(mall, l);
     }
+}
+
+constexpr int kJoinY = 8;  // blocks that share a unit of many rows
+template <int D, int ROWS, int STEP>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Span span) {
+    join_parts<D, ROWS, STEP>(a, span, blockIdx.x, blockIdx.y, gridDim.y);
+}
+// Both launches' parts at once: `many` borders and heads of tiles of ROWS rows
+// (kJoinY blocks each), then those of 16-row tiles.
+template <int D, int ROWS, int STEP, int FEWSTEP>
+__global__ __launch_bounds__(256) void attn_join_both_kernel(AttnArgs a, Span span, Span few, int many) {
+    const int i = blockIdx.x;
+    if (i < many * kJoinY)
+        join_parts<D, ROWS, STEP>(a, span, i / kJoinY, i % kJoinY, kJoinY);
+    else
+        join_parts<D, 16, FEWSTEP>(a, few, i - many * kJoinY, 0, 1);
 }
 
 // One launch of a kernel (and of the join): the sequences it takes, its tile's
@@ -1314,8 +1331,8 @@ Plan plan_of(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int
         // 539; ragged chunks of 64-wide heads 99 and 95), of 128 otherwise. In a
         // batch of single tokens beside few chunks (the others than the longest
         // have few rows) the sequences of up to 16 rows go to the kernel for few
-        // rows in a launch of their own (10 single tokens beside 2 chunks: 150
-        // us, 170 in one).
+        // rows in a launch of their own (10 single tokens beside 2 chunks: 128
+        // us, 160 in one); one launch joins both kinds' parts (133 with two).
         p.pass[0] = pass(rows * group >= 256 * b && head_dim != 256 ? 256 : 128);
         if (b >= 4 && (rows - n) * group <= 64 * (b - 1)) {
             p.pass[0].least = 17;
@@ -1335,41 +1352,59 @@ int64_t attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, 
     return plan_of(rows, q_heads, heads, head_dim, b, max_pages * page_size, max_rows, max_kv).bytes;
 }
 
+static Span span_of(const AttnArgs &a, const Pass &p, char *workspace) {
+    float *o = reinterpret_cast<float *>(workspace);
+    return {o, o + (int64_t)2 * p.cap * a.c.heads * p.row_tile * a.c.head_dim, p.cap, p.by_unit, p.least, p.most};
+}
+static uint32_t borders_of(const AttnArgs &a, const Pass &p) {  // and key heads: blocks of the join
+    return p.by_unit ? 0 : (uint32_t)((p.cap - 1) * a.c.heads);
+}
+
 template <int D, int BITS, bool SYM, int ROWS>
-static hipError_t launch_tiles(const AttnArgs &a, const Pass &p, char *workspace, hipStream_t st) {
-    Span span{reinterpret_cast<float *>(workspace), nullptr, p.cap, p.by_unit, p.least, p.most};
-    span.ml = span.o + (int64_t)2 * p.cap * a.c.heads * ROWS * D;
+static hipError_t launch_tiles(const AttnArgs &a, const Pass &p, const Span &span, hipStream_t st) {
     const dim3 grid((uint32_t)(p.cap * a.c.heads));
-    constexpr int step = ROWS < 128 ? kFewStep : Many<D, BITS, SYM, ROWS / 32>::KT;
     if constexpr (ROWS < 128)
         hipLaunchKernelGGL((attn_few_kernel<D, BITS, SYM, ROWS, kFewWaves>), grid, dim3(64 * kFewWaves), 0, st, a, span);
     else
         hipLaunchKernelGGL((attn_many_kernel<D, BITS, SYM, ROWS / 32>), grid, dim3(2 * ROWS), 0, st, a, span);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.cap == 1 || p.by_unit) return e;
-    hipLaunchKernelGGL((attn_join_kernel<D, ROWS, step>), dim3((uint32_t)((p.cap - 1) * a.c.heads), ROWS < 128 ? 1 : 8),
-                       dim3(256), 0, st, a, span);
+    return hipGetLastError();
+}
+
+// The pass's kernel and the join; with `few`, the kernel for few rows between
+// them (its workspace behind the pass's own) and one join for both.
+template <int D, int BITS, bool SYM, int ROWS>
+static hipError_t launch_pass(const AttnArgs &a, const Pass &p, const Pass *few, hipStream_t st) {
+    char *ws = static_cast<char *>(a.workspace);
+    const Span span = span_of(a, p, ws);
+    hipError_t e = launch_tiles<D, BITS, SYM, ROWS>(a, p, span, st);
+    if (e != hipSuccess) return e;
+    const uint32_t borders = borders_of(a, p);
+    constexpr int step = ROWS < 128 ? kFewStep : Many<D, BITS, SYM, (ROWS < 128 ? 128 : ROWS) / 32>::KT;
+    if constexpr (ROWS >= 128) {
+        if (few) {
+            const Span small = span_of(a, *few, ws + p.bytes);
+            e = launch_tiles<D, BITS, SYM, 16>(a, *few, small, st);
+            const uint32_t blocks = borders * kJoinY + borders_of(a, *few);
+            if (e != hipSuccess || blocks == 0) return e;
+            hipLaunchKernelGGL((attn_join_both_kernel<D, ROWS, step, kFewStep>), dim3(blocks), dim3(256), 0, st, a, span,
+                               small, (int)borders);
+            return hipGetLastError();
+        }
+    }
+    if (borders == 0) return e;
+    hipLaunchKernelGGL((attn_join_kernel<D, ROWS, step>), dim3(borders, ROWS < 128 ? 1 : kJoinY), dim3(256), 0, st, a, span);
     return hipGetLastError();
 }
 
 template <int D, int BITS, bool SYM>
 static hipError_t launch_plan(const AttnArgs &a, const Plan &p, hipStream_t st) {
-    char *ws = static_cast<char *>(a.workspace);
-    for (int i = 0; i < p.passes; ++i) {
-        const Pass &q = p.pass[i];
-        hipError_t e;
-        if (q.row_tile == 8)
-            e = launch_tiles<D, BITS, SYM, 8>(a, q, ws, st);
-        else if (q.row_tile == 16)
-            e = launch_tiles<D, BITS, SYM, 16>(a, q, ws, st);
-        else if (D == 256 || q.row_tile == 128)
-            e = launch_tiles<D, BITS, SYM, 128>(a, q, ws, st);
-        else
-            e = launch_tiles<D, BITS, SYM, D == 256 ? 128 : 256>(a, q, ws, st);
-        if (e != hipSuccess) return e;
-        ws += q.bytes;
+    const Pass *few = p.passes == 2 ? &p.pass[1] : nullptr;
+    switch (p.pass[0].row_tile) {
+        case 8: return launch_pass<D, BITS, SYM, 8>(a, p.pass[0], nullptr, st);
+        case 16: return launch_pass<D, BITS, SYM, 16>(a, p.pass[0], nullptr, st);
+        case 128: return launch_pass<D, BITS, SYM, 128>(a, p.pass[0], few, st);
+        default: return launch_pass<D, BITS, SYM, D == 256 ? 128 : 256>(a, p.pass[0], few, st);
     }
-    return hipSuccess;
 }
 
 hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st) {
