@@ -464,10 +464,10 @@ typedef struct {
  * a page that is not in the pool are not written to the cache, read back as
  * zeros, and not attended to. Rows before row_starts[0] or from
  * row_starts[b] on are left as they were.
- * rows is the number of rows of the row tensors. max_rows (and max_kv) bound
- * the rows (the tokens held) of any one sequence; they size the launch and
- * choose the kernel, no result depends on their being exact or right (0:
- * not known).
+ * rows is the number of rows of the row tensors; b is at most 65535 and
+ * max_pages * page_size at most 2^30. max_rows (and max_kv) bound the rows
+ * (the tokens held) of any one sequence; they size the launch and choose the
+ * kernel, no result depends on their being exact or right (0: not known).
  *
  * kv_cache_write -- quantize the rows k, v [rows][heads][head_dim] of `type`
  * into their slots. k_stride and v_stride: elements from one row to the
@@ -503,8 +503,10 @@ lq_status kv_cache_read(const lq_kv_cache *cache, void *k, void *v, lq_dtype typ
  * Products run on fp16 MFMA with exact integer codes, q scaled by a power of
  * two for each row and head (exact down to 2^-30 of its largest element) and
  * weights p rounded to fp16; scales, sums and softmax statistics are fp32.
- * |q| up to 1e30, |scale q . k_hat| below 1e30; at most 2^30 tokens in a
- * sequence. A NaN in q makes its own row and head NaN (lse too) and no other.
+ * |q| up to 1e30, |scale q . k_hat| below 1e30; rows * q_heads below 2^31.
+ * Values whose scale is below 2^-17 of the largest in the sequence lose
+ * accuracy, below 2^-28 they count as nothing. A NaN in q makes its own row
+ * and head NaN (lse too) and no other.
  * workspace: at least paged_attention_workspace_bytes(...) bytes for the same
  * arguments (may be 0: then NULL is fine), 256-byte aligned, scratch: calls
  * that may overlap need one each.
