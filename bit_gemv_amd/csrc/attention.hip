@@ -1274,7 +1274,8 @@ Pass pass_of(int row_tile, int64_t rows, int64_t group, int64_t heads, int64_t h
     const int64_t tiles = (n * group + row_tile - 1) / row_tile;         // of a sequence
     const int64_t step = row_tile < 128 ? kFewStep : row_tile / (head_dim == 64 ? 2 : 4);
     // What the kernels' registers allow on 256 CUs: all blocks run at once, and
-    // more spans only repeat the fixed part. Single tokens' kernel (row_tile 8)
+    // more spans only repeat the fixed part (twice as many for many rows: 2 chunks
+    // beside single tokens 146 us, not 128; 64-wide heads 111, not 95). Single tokens' kernel (row_tile 8)
     // has room for three blocks a CU, which pays while spans are short and costs
     // a few per cent of HBM's rate when they are long (512, 768, 1024 blocks:
     // INT4 decode of 16 sequences up to 8192 tokens 30.6, 28.0, 33.5 us; INT8 of
