@@ -1335,9 +1335,12 @@ Plan plan_of(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int
         // rows in a launch of their own (10 single tokens beside 2 chunks: 128
         // us, 160 in one); one launch joins both kinds' parts (133 with two).
         p.pass[0] = pass(rows * group >= 256 * b && head_dim != 256 ? 256 : 128);
-        if (b >= 4 && (rows - n) * group <= 64 * (b - 1)) {
+        // That launch is sized by what such sequences can hold, one tile each: at
+        // most b units, however many rows the chunks have (39 beside a chunk of
+        // 300 on one head, 1500 tokens: 49.7 us, 60.6 by the chunk's rows).
+        if (b >= 4 && group <= 16 && (rows - n) * group <= 64 * (b - 1)) {
             p.pass[0].least = 17;
-            p.pass[1] = pass(16);
+            p.pass[1] = pass_of(16, 0, group, heads, head_dim, b, kv, 1);
             p.pass[1].most = 16;
             p.passes = 2;
         }
