@@ -537,7 +537,8 @@ class KVCache:
     paged_attention over the caller's tensors (layout: lq_kv_cache in
     libquant.h): codes uint8 k [pages][heads][page_size][row] and
     v [pages][heads][page_size / 4][row][4], row = head_dim * bits / 8; scales
-    and zeros fp32 [pages][heads][page_size] (zeros None: symmetric)."""
+    and zeros fp32 [pages][heads][page_size] (zeros None: symmetric). The
+    tensors and sizes are fixed; their contents are the caller's."""
 
     def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
                  k_zeros: Optional[torch.Tensor], v_zeros: Optional[torch.Tensor], head_dim: int, bits: int):
@@ -558,15 +559,30 @@ class KVCache:
         if k_zeros is not None:
             _on(index, k_zeros, "k_zeros", _F32, meta)
             _on(index, v_zeros, "v_zeros", _F32, meta)
-        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
-        self.k_zeros, self.v_zeros = k_zeros, v_zeros
-        self.pages, self.heads, self.page_size, self.head_dim = pages, heads, page_size, head_dim
-        self.bits, self.symmetric, self.device, self._index = bits, k_zeros is None, dev, index
-        self._record = _KvCacheRecord(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
-                                      None if k_zeros is None else k_zeros.data_ptr(), v_scales.data_ptr(),
-                                      None if v_zeros is None else v_zeros.data_ptr(), pages, page_size, heads,
-                                      head_dim, bits, int(k_zeros is None))
-        self._ref = ctypes.addressof(self._record)
+        record = _KvCacheRecord(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
+                                None if k_zeros is None else k_zeros.data_ptr(), v_scales.data_ptr(),
+                                None if v_zeros is None else v_zeros.data_ptr(), pages, page_size, heads, head_dim, bits,
+                                int(k_zeros is None))
+        self.__dict__.update(
+            k_codes=k_codes, v_codes=v_codes, k_scales=k_scales, v_scales=v_scales, k_zeros=k_zeros, v_zeros=v_zeros,
+            pages=pages, heads=heads, page_size=page_size, head_dim=head_dim, bits=bits, symmetric=k_zeros is None,
+            device=dev, _index=index, _record=record, _ref=ctypes.addressof(record))
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"a KVCache's {name} is fixed: make another KVCache over the other tensors")
+
+    def __delattr__(self, name):
+        self.__setattr__(name, None)
+
+    def _live(self) -> int:
+        """The record's address, as long as its tensors are where they were (not
+        resized, freed or pointed elsewhere in place)."""
+        r = self._record
+        if (self.k_codes.data_ptr() != r.k_codes or self.v_codes.data_ptr() != r.v_codes
+                or self.k_scales.data_ptr() != r.k_scales or self.v_scales.data_ptr() != r.v_scales
+                or not (self.symmetric or (self.k_zeros.data_ptr() == r.k_zeros and self.v_zeros.data_ptr() == r.v_zeros))):
+            raise ValueError("the KVCache's tensors have moved since it was made: make another")
+        return self._ref
 
     @classmethod
     def empty(cls, pages: int, page_size: int, heads: int, head_dim: int, bits: int = 8, symmetric: bool = True,
@@ -621,7 +637,7 @@ def kv_cache_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, block_table
     ks, vs = _rows(cache, k, "k", cache.heads), _rows(cache, v, "v", cache.heads)
     if v.shape != k.shape or v.dtype != k.dtype:
         raise ValueError("k and v must share shape and type")
-    _launch("kv_cache_write", cache._index, cache._ref, k.data_ptr(), v.data_ptr(), _dtype(k, "k"), k.shape[0], ks, vs,
+    _launch("kv_cache_write", cache._index, cache._live(), k.data_ptr(), v.data_ptr(), _dtype(k, "k"), k.shape[0], ks, vs,
             *_batch(cache._index, block_table, kv_lens, row_starts), max_rows)
 
 
@@ -641,7 +657,7 @@ def kv_cache_read(cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tens
         v = _empty(shape, steps, dtype=dtype, device=cache.device)
     else:
         _on(index, v, "v", dtype, shape)
-    _launch("kv_cache_read", index, cache._ref, k.data_ptr(), v.data_ptr(), _dtype(k, "k"), rows,
+    _launch("kv_cache_read", index, cache._live(), k.data_ptr(), v.data_ptr(), _dtype(k, "k"), rows,
             *_batch(index, block_table, kv_lens, row_starts), max_rows)
     return k, v
 
@@ -678,7 +694,7 @@ def paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     else:
         _on(index, workspace, "workspace", _U8, None)
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
-    _launch("paged_attention", index, cache._ref, q.data_ptr(), rows, q_heads, qs, d ** -0.5 if scale is None else scale,
+    _launch("paged_attention", index, cache._live(), q.data_ptr(), rows, q_heads, qs, d ** -0.5 if scale is None else scale,
             table, max_pages, lens, starts, b, max_rows, max_kv, ws_ptr, ws_bytes, out.data_ptr(),
             None if lse is None else lse.data_ptr())
     return out
