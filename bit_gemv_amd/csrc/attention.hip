@@ -1008,11 +1008,16 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
             }
             if (!SYM && ((flags0 | flags1) & C::kWideV)) {
                 // of the unrounded weights: they may vanish in fp16 where a tiny
-                // scale goes with a large zero
+                // scale goes with a large zero. Their reference is hidden from the
+                // compiler, which otherwise finds them equal to weigh's and moves
+                // all weights ahead of this branch, away from the products: 2048
+                // over 8192 tokens, 64 / 8 heads of 128, INT8 587 us, not 571.
+                float ref = mm;
+                asm volatile("" : "+v"(ref));
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int at = kb * 32 + 8 * (i / 4) + 4 * half + i % 4;
-                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(t[i], c1, -mm));
+                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(t[i], c1, -ref));
                     vz = __builtin_fmaf(p, b.meta[1][at] * b.meta[3][at], vz);
                 }
             }
@@ -1024,16 +1029,18 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
                 sv[r] = *reinterpret_cast<const f32x4 *>(&b.meta[1][kb * 32 + 16 * s + 8 * r + 4 * half]);
         };
         // The weights of t (block kb of tile b), their product with the values,
-        // the next block's scores u = keys kr . q, and (STORE) the tile x on its
-        // way to LDS, in one run of instructions without a branch, with the
-        // independent work side by side: JT groups of the first 16 keys' weights,
-        // each beside a score instruction; JT groups of the others', each beside a
-        // score and a value instruction; then the other value instructions
-        // beside the scaling of u (peak: its maximum) and the conversion of x. The
-        // 2048-token chunk takes 538 us so, 550 with the scaling and the sums of
-        // the weights after the run. (Holding the compiler to this order with
-        // scheduling barriers, or raising the wave's priority over it, changed
-        // nothing beyond noise.)
+        // the next block's scores u = keys kr . q, and (with_store) the tile x on
+        // its way to LDS, with the independent work side by side: JT groups of the
+        // first 16 keys' weights, each beside a score instruction; JT groups of the
+        // others', each beside a score and a value instruction; then the other
+        // value instructions beside the scaling of u (peak: its maximum) and the
+        // conversion of x. All of it is one run of instructions without a branch
+        // but for asymmetric tiles of 128- and 256-wide heads, where the zeros'
+        // part of store_meta, on half the lanes, comes between the weights and
+        // the last value instructions. The 2048-token chunk took 538 us so, 550
+        // with the scaling and the sums of the weights after the run. (Holding the
+        // compiler to this order with scheduling barriers, or raising the wave's
+        // priority over it, changed nothing beyond noise.)
         auto weigh = [&](const typename C::Buf &b, int kb, const f32x16 &t, const typename C::Buf &bn, int kn, f16x8 *kr,
                          f32x4 *sv, f32x16 &u, float &peak, bool with_store, typename C::Buf &to) {
             constexpr int EG = 8 / C::JT;  // weights of a group
