@@ -134,7 +134,10 @@ __global__ __launch_bounds__(TPB) void rms_norm_int8_kernel(const void *x, const
     ss = red_sum[0];
 #pragma unroll
     for (int i = 1; i < kWaves; ++i) ss += red_sum[i];
-    const float r = (float)(1.0 / sqrt(ss / (double)k + eps));
+    // with eps 0 a row of zeros, or of rms below 2^-128, has no fp32 r: the largest
+    // float stands for it, so that zeros stay zeros and nothing becomes NaN
+    float r = (float)(1.0 / sqrt(ss / (double)k + eps));
+    r = r > 3.402823466e+38f ? 3.402823466e+38f : r;
 
     // y in place of h
     auto scale_h = [&](int64_t c0) {

@@ -405,6 +405,7 @@ typedef enum { LQ_BF16 = 0, LQ_FP32 = 1 } lq_dtype;
  * rounded to fp32:
  *   h[j]  = x[j] + residual[j]                  (fp32; h = x without residual)
  *   r     = fp32((sum_j h[j]^2 / k + eps)^-1/2) (fp64 up to that rounding)
+ *           and at most the largest fp32 (eps 0: a row of zeros gives zeros)
  *   y[j]  = (h[j] * r) * weight[j]
  *   sx    = max(max_j |y[j]|, 1e-8) / 127
  *   qx[j] = clamp(round(y[j] / sx), -127, 127)

@@ -19,7 +19,8 @@ def rms_norm_int8(x, weight, eps, residual=None):
     y float32); fp32 roundings as defined, the sum of squares in fp64."""
     h = x.astype(F32) if residual is None else x.astype(F32) + residual.astype(F32)
     ss = (h.astype(np.float64) ** 2).sum(-1, keepdims=True)
-    r = (1.0 / np.sqrt(ss / x.shape[1] + eps)).astype(F32)
+    with np.errstate(divide="ignore", over="ignore"):
+        r = np.minimum((1.0 / np.sqrt(ss / x.shape[1] + eps)).astype(F32), np.finfo(F32).max)
     y = (h * r) * weight.astype(F32)
     sx = np.maximum(np.abs(y).max(-1, keepdims=True), F32(1e-8)) / F32(127)
     q = np.clip(np.rint(y / sx), -127, 127).astype(np.int8)
