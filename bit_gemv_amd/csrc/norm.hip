@@ -6,9 +6,10 @@
 // registers over both reductions; the kernel is bound by HBM (2-4 bytes of x,
 // 2 x 2 of a bf16 residual and 1 of codes per element; 8192 rows of 8192 from
 // fp32 107 us, 5.6 TB/s), a few rows by latency (one row 4.4 us). The sum of squares is
-// in fp64: products of fp32 values are exact there, so r is the correctly
-// rounded value whatever the order of the sum, and the codes follow the
-// definition bit for bit.
+// in fp64: products of fp32 values are exact there and a sum of k terms errs by
+// at most k 2^-53 of itself, so after its one rounding to fp32 r is the definition's
+// value unless that lies within 2^-39 (k = 8192) of the middle between two floats;
+// only there could another order of the sum give another last bit.
 #include "common.hpp"
 #include "launch.hpp"
 
