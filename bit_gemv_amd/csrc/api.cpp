@@ -139,7 +139,7 @@ lq_status check_kv(const char *fn, const lq_kv_cache *c, int64_t rows, const int
     if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
         return fail(LQ_ERR_UNSUPPORTED, "%s: page_size %lld (a power of two, 16 to 256)", fn, (long long)c->page_size);
     if (rows < 0 || b < 0 || max_pages < 0 || max_rows < 0) return fail(LQ_ERR_INVALID_ARG, "%s: negative size", fn);
-    if (c->pages > kMaxDim || c->heads > 65536 || rows > kMaxDim || max_pages > (int64_t(1) << 30) / c->page_size || b > 65535 ||
+    if (c->pages > kMaxDim || c->heads > 65536 || rows > kMaxDim || max_pages > lq::kMaxTokens / c->page_size || b > 65535 ||
         c->pages * c->heads > kMaxElems / (c->page_size * c->head_dim) || b * max_pages > kMaxElems ||
         rows > kMaxElems / (c->heads * c->head_dim))
         return fail(LQ_ERR_UNSUPPORTED, "%s: cache or batch too large", fn);
@@ -667,7 +667,7 @@ int64_t paged_attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t h
                                         int64_t max_pages, int64_t page_size, int64_t max_rows, int64_t max_kv) {
     if (rows < 0 || b < 0 || max_pages < 0 || max_rows < 0 || max_kv < 0 || q_heads <= 0 || heads <= 0 ||
         q_heads % heads || q_heads > 65536 || head_dim <= 0 || head_dim > 256 || page_size <= 0 || rows > kMaxDim ||
-        b > 65535 || max_pages > (int64_t(1) << 30) / page_size || rows > kMaxDim / q_heads)
+        b > 65535 || max_pages > lq::kMaxTokens / page_size || rows > kMaxDim / q_heads)
         return -1;
     if (rows == 0 || b == 0) return 0;
     return lq::attention_workspace_bytes(rows, q_heads, heads, head_dim, b, max_pages, page_size, max_rows, max_kv);

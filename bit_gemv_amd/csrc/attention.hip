@@ -89,11 +89,6 @@ LQ_DEVICE float max_halves16(float v) {
     const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
-// Lane exchanges inside rows of 16 that fold into the instruction using them.
-template <int CTRL>
-LQ_DEVICE float dpp_f32(float v) {
-    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
-}
 LQ_DEVICE float row_max(float v) {  // over 16 lanes
     v = fmaxf(v, dpp_f32<kDppXor1>(v));
     v = fmaxf(v, dpp_f32<kDppXor2>(v));
@@ -245,7 +240,6 @@ struct Few {
     static constexpr int OCC = D <= 128 && ROWS == 8 ? 3 : 2;
 };
 constexpr int kNoKey = 0x7FFFFF00;
-constexpr int64_t kMaxTokens = int64_t(1) << 30;  // of one sequence: keys are 32-bit
 
 // NT: streaming loads. The few-row kernel reads each code once (decode of 64
 // sequences, 1.42 GB: 247 us with the default policy, 221 us streaming); the

@@ -55,7 +55,12 @@ template <int CTRL>
 LQ_DEVICE float dpp_move(float v) {
     return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
 }
-
+// The same where every lane has a source: nothing to fill in, so that the move
+// folds into the instruction using it.
+template <int CTRL>
+LQ_DEVICE float dpp_f32(float v) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
+}
 
 // Raw buffer resource over [base, base + bytes) (gfx9 descriptor word 3).
 // Loads whose offset falls outside return zeros instead of faulting.

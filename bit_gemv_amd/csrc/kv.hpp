@@ -6,6 +6,8 @@
 
 namespace lq {
 
+constexpr int64_t kMaxTokens = int64_t(1) << 30;  // a table's room for one sequence: the kernels' keys are 32-bit
+
 struct KvCache {
     uint8_t *k_codes, *v_codes;
     float *k_scales, *k_zeros, *v_scales, *v_zeros;

@@ -41,10 +41,6 @@ LQ_DEVICE void widen_row8(const Raw<F32> &r, bool in, float *f) {
 }
 
 // Maximum over the team's W (8, 16 or 32) lanes.
-template <int CTRL>
-LQ_DEVICE float dpp_f32(float v) {
-    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
-}
 template <int W>
 LQ_DEVICE float lanes_max(float v) {
     v = fmaxf(v, dpp_f32<kDppXor1>(v));
