@@ -1266,7 +1266,8 @@ struct Plan {
 };
 constexpr int kFewWaves = 4, kFewStep = 32 * kFewWaves;
 
-Pass pass_of(int row_tile, int64_t rows, int64_t group, int64_t heads, int64_t head_dim, int64_t b, int64_t kv, int64_t n) {
+Pass pass_of(int row_tile, int64_t rows, int64_t group, int64_t heads, int64_t head_dim, int bits, int64_t b, int64_t kv,
+             int64_t n) {
     Pass p{};
     p.row_tile = row_tile;
     p.least = 1;
@@ -1276,15 +1277,18 @@ Pass pass_of(int row_tile, int64_t rows, int64_t group, int64_t heads, int64_t h
     const int64_t step = row_tile < 128 ? kFewStep : row_tile / (head_dim == 64 ? 2 : 4);
     // What the kernels' registers allow on 256 CUs: all blocks run at once, and
     // more spans only repeat the fixed part (twice as many for many rows: 2 chunks
-    // beside single tokens 146 us, not 128; 64-wide heads 111, not 95). Single tokens' kernel (row_tile 8)
-    // has room for three blocks a CU, which pays while spans are short and costs
-    // a few per cent of HBM's rate when they are long (512, 768, 1024 blocks:
-    // INT4 decode of 16 sequences up to 8192 tokens 30.6, 28.0, 33.5 us; INT8 of
-    // 64 up to 16384 215.7, 224.5, 228.8).
+    // beside single tokens 146 us, not 128; 64-wide heads 111, not 95). Single
+    // tokens' kernel (row_tile 8) has room for three blocks a CU. The third pays
+    // where a token's codes are few bytes, as the instructions per byte bound it
+    // then, and costs some of HBM's rate otherwise. 512 and 768 blocks, up to 8192
+    // tokens: INT4 of 128-wide heads, 8 sequences 25.5 and 24.9 us, 16 35.7 and
+    // 33.2, 64 89.4 and 83.0 (up to 16384 158 and 146); INT8 of 64-wide heads, 64
+    // sequences 30.0 and 27.9; INT8 of 128-wide heads, 16 sequences 42.7 and 43.4,
+    // 24 56.4 and 58.3, 64 124 and 125 (up to 16384 230 and 232).
     const int64_t unit_steps = (kv + step - 1) / step < 1 ? 1 : (kv + step - 1) / step;
     const int64_t likely = b * tiles < units ? b * tiles : units;
-    const bool short_spans = likely * unit_steps * heads <= 32 * 512;
-    const int64_t blocks = row_tile == 256 ? 256 : row_tile == 8 && head_dim <= 128 && short_spans ? 768 : 512;
+    const bool thin = head_dim <= 128 && head_dim * bits <= 512;  // up to 64 bytes
+    const int64_t blocks = row_tile == 256 ? 256 : row_tile == 8 && thin ? 768 : 512;
     int64_t cap = (blocks + heads - 1) / heads;
     // Blocks take whole units, and nothing is joined.
     if (row_tile >= 128) {
@@ -1317,13 +1321,13 @@ Pass pass_of(int row_tile, int64_t rows, int64_t group, int64_t heads, int64_t h
     return p;
 }
 
-Plan plan_of(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b, int64_t room, int64_t max_rows,
-             int64_t max_kv) {
+Plan plan_of(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int bits, int64_t b, int64_t room,
+             int64_t max_rows, int64_t max_kv) {
     Plan p{};
     const int64_t n = max_rows <= 0 || max_rows > rows ? rows : max_rows;
     const int64_t kv = max_kv <= 0 || max_kv > room ? room : max_kv;
     const int64_t group = q_heads / heads;
-    auto pass = [&](int row_tile) { return pass_of(row_tile, rows, group, heads, head_dim, b, kv, n); };
+    auto pass = [&](int row_tile) { return pass_of(row_tile, rows, group, heads, head_dim, bits, b, kv, n); };
     p.passes = 1;
     if (n * group <= 16) {
         p.pass[0] = pass(n * group <= 8 ? 8 : 16);
@@ -1341,7 +1345,7 @@ Plan plan_of(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int
         // 300 on one head, 1500 tokens: 49.7 us, 60.6 by the chunk's rows).
         if (b >= 4 && group <= 16 && (rows - n) * group <= 64 * (b - 1)) {
             p.pass[0].least = 17;
-            p.pass[1] = pass_of(16, 0, group, heads, head_dim, b, kv, 1);
+            p.pass[1] = pass_of(16, 0, group, heads, head_dim, bits, b, kv, 1);
             p.pass[1].most = 16;
             p.passes = 2;
         }
@@ -1354,7 +1358,8 @@ Plan plan_of(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int
 
 int64_t attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b,
                                   int64_t max_pages, int64_t page_size, int64_t max_rows, int64_t max_kv) {
-    return plan_of(rows, q_heads, heads, head_dim, b, max_pages * page_size, max_rows, max_kv).bytes;
+    // of either format: INT4's blocks are as many as INT8's or more
+    return plan_of(rows, q_heads, heads, head_dim, 4, b, max_pages * page_size, max_rows, max_kv).bytes;
 }
 
 static Span span_of(const AttnArgs &a, const Pass &p, char *workspace) {
@@ -1413,7 +1418,7 @@ static hipError_t launch_plan(const AttnArgs &a, const Plan &p, hipStream_t st) 
 }
 
 hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st) {
-    const Plan p = plan_of(a.batch.rows, a.q_heads, a.c.heads, a.c.head_dim, a.batch.b,
+    const Plan p = plan_of(a.batch.rows, a.q_heads, a.c.heads, a.c.head_dim, a.c.bits, a.batch.b,
                            a.batch.max_pages << a.c.page_shift, a.max_rows, a.max_kv);
 #define LQ_ATTN(D, BITS, SYM) \
     if (a.c.head_dim == D && a.c.bits == BITS && (a.c.symmetric != 0) == SYM) return launch_plan<D, BITS, SYM>(a, p, st);

@@ -39,7 +39,7 @@ class Pass:
                 f"{self.cap}, share {self.share}, cut {len(self.parts)}, second places {self.second}, longest piece {self.longest}")
 
 
-def forms(seqs, d, heads, group, room, max_rows, max_kv, rows):
+def forms(seqs, d, bits, heads, group, room, max_rows, max_kv, rows):
     """The launches of a call with these hints over `rows` rows, the workspace
     they need checked against the library's."""
     b = len(seqs)
@@ -51,7 +51,7 @@ def forms(seqs, d, heads, group, room, max_rows, max_kv, rows):
         units, tiles = ceil(rows * group, tile) + b, ceil(n * group, tile)
         step = FEW_STEP if tile < 128 else tile // (2 if d == 64 else 4)
         unit_steps, likely = max(1, ceil(kv, step)), min(b * tiles, units)
-        blocks = 256 if tile == 256 else 768 if tile == 8 and d <= 128 and likely * unit_steps * heads <= 32 * 512 else 512
+        blocks = lambda bits: 256 if tile == 256 else 768 if tile == 8 and d <= 128 and d * bits <= 512 else 512  # noqa: E731
         if tile >= 128:
             slots, load = (256 if tile == 256 or d == 256 else 512), likely * heads
             mean = kv - min(n, kv) // 2 if b == 1 else kv // 2
@@ -60,8 +60,8 @@ def forms(seqs, d, heads, group, room, max_rows, max_kv, rows):
                                             and (idle * prior <= 1200 * slots if b == 1 else prior <= 1200))
         else:
             by_unit = kv <= 1024 or (kv <= 2048 and likely * heads >= 128)
-        cap = min(likely if by_unit else ceil(blocks, heads), units * unit_steps)
-        need = 2 * cap * heads * tile * (d + 2) * 4 if cap > 1 and not by_unit else 0
+        cap, most_cap = (min(likely if by_unit else ceil(blocks(x), heads), units * unit_steps) for x in (bits, 4))
+        need = 2 * most_cap * heads * tile * (d + 2) * 4 if most_cap > 1 and not by_unit else 0
         return Pass(tile, step, cap, by_unit, least, most, seqs, group, room), ceil(need, 256) * 256
 
     if n * group <= 16:

@@ -52,9 +52,10 @@ def test_the_model_of_the_forms_is_the_librarys(d):
         if rows == 0:
             continue
         most, room = max(n for _, n in seqs), 16 * rng.choice([400, 700, 4096])
+        bits = rng.choice([4, 8])
         for max_rows in (0, most, 2 * most, 1):
             for max_kv in (0, max(h for h, _ in seqs), 1000):
-                for p in forms(seqs, d, heads, group, room, max_rows, max_kv, rows):
+                for p in forms(seqs, d, bits, heads, group, room, max_rows, max_kv, rows):
                     seen.add((p.tile, p.by_unit, p.share > 1, p.second > 0))
     for tile in (8, 16, 128) + ((256,) if d < 256 else ()):
         assert {(tile, True, False, False), (tile, False, True, True)} <= seen, (tile, seen)

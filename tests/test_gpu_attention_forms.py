@@ -65,7 +65,7 @@ def _run(seqs, d, bits, sym, heads, group, hints, form, room=ROOM, page=16, seed
     rng = np.random.default_rng(seed + d + bits)
     b = Batch(seqs, page, rng, lead=lead, wide=room // page - 1)
     rows, qh = b.rows + 1, heads * group
-    launches = forms(seqs, d, heads, group, b.table.shape[1] * page, *hints, rows)
+    launches = forms(seqs, d, bits, heads, group, b.table.shape[1] * page, *hints, rows)
     assert b.table.shape[1] * page == room
     assert form(launches), launches
     ref = _random_cache(b, page, heads, d, bits, sym, rng, far)
