@@ -1307,10 +1307,13 @@ Pass pass_of(int row_tile, int64_t rows, int64_t group, int64_t heads, int64_t h
         p.by_unit = load >= 4 * slots || (kv <= load * mean / slots + kCut && (b == 1 ? idle * prior <= kCut * slots : prior <= kCut));
     } else {
         // Decode batches of short contexts, which would spend longer on the
-        // second launch (a pass over spans and over units: 1 x 1003 tokens on one
-        // head 16.3 and 12.1 us, 64 x 500 on 8 heads 20.9 and 13.7, 16 x 2000 on
-        // 8 heads 20.4 and 17.7; 4 x 2000 on 8 heads 15.8 and 17.5).
-        p.by_unit = kv <= 1024 || (kv <= 2048 && likely * heads >= 128);
+        // second launch, and of up to 2048 tokens where units fill the card. Spans
+        // and units, INT8 of 128-wide heads: 1 x 1003 tokens on one head 16.8 and
+        // 12.2 us a pass, 64 x 500 on 8 heads 21.8 and 14.5; 4 x 2000 on 8 heads
+        // 16.2 and 22.2, 16 x 2000 19.8 and 23.4, 32 x 2000 27.0 and 25.1, 64 x
+        // 2000 41.3 and 39.7 (INT4 asymmetric: 16 18.2 and 24.1, 32 24.4 and 24.9,
+        // 64 35.2 and 30.7).
+        p.by_unit = kv <= 1024 || (kv <= 2048 && likely * heads >= 256);
     }
     if (p.by_unit) cap = likely;
     // no more blocks than steps of work

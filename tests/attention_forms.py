@@ -59,7 +59,7 @@ def forms(seqs, d, bits, heads, group, room, max_rows, max_kv, rows):
             by_unit = load >= 4 * slots or (kv <= load * mean // slots + 1200
                                             and (idle * prior <= 1200 * slots if b == 1 else prior <= 1200))
         else:
-            by_unit = kv <= 1024 or (kv <= 2048 and likely * heads >= 128)
+            by_unit = kv <= 1024 or (kv <= 2048 and likely * heads >= 256)
         cap, most_cap = (min(likely if by_unit else ceil(blocks(x), heads), units * unit_steps) for x in (bits, 4))
         need = 2 * most_cap * heads * tile * (d + 2) * 4 if most_cap > 1 and not by_unit else 0
         return Pass(tile, step, cap, by_unit, least, most, seqs, group, room), ceil(need, 256) * 256

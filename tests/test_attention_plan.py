@@ -28,6 +28,11 @@ def test_single_tokens_beside_a_chunk_are_cut_as_they_are_alone(chunk, own):
     assert _need(chunk + 3, 64, 8, 128, 4, 32768, chunk, kv) == own + _parts(min(64, steps), 8, 16, 128)
 
 
+@pytest.mark.parametrize("b,heads,whole", [(16, 8, False), (64, 2, False), (32, 8, True), (8, 32, True)])
+def test_decode_batches_of_up_to_2048_tokens_are_whole_where_units_fill_the_card(b, heads, whole):
+    assert (_need(b, 8 * heads, heads, 128, b, 2048, 1, 2000) == 0) == whole
+
+
 def test_groups_without_a_place_among_few_rows_take_one_launch():
     """A group of more than 16 heads has no sequence of up to 16 query rows."""
     d = 64
