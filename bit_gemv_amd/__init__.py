@@ -568,11 +568,18 @@ class KVCache:
             pages=pages, heads=heads, page_size=page_size, head_dim=head_dim, bits=bits, symmetric=k_zeros is None,
             device=dev, _index=index, _record=record, _ref=ctypes.addressof(record))
 
+    _FIXED = frozenset(("k_codes", "v_codes", "k_scales", "v_scales", "k_zeros", "v_zeros", "pages", "heads", "page_size",
+                        "head_dim", "bits", "symmetric", "device", "_index", "_record", "_ref"))
+
     def __setattr__(self, name, value):
-        raise AttributeError(f"a KVCache's {name} is fixed: make another KVCache over the other tensors")
+        if name in self._FIXED:
+            raise AttributeError(f"a KVCache's {name} is fixed: make another KVCache over the other tensors")
+        object.__setattr__(self, name, value)
 
     def __delattr__(self, name):
-        self.__setattr__(name, None)
+        if name in self._FIXED:
+            raise AttributeError(f"a KVCache's {name} is fixed")
+        object.__delattr__(self, name)
 
     def _live(self) -> int:
         """The record's address, as long as its tensors are where they were (not

@@ -53,3 +53,17 @@ def test_contents_may_change(cache):
     cache.k_codes.zero_()
     cache.k_scales.copy_(torch.rand(2, 1, 16))
     assert cache._live() == cache._ref
+
+
+def test_a_programs_own_attributes(cache):
+    cache.table = 3
+    assert cache.table == 3
+    del cache.table
+
+    class Named(bg.KVCache):
+        def __init__(self, *args):
+            super().__init__(*args)
+            self.name = "layer 1"
+
+    c = Named(cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales, cache.k_zeros, cache.v_zeros, 64, 8)
+    assert c.name == "layer 1" and c._live() == c._ref
