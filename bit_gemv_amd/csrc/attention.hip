@@ -132,7 +132,9 @@ struct Piece {
 };
 
 // One wave's view of all units: a lane a sequence, 64 at a time; the first 64
-// are kept.
+// are kept. Every piece is looked up from the first sequence on, which is little
+// beside a decode batch of 512 sequences (100 tokens each, 8 heads: 79 us) and
+// most of the time of one of 4096 (2135 us).
 template <int STEP>
 struct Schedule {
     struct Lane {

@@ -467,6 +467,11 @@ typedef struct {
  * max_pages * page_size at most 2^30. max_rows (and max_kv) bound the rows
  * (the tokens held) of any one sequence; they size the launch and choose the
  * kernel, no result depends on their being exact or right (0: not known).
+ * Lengths are added up on the device, by each block from the first sequence
+ * on: past about a thousand sequences time grows with the square of b, and a
+ * batch is better split (single tokens over 100 tokens each, 8 heads:
+ * paged_attention 79 us for 512, 212 for 1024, 2135 for 4096; kv_cache_write
+ * without max_rows 18, 42 and 403, with it 12, 14 and 25).
  *
  * kv_cache_write -- quantize the rows k, v [rows][heads][head_dim] of `type`
  * into their slots. k_stride and v_stride: elements from one row to the
