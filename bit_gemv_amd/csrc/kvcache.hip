@@ -55,35 +55,20 @@ LQ_DEVICE float lanes_max(float v) {
 }
 
 // Scale, zero and codes (stored unsigned) of the team's D elements, 8 in this
-// lane: quantize_groupwise's formulas with the head as the group, bit for bit.
-// The code is in the low byte of c. Quotients go through div_rn (common.hpp)
-// while every magnitude is at most 2^59: the range (or absmax) is then in
-// [1e-8, 2^60] and s in [1e-8 / 256, 2^60], so that a quotient x / s of 1/2 or
-// more has |x| >= s / 2 and every intermediate is normal; smaller ones round to
-// 0 either way. (The IEEE division sequence took the kernel from HBM's rate to
-// the instruction rate: 45 us for 21k tokens of the 70B heads; for the scale
-// alone it costs 1.3 us of 24 in INT4.)
-template <bool FAST>
-LQ_DEVICE float quotient(float a, float b, float y) {  // y = RN(1 / b)
-    return FAST ? div_rn(a, b, y) : a / b;
-}
-
+// lane: quantize_groupwise's formulas, except that the scale is the range
+// times the fp32 reciprocal of the level count, a multiplication (at most one
+// ulp from the quotient) in place of a division. The code is in the low byte
+// of c. Quotients x / s go through div_rn (common.hpp) while every magnitude
+// is at most 2^59: s is then in [1e-8 / 256, 2^60], so that a quotient of 1/2
+// or more has |x| >= s / 2 and every intermediate is normal; smaller ones
+// round to 0 either way. (The IEEE division sequence took the kernel from
+// HBM's rate to the instruction rate: 45 us for 21k tokens of the 70B heads.)
 template <int BITS, bool SYM, bool FAST>
-LQ_DEVICE void encode_range(const float *x, float lo, float hi, float &s, float &z, uint32_t *c) {
-    if constexpr (SYM) {  // hi: the absmax
-        constexpr float qmax = (float)((1 << (BITS - 1)) - 1);
-        s = quotient<FAST>(hi < kFloor ? kFloor : hi, qmax, 1.0f / qmax);
-        z = 0.0f;
-    } else {
-        constexpr float levels = (float)((1 << BITS) - 1);
-        const float range = hi - lo;
-        s = quotient<FAST>(range < kFloor ? kFloor : range, levels, 1.0f / levels);
-        z = rintf(-lo / s) + 0.0f;  // -0 -> +0
-    }
+LQ_DEVICE void codes8(const float *x, float s, float z, uint32_t *c) {
     const float y = 1.0f / s;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float q = quotient<FAST>(x[j], s, y);
+        const float q = FAST ? div_rn(x[j], s, y) : x[j] / s;
         if constexpr (SYM) {
             constexpr float mid = (float)(1 << (BITS - 1));
             // |q| <= (mid - 1)(1 + 2^-21), so no clamp is needed; floats from
@@ -99,14 +84,18 @@ LQ_DEVICE void encode_range(const float *x, float lo, float hi, float &s, float 
 template <int D, int BITS, bool SYM>
 LQ_DEVICE void encode8(const float *x, float &s, float &z, uint32_t *c) {
     constexpr int W = D / 8;
-    float lo = 0.0f, hi, top;  // top: largest magnitude
+    float top;  // largest magnitude
     if constexpr (SYM) {
+        constexpr float qmax = (float)((1 << (BITS - 1)) - 1);
         float a = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(x[j]));
-        top = hi = lanes_max<W>(a);
+        top = lanes_max<W>(a);
+        s = (top < kFloor ? kFloor : top) * (1.0f / qmax);
+        z = 0.0f;
     } else {
-        lo = x[0], hi = x[0];
+        constexpr float levels = (float)((1 << BITS) - 1);
+        float lo = x[0], hi = x[0];
 #pragma unroll
         for (int j = 1; j < 8; ++j) {
             lo = fminf(lo, x[j]);
@@ -114,12 +103,15 @@ LQ_DEVICE void encode8(const float *x, float &s, float &z, uint32_t *c) {
         }
         lo = -lanes_max<W>(-lo);
         hi = lanes_max<W>(hi);
+        const float range = hi - lo;
+        s = (range < kFloor ? kFloor : range) * (1.0f / levels);
+        z = rintf(-lo / s) + 0.0f;  // -0 -> +0
         top = fmaxf(fabsf(lo), fabsf(hi));
     }
     if (__all(top <= 5.76460752303423488e+17f))  // 2^59
-        encode_range<BITS, SYM, true>(x, lo, hi, s, z, c);
+        codes8<BITS, SYM, true>(x, s, z, c);
     else
-        encode_range<BITS, SYM, false>(x, lo, hi, s, z, c);
+        codes8<BITS, SYM, false>(x, s, z, c);
 }
 
 // four low bytes to a word

@@ -428,9 +428,11 @@ lq_status rms_norm_int8(const void *x, lq_dtype x_type, const void *residual, lq
  * paged_attention (W/A/KV notation: KV8 and KV4). A pool of `pages` pages
  * holds page_size tokens each for `heads` key/value heads of head_dim
  * elements. Each token and head has one scale (and one zero point when
- * asymmetric) for its key and one for its value: those that quantize_groupwise
- * gives with the head as the group. Codes are stored unsigned, symmetric ones
- * as q + 2^(bits - 1). With D = head_dim, e = element, o = token in page
+ * asymmetric) for its key and one for its value: quantize_groupwise's
+ * formulas with the head as the group, except that the scale is the range (or
+ * absmax) times the fp32 reciprocal of the level count, at most one ulp from
+ * their quotient. Codes are stored unsigned, symmetric ones as
+ * q + 2^(bits - 1). With D = head_dim, e = element, o = token in page
  * and row = D bytes (bits 8) or D / 2 (bits 4):
  *   k_codes [pages][heads][page_size][row]         bits 8: byte e;
  *           bits 4: byte e / 2, even elements in the low nibble

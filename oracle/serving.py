@@ -29,16 +29,17 @@ def rms_norm_int8(x, weight, eps, residual=None):
 
 def kv_quantize(x, bits, symmetric):
     """float32 [..., head_dim] -> (unsigned codes uint8, scale, zero or None): the
-    group quantizer's formulas with the head as the group."""
+    group quantizer's formulas with the scale as a product with the rounded
+    reciprocal of the level count."""
     x = x.astype(F32)
     if symmetric:
         qmax = F32(2 ** (bits - 1) - 1)
-        s = np.maximum(np.abs(x).max(-1), F32(1e-8)) / qmax
+        s = np.maximum(np.abs(x).max(-1), F32(1e-8)) * (F32(1) / qmax)
         q = np.clip(np.rint(x / s[..., None]), -qmax, qmax) + F32(2 ** (bits - 1))
         return q.astype(np.uint8), s, None
     top = F32(2 ** bits - 1)
     lo, hi = x.min(-1), x.max(-1)
-    s = np.maximum(hi - lo, F32(1e-8)) / top
+    s = np.maximum(hi - lo, F32(1e-8)) * (F32(1) / top)
     z = np.rint(-lo / s) + F32(0)
     q = np.clip(np.rint(x / s[..., None]) + z[..., None], 0, top)
     return q.astype(np.uint8), s, z
