@@ -56,9 +56,11 @@ LQ_DEVICE float lanes_max(float v) {
 
 // Scale, zero and codes (stored unsigned) of the team's D elements, 8 in this
 // lane: quantize_groupwise's formulas, except that the scale is the range
-// times the fp32 reciprocal of the level count, a multiplication (at most one
-// ulp from the quotient) in place of a division. The code is in the low byte
-// of c. Quotients x / s go through div_rn (common.hpp) while every magnitude
+// times the fp32 reciprocal of the level count, at most one ulp from the
+// quotient. That is how torch divides a GPU tensor by a number, so the cache
+// holds what the formulas written in torch give, bit for bit; the quotient
+// (no slower through div_rn) puts a code or a zero one off from theirs where
+// its rounding lies within that ulp. The code is in the low byte of c. Quotients x / s go through div_rn (common.hpp) while every magnitude
 // is at most 2^59: s is then in [1e-8 / 256, 2^60], so that a quotient of 1/2
 // or more has |x| >= s / 2 and every intermediate is normal; smaller ones
 // round to 0 either way. (The IEEE division sequence took the kernel from

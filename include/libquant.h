@@ -431,7 +431,8 @@ lq_status rms_norm_int8(const void *x, lq_dtype x_type, const void *residual, lq
  * asymmetric) for its key and one for its value: quantize_groupwise's
  * formulas with the head as the group, except that the scale is the range (or
  * absmax) times the fp32 reciprocal of the level count, at most one ulp from
- * their quotient. Codes are stored unsigned, symmetric ones as
+ * their quotient (torch divides a GPU tensor by a number so: the formulas in
+ * torch give the same bits). Codes are stored unsigned, symmetric ones as
  * q + 2^(bits - 1). With D = head_dim, e = element, o = token in page
  * and row = D bytes (bits 8) or D / 2 (bits 4):
  *   k_codes [pages][heads][page_size][row]         bits 8: byte e;
