@@ -672,8 +672,8 @@ __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void at
 // a SIMD are what the registers allow, and a wave alone issues a vector
 // instruction every 5-12 cycles: the products (16 instructions of 32 cycles for
 // 32 keys of 32 rows) and the softmax (some 150) together are the bound, not
-// either rate: 522 to 557 us on different cards for a 2048-token chunk over 8192
-// (860 to 920 TFLOP/s).
+// either rate: 522 to 626 us on different cards for a 2048-token chunk over 8192
+// (770 to 920 TFLOP/s).
 template <int D, int BITS, bool SYM, int W>
 struct Many {
     static constexpr int ROWS = 32 * W;
@@ -1298,8 +1298,10 @@ Pass pass_of(int row_tile, int64_t rows, int64_t group, int64_t heads, int64_t h
         // (parts written, read and joined, more first loads); whole units cost
         // the last round's idle blocks, and at least the longest unit's time.
         // Measured, 64 / 8 heads of 128, spans and units: prompts of 1100, 1800
-        // and 3000 83 and 55, 122 and 95, 257 and 223 us; 2048 over 8192 555 and
-        // 550; 1500 over 8192 (1.5 rounds) 462 and 505; 512 over 4096 113 and 146.
+        // and 3000 85 and 57, 125 and 97, 263 and 225 us; 2048 over 8192 581 and
+        // 579; 1500 over 8192 (1.5 rounds) 484 and 519; 512 over 4096 107 and 139;
+        // two prompts of 4000 703 and 631; four ragged chunks of up to 1000 over
+        // up to 4000 349 and 381, of 700 over 3000 218 and 200 (spans are taken).
         // Lengths other than the longest are not known here: half of it on the
         // average, and short contexts before the rows only.
         constexpr int64_t kCut = 1200;
