@@ -60,11 +60,12 @@ LQ_DEVICE float lanes_max(float v) {
 // quotient. That is how torch divides a GPU tensor by a number, so the cache
 // holds what the formulas written in torch give, bit for bit; the quotient
 // (no slower through div_rn) puts a code or a zero one off from theirs where
-// its rounding lies within that ulp. The code is in the low byte of c. Quotients x / s go through div_rn (common.hpp) while every magnitude
-// is at most 2^59: s is then in [1e-8 / 256, 2^60], so that a quotient of 1/2
-// or more has |x| >= s / 2 and every intermediate is normal; smaller ones
-// round to 0 either way. (The IEEE division sequence took the kernel from
-// HBM's rate to the instruction rate: 45 us for 21k tokens of the 70B heads.)
+// its rounding lies within that ulp. The code is in the low byte of c.
+// Quotients x / s go through div_rn (common.hpp) while every magnitude is at
+// most 2^59: s is then in [1e-8 / 256, 2^60], so that a quotient of 1/2 or more
+// has |x| >= s / 2 and every intermediate is normal; smaller ones round to 0
+// either way. (The IEEE division sequence took the kernel from HBM's rate to
+// the instruction rate: 45 us for 21k tokens of the 70B heads.)
 template <int BITS, bool SYM, bool FAST>
 LQ_DEVICE void codes8(const float *x, float s, float z, uint32_t *c) {
     const float y = 1.0f / s;
