@@ -28,7 +28,8 @@ LQ_OK, LQ_ERR_INVALID_ARG, LQ_ERR_UNSUPPORTED, LQ_ERR_HIP, LQ_ERR_NO_DEVICE = ra
 ENTRY_POINTS = ("quantize_groupwise", "dequantize_groupwise", "w4a16_gemv", "w8a16_gemv", "w4a16_gemm",
                 "smooth_scale", "quant_per_token_int8", "w8a8_gemm", "act_absmean", "awq_search",
                 "mxfp4_quantize", "mxfp4_gemv", "mxfp4_gemm", "gptq_hessian_factor", "gptq_quantize",
-                "rms_norm_int8", "kv_cache_write", "kv_cache_read", "paged_attention")
+                "rms_norm_int8", "kv_cache_write", "kv_cache_read", "paged_attention", "cross_attention",
+                "prefix_attention")
 
 
 class LibquantError(RuntimeError):
@@ -75,6 +76,8 @@ def load_library(path: Optional[str] = None):
         "kv_cache_write": [P, P, P, I, I64, I64, I64, P, I64, P, P, I64, I64, P],
         "kv_cache_read": [P, P, P, I, I64, P, I64, P, P, I64, I64, P],
         "paged_attention": [P, P, I64, I64, I64, F, P, I64, P, P, I64, I64, I64, P, I64, P, P, P],
+        "cross_attention": [P, P, I64, I64, I64, F, P, I64, P, P, I64, I64, I64, P, I64, P, P, P],
+        "prefix_attention": [P, P, I64, I64, I64, F] + [P, I64, P, P, I64, I64, I64] * 2 + [P, I64, P, P, P],
     }
     for name, argtypes in sigs.items():
         fn = getattr(lib, name)
@@ -93,6 +96,10 @@ def load_library(path: Optional[str] = None):
     lib.gptq_quantize_noalloc_max_bytes.restype = ctypes.c_int64
     lib.paged_attention_workspace_bytes.argtypes = [I64] * 9
     lib.paged_attention_workspace_bytes.restype = ctypes.c_int64
+    lib.cross_attention_workspace_bytes.argtypes = [I64] * 9
+    lib.cross_attention_workspace_bytes.restype = ctypes.c_int64
+    lib.prefix_attention_workspace_bytes.argtypes = [I64] * 13
+    lib.prefix_attention_workspace_bytes.restype = ctypes.c_int64
     lib.lq_read_probe_sink_words.argtypes = []
     lib.lq_read_probe_sink_words.restype = ctypes.c_int64
     lib.lq_hbm_read_probe.argtypes = [P, I64, P, P]
@@ -714,4 +721,99 @@ def paged_attention_workspace(rows: int, q_heads: int, cache: KVCache, b: int, m
                                                           cache.page_size, max_rows, max_kv)
     if need < 0:
         raise LibquantError(LQ_ERR_INVALID_ARG, "paged_attention", "sizes out of range")
+    return need
+
+
+def _attention(name: str, q, cache: KVCache, block_table, kv_lens, row_starts, scale, max_rows: int, max_kv: int, out, lse,
+               workspace, prefix: tuple = (), prefix_sizes: tuple = ()) -> torch.Tensor:
+    """cross_attention, or with `prefix` (its further arguments; prefix_sizes: those
+    that its workspace depends on) prefix_attention."""
+    qs = _rows(cache, q, "q", None)
+    if q.dtype is not _BF16:
+        raise TypeError(f"q must be {_BF16}, got {q.dtype}")
+    shape = rows, q_heads, d = q.shape
+    index = cache._index
+    table, max_pages, lens, starts, b = _batch(index, block_table, kv_lens, row_starts)
+    if out is None:
+        out = _empty(shape, (q_heads * d, d, 1), dtype=_BF16, device=cache.device)
+    else:
+        _on(index, out, "out", _BF16, shape)
+    if lse is not None:
+        _on(index, lse, "lse", _F32, (rows, q_heads))
+    ws_ptr, ws_bytes = None, 0
+    if workspace is None:
+        lib = _lib or load_library()
+        if prefix:
+            ws_bytes = lib.prefix_attention_workspace_bytes(rows, q_heads, cache.heads, d, cache.page_size, *prefix_sizes, b,
+                                                            max_pages, max_rows, max_kv)
+        else:
+            ws_bytes = lib.cross_attention_workspace_bytes(rows, q_heads, cache.heads, d, b, max_pages, cache.page_size,
+                                                           max_rows, max_kv)
+        if ws_bytes > 0:
+            workspace = _empty((ws_bytes,), (1,), dtype=_U8, device=cache.device)
+            ws_ptr = workspace.data_ptr()
+    else:
+        _on(index, workspace, "workspace", _U8, None)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
+    _launch(name, index, cache._live(), q.data_ptr(), rows, q_heads, qs, d ** -0.5 if scale is None else scale, *prefix,
+            table, max_pages, lens, starts, b, max_rows, max_kv, ws_ptr, ws_bytes, out.data_ptr(),
+            None if lse is None else lse.data_ptr())
+    return out
+
+
+def cross_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                    row_starts: torch.Tensor, scale: Optional[float] = None, max_rows: int = 0, max_kv: int = 0,
+                    out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of the rows q over all kv_lens[i] tokens of their sequences (a
+    decoder's rows over an encoder's states): rows row_starts[i] ..
+    row_starts[i + 1] - 1 are sequence i's and no tokens of it. Arguments as
+    paged_attention; workspace: of at least cross_attention_workspace(...) bytes."""
+    return _attention("cross_attention", q, cache, block_table, kv_lens, row_starts, scale, max_rows, max_kv, out, lse,
+                      workspace)
+
+
+def cross_attention_workspace(rows: int, q_heads: int, cache: KVCache, b: int, max_pages: int, max_rows: int = 0,
+                              max_kv: int = 0) -> int:
+    """Bytes of workspace cross_attention needs for these sizes."""
+    need = load_library().cross_attention_workspace_bytes(rows, q_heads, cache.heads, cache.head_dim, b, max_pages,
+                                                          cache.page_size, max_rows, max_kv)
+    if need < 0:
+        raise LibquantError(LQ_ERR_INVALID_ARG, "cross_attention", "sizes out of range")
+    return need
+
+
+def prefix_attention(q: torch.Tensor, cache: KVCache, prefix_table: torch.Tensor, prefix_lens: torch.Tensor,
+                     prefix_row_starts: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                     row_starts: torch.Tensor, scale: Optional[float] = None, max_prefix_rows: int = 0, max_prefix: int = 0,
+                     max_rows: int = 0, max_kv: int = 0, out: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """paged_attention of sequences that share prefixes, each prefix read once:
+    rows prefix_row_starts[i] .. prefix_row_starts[i + 1] - 1 see the
+    prefix_lens[i] tokens in prefix_table[i]'s pages, and then their own
+    sequence's, whose kv_lens and block_table hold the tokens behind the prefix
+    only. max_prefix_rows and max_prefix bound any one prefix's rows and tokens,
+    if known. Arguments otherwise as paged_attention; workspace: of at least
+    prefix_attention_workspace(...) bytes."""
+    if not isinstance(prefix_table, torch.Tensor) or prefix_table.dim() != 2:
+        raise ValueError("prefix_table must be a tensor [p][prefix_pages]")
+    index = cache._index
+    p, pages = prefix_table.shape
+    _on(index, prefix_table, "prefix_table", _I32, None)
+    _on(index, prefix_lens, "prefix_lens", _I32, (p,))
+    _on(index, prefix_row_starts, "prefix_row_starts", _I32, (p + 1,))
+    prefix = (prefix_table.data_ptr(), pages, prefix_lens.data_ptr(), prefix_row_starts.data_ptr(), p, max_prefix_rows,
+              max_prefix)
+    return _attention("prefix_attention", q, cache, block_table, kv_lens, row_starts, scale, max_rows, max_kv, out, lse,
+                      workspace, prefix, (p, pages, max_prefix_rows, max_prefix))
+
+
+def prefix_attention_workspace(rows: int, q_heads: int, cache: KVCache, p: int, prefix_pages: int, b: int, max_pages: int,
+                               max_prefix_rows: int = 0, max_prefix: int = 0, max_rows: int = 0, max_kv: int = 0) -> int:
+    """Bytes of workspace prefix_attention needs for these sizes."""
+    need = load_library().prefix_attention_workspace_bytes(rows, q_heads, cache.heads, cache.head_dim, cache.page_size, p,
+                                                           prefix_pages, max_prefix_rows, max_prefix, b, max_pages, max_rows,
+                                                           max_kv)
+    if need < 0:
+        raise LibquantError(LQ_ERR_INVALID_ARG, "prefix_attention", "sizes out of range")
     return need

@@ -663,51 +663,74 @@ lq_status kv_cache_read(const lq_kv_cache *cache, void *k, void *v, lq_dtype typ
     return launched(lq::launch_kv_read(a, static_cast<hipStream_t>(stream)), fn);
 }
 
-int64_t paged_attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b,
-                                        int64_t max_pages, int64_t page_size, int64_t max_rows, int64_t max_kv) {
-    if (rows < 0 || b < 0 || max_pages < 0 || max_rows < 0 || max_kv < 0 || q_heads <= 0 || heads <= 0 ||
-        q_heads % heads || q_heads > 65536 || head_dim <= 0 || head_dim > 256 || page_size <= 0 || rows > kMaxDim ||
-        b > 65535 || max_pages > lq::kMaxTokens / page_size || rows > kMaxDim / q_heads)
-        return -1;
-    if (rows == 0 || b == 0) return 0;
-    return lq::attention_workspace_bytes(rows, q_heads, heads, head_dim, b, max_pages, page_size, max_rows, max_kv);
+namespace {
+
+// Sizes for which an attention call's workspace has a size; false: refused.
+bool attention_sizes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b, int64_t max_pages,
+                     int64_t page_size, int64_t max_rows, int64_t max_kv) {
+    return !(rows < 0 || b < 0 || max_pages < 0 || max_rows < 0 || max_kv < 0 || q_heads <= 0 || heads <= 0 ||
+             q_heads % heads || q_heads > 65536 || head_dim <= 0 || head_dim > 256 || page_size <= 0 || rows > kMaxDim ||
+             b > 65535 || max_pages > lq::kMaxTokens / page_size || rows > kMaxDim / q_heads);
 }
 
-lq_status paged_attention(const lq_kv_cache *cache, const void *q_bf16, int64_t rows, int64_t q_heads,
-                          int64_t q_stride, float scale, const int32_t *block_table, int64_t max_pages,
-                          const int32_t *kv_lens, const int32_t *row_starts, int64_t b, int64_t max_rows,
-                          int64_t max_kv, void *workspace, int64_t workspace_bytes, void *out_bf16, float *lse,
-                          void *stream) {
-    const char *fn = "paged_attention";
-    lq::AttnArgs a{};
-    lq_status st = check_kv(fn, cache, rows, block_table, max_pages, kv_lens, row_starts, b, max_rows, &a.c, &a.batch);
-    if (st != LQ_OK) return st;
-    if (max_kv < 0) return fail(LQ_ERR_INVALID_ARG, "%s: negative size", fn);
-    if (q_heads <= 0 || q_heads % cache->heads)
-        return fail(LQ_ERR_INVALID_ARG, "%s: q_heads (%lld) is not a multiple of heads (%lld)", fn, (long long)q_heads,
-                    (long long)cache->heads);
-    if (!(scale > -1e30f && scale < 1e30f)) return fail(LQ_ERR_INVALID_ARG, "%s: scale not finite", fn);
-    if (rows == 0 || b == 0) return LQ_OK;
-    const int64_t d = cache->head_dim, width = q_heads * d;
-    if (q_heads > 65536 || rows > kMaxDim / q_heads) return fail(LQ_ERR_UNSUPPORTED, "%s: q too large", fn);
+// rows that see a whole sequence stand behind its last token: their positions
+// are 32-bit
+constexpr int64_t kMaxWholeRows = int64_t(1) << 30;
+
+// What the attention calls check alike, the caches's and the batch's checks done:
+// q, scale, outputs and, with `need` bytes of it, the workspace, which together
+// may overlap neither the inputs nor `more`.
+lq_status check_attention(const char *fn, const lq_kv_cache *cache, const void *q_bf16, int64_t q_stride, int64_t need,
+                          const void *workspace, int64_t workspace_bytes, const void *out_bf16, const float *lse,
+                          const Range (&more)[3], const lq::AttnArgs &a) {
+    const int64_t d = cache->head_dim, width = a.q_heads * d, rows = a.batch.rows;
     if (q_stride < width || q_stride % 8)
         return fail(LQ_ERR_INVALID_ARG, "%s: q_stride must be a multiple of 8 and at least q_heads * head_dim", fn);
     if (q_stride > kMaxElems / rows) return fail(LQ_ERR_UNSUPPORTED, "%s: q_stride too large", fn);
     if (!q_bf16 || !aligned(q_bf16, 16)) return fail(LQ_ERR_INVALID_ARG, "%s: q null or not 16-byte aligned", fn);
     if (!out_bf16 || !aligned(out_bf16, 16)) return fail(LQ_ERR_INVALID_ARG, "%s: out null or not 16-byte aligned", fn);
     if (!aligned(lse, 4)) return fail(LQ_ERR_INVALID_ARG, "%s: lse misaligned", fn);
-    const int64_t need = lq::attention_workspace_bytes(rows, q_heads, cache->heads, d, b, max_pages, cache->page_size,
-                                                       max_rows, max_kv);
     if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
         return fail(LQ_ERR_INVALID_ARG, "%s: workspace null, not 256-byte aligned or smaller than %lld bytes", fn,
                     (long long)need);
     const int64_t codes = kv_code_bytes(cache), meta = kv_meta_bytes(cache), zeros = cache->symmetric ? 0 : meta;
-    if (any_overlap({{out_bf16, rows * width * 2}, {lse, lse ? rows * q_heads * 4 : 0}, {workspace, need}},
+    const lq::KvBatch &bt = a.batch;
+    if (any_overlap({{out_bf16, rows * width * 2}, {lse, lse ? rows * a.q_heads * 4 : 0}, {workspace, need}},
                     {{q_bf16, ((rows - 1) * q_stride + width) * 2}, {cache->k_codes, codes}, {cache->v_codes, codes},
                      {cache->k_scales, meta}, {cache->v_scales, meta}, {cache->k_zeros, zeros}, {cache->v_zeros, zeros},
-                     {block_table, b * max_pages * 4}, {kv_lens, b * 4}, {row_starts, (b + 1) * 4}}))
+                     {bt.table, bt.b * bt.max_pages * 4}, {bt.lens, bt.b * 4}, {bt.starts, (bt.b + 1) * 4}, more[0],
+                     more[1], more[2]}))
         return fail(LQ_ERR_INVALID_ARG, "%s: an output overlaps an input or another output", fn);
-    if ((st = need_device()) != LQ_OK) return st;
+    return need_device();
+}
+
+lq_status check_heads(const char *fn, const lq_kv_cache *cache, int64_t q_heads, float scale) {
+    if (q_heads <= 0 || q_heads % cache->heads)
+        return fail(LQ_ERR_INVALID_ARG, "%s: q_heads (%lld) is not a multiple of heads (%lld)", fn, (long long)q_heads,
+                    (long long)cache->heads);
+    if (!(scale > -1e30f && scale < 1e30f)) return fail(LQ_ERR_INVALID_ARG, "%s: scale not finite", fn);
+    return LQ_OK;
+}
+
+lq_status check_rows(const char *fn, int64_t rows, int64_t q_heads, bool whole) {
+    if (q_heads > 65536 || rows > kMaxDim / q_heads) return fail(LQ_ERR_UNSUPPORTED, "%s: q too large", fn);
+    if (whole && rows > kMaxWholeRows) return fail(LQ_ERR_UNSUPPORTED, "%s: more than 2^30 rows", fn);
+    return LQ_OK;
+}
+
+// paged_attention and cross_attention: one batch, causal or whole.
+lq_status attention(const char *fn, bool whole, const lq_kv_cache *cache, const void *q_bf16, int64_t rows, int64_t q_heads,
+                    int64_t q_stride, float scale, const int32_t *block_table, int64_t max_pages, const int32_t *kv_lens,
+                    const int32_t *row_starts, int64_t b, int64_t max_rows, int64_t max_kv, void *workspace,
+                    int64_t workspace_bytes, void *out_bf16, float *lse, void *stream) {
+    lq::AttnArgs a{};
+    lq_status st = check_kv(fn, cache, rows, block_table, max_pages, kv_lens, row_starts, b, max_rows, &a.c, &a.batch);
+    if (st != LQ_OK) return st;
+    if (max_kv < 0) return fail(LQ_ERR_INVALID_ARG, "%s: negative size", fn);
+    if ((st = check_heads(fn, cache, q_heads, scale)) != LQ_OK) return st;
+    if (rows == 0 || b == 0) return LQ_OK;
+    if ((st = check_rows(fn, rows, q_heads, whole)) != LQ_OK) return st;
+    a.batch.whole = whole;
     a.q = static_cast<const uint16_t *>(q_bf16);
     a.q_stride = q_stride;
     a.q_heads = (int)q_heads;
@@ -717,7 +740,103 @@ lq_status paged_attention(const lq_kv_cache *cache, const void *q_bf16, int64_t 
     a.workspace = workspace;
     a.out = static_cast<uint16_t *>(out_bf16);
     a.lse = lse;
+    const int64_t need = lq::attention_workspace_bytes(rows, q_heads, cache->heads, cache->head_dim, b, max_pages,
+                                                       cache->page_size, max_rows, max_kv, whole);
+    st = check_attention(fn, cache, q_bf16, q_stride, need, workspace, workspace_bytes, out_bf16, lse, {}, a);
+    if (st != LQ_OK) return st;
     return launched(lq::launch_paged_attention(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+int64_t attention_workspace(bool whole, int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b,
+                            int64_t max_pages, int64_t page_size, int64_t max_rows, int64_t max_kv) {
+    if (!attention_sizes(rows, q_heads, heads, head_dim, b, max_pages, page_size, max_rows, max_kv) ||
+        (whole && rows > kMaxWholeRows))
+        return -1;
+    if (rows == 0 || b == 0) return 0;
+    return lq::attention_workspace_bytes(rows, q_heads, heads, head_dim, b, max_pages, page_size, max_rows, max_kv, whole);
+}
+
+}  // namespace
+
+int64_t paged_attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b,
+                                        int64_t max_pages, int64_t page_size, int64_t max_rows, int64_t max_kv) {
+    return attention_workspace(false, rows, q_heads, heads, head_dim, b, max_pages, page_size, max_rows, max_kv);
+}
+
+lq_status paged_attention(const lq_kv_cache *cache, const void *q_bf16, int64_t rows, int64_t q_heads,
+                          int64_t q_stride, float scale, const int32_t *block_table, int64_t max_pages,
+                          const int32_t *kv_lens, const int32_t *row_starts, int64_t b, int64_t max_rows,
+                          int64_t max_kv, void *workspace, int64_t workspace_bytes, void *out_bf16, float *lse,
+                          void *stream) {
+    return attention("paged_attention", false, cache, q_bf16, rows, q_heads, q_stride, scale, block_table, max_pages,
+                     kv_lens, row_starts, b, max_rows, max_kv, workspace, workspace_bytes, out_bf16, lse, stream);
+}
+
+int64_t cross_attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b,
+                                        int64_t max_pages, int64_t page_size, int64_t max_rows, int64_t max_kv) {
+    return attention_workspace(true, rows, q_heads, heads, head_dim, b, max_pages, page_size, max_rows, max_kv);
+}
+
+lq_status cross_attention(const lq_kv_cache *cache, const void *q_bf16, int64_t rows, int64_t q_heads,
+                          int64_t q_stride, float scale, const int32_t *block_table, int64_t max_pages,
+                          const int32_t *kv_lens, const int32_t *row_starts, int64_t b, int64_t max_rows,
+                          int64_t max_kv, void *workspace, int64_t workspace_bytes, void *out_bf16, float *lse,
+                          void *stream) {
+    return attention("cross_attention", true, cache, q_bf16, rows, q_heads, q_stride, scale, block_table, max_pages,
+                     kv_lens, row_starts, b, max_rows, max_kv, workspace, workspace_bytes, out_bf16, lse, stream);
+}
+
+int64_t prefix_attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim,
+                                         int64_t page_size, int64_t p, int64_t prefix_pages, int64_t max_prefix_rows,
+                                         int64_t max_prefix, int64_t b, int64_t max_pages, int64_t max_rows,
+                                         int64_t max_kv) {
+    if (!attention_sizes(rows, q_heads, heads, head_dim, b, max_pages, page_size, max_rows, max_kv) ||
+        !attention_sizes(rows, q_heads, heads, head_dim, p, prefix_pages, page_size, max_prefix_rows, max_prefix) ||
+        rows > kMaxWholeRows)
+        return -1;
+    if (rows == 0 || b == 0) return 0;
+    return lq::prefix_workspace_bytes(rows, q_heads, heads, head_dim, page_size, p, prefix_pages, max_prefix_rows,
+                                      max_prefix, b, max_pages, max_rows, max_kv);
+}
+
+lq_status prefix_attention(const lq_kv_cache *cache, const void *q_bf16, int64_t rows, int64_t q_heads, int64_t q_stride,
+                           float scale, const int32_t *prefix_table, int64_t prefix_pages, const int32_t *prefix_lens,
+                           const int32_t *prefix_row_starts, int64_t p, int64_t max_prefix_rows, int64_t max_prefix,
+                           const int32_t *block_table, int64_t max_pages, const int32_t *kv_lens,
+                           const int32_t *row_starts, int64_t b, int64_t max_rows, int64_t max_kv, void *workspace,
+                           int64_t workspace_bytes, void *out_bf16, float *lse, void *stream) {
+    const char *fn = "prefix_attention";
+    lq::PrefixArgs a{};
+    lq_status st = check_kv(fn, cache, rows, block_table, max_pages, kv_lens, row_starts, b, max_rows, &a.own.c, &a.own.batch);
+    if (st != LQ_OK) return st;
+    lq::KvCache same;
+    if ((st = check_kv(fn, cache, rows, prefix_table, prefix_pages, prefix_lens, prefix_row_starts, p, max_prefix_rows,
+                       &same, &a.prefix)) != LQ_OK)
+        return st;
+    if (max_kv < 0 || max_prefix < 0) return fail(LQ_ERR_INVALID_ARG, "%s: negative size", fn);
+    if ((st = check_heads(fn, cache, q_heads, scale)) != LQ_OK) return st;
+    if (rows == 0 || b == 0) return LQ_OK;
+    if ((st = check_rows(fn, rows, q_heads, true)) != LQ_OK) return st;
+    a.prefix.whole = 1;
+    a.max_prefix_rows = max_prefix_rows;
+    a.max_prefix = max_prefix;
+    a.own.q = static_cast<const uint16_t *>(q_bf16);
+    a.own.q_stride = q_stride;
+    a.own.q_heads = (int)q_heads;
+    a.own.scale = scale;
+    a.own.max_rows = max_rows;
+    a.own.max_kv = max_kv;
+    a.own.workspace = workspace;
+    a.own.out = static_cast<uint16_t *>(out_bf16);
+    a.own.lse = lse;
+    const int64_t need = lq::prefix_workspace_bytes(rows, q_heads, cache->heads, cache->head_dim, cache->page_size, p,
+                                                    prefix_pages, max_prefix_rows, max_prefix, b, max_pages, max_rows,
+                                                    max_kv);
+    st = check_attention(fn, cache, q_bf16, q_stride, need, workspace, workspace_bytes, out_bf16, lse,
+                         {{prefix_table, p * prefix_pages * 4}, {prefix_lens, p * 4},
+                          {prefix_row_starts, p ? (p + 1) * 4 : 0}}, a.own);
+    if (st != LQ_OK) return st;
+    return launched(lq::launch_prefix_attention(a, static_cast<hipStream_t>(stream)), fn);
 }
 
 int64_t lq_read_probe_sink_words(void) { return lq::read_probe_sink_words(); }

@@ -633,15 +633,17 @@ __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void at
             for (int w = 0; w < WAVES; ++w) lr += lds_l[w][r] * __builtin_amdgcn_exp2f(lds_m[w][r] - mr);
             const uint32_t wt = wr / (uint32_t)group;
             const int64_t at = (rows.begin + wt) * a.q_heads + h * group + (wr - wt * (uint32_t)group);
-            const float norm = !whole ? 1.0f : inverse_sum(lr);
+            // relative to the maximum in fp32, or the result
+            float *const part = !whole ? span.o + (slot_of + r) * D : a.part_o ? a.part_o + at * D : nullptr;
+            const float norm = part ? 1.0f : inverse_sum(lr);
 #pragma unroll
             for (int d = 4 * c; d < D; d += 4 * kTeam) {
                 f32x4 v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int w = 0; w < WAVES; ++w) v += *reinterpret_cast<const f32x4 *>(&lds_o[w][r][d]);
                 v *= norm;
-                if (!whole) {
-                    *reinterpret_cast<f32x4 *>(span.o + (slot_of + r) * D + d) = v;
+                if (part) {
+                    *reinterpret_cast<f32x4 *>(part + d) = v;
                 } else {
                     const bf16x2_t b0{(__bf16)v[0], (__bf16)v[1]}, b1{(__bf16)v[2], (__bf16)v[3]};
                     *reinterpret_cast<u32x2 *>(a.out + at * D + d) =
@@ -649,8 +651,8 @@ __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void at
                 }
             }
             if (c == 0) {
-                if (!whole) {
-                    float *ml = span.ml + (slot_of + r) * 2;
+                if (part) {
+                    float *ml = !whole ? span.ml + (slot_of + r) * 2 : a.part_ml + at * 2;
                     ml[0] = lr == 0.0f ? -__builtin_inff() : mr;
                     ml[1] = lr;
                 } else if (a.lse) {
@@ -1147,9 +1149,10 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
         if (!SYM) vz = add_halves32(vz);
         if (live) {
             const int64_t at = (rows.begin + tok) * a.q_heads + qh;
-            const int64_t part = slot_of + wave * 32 + n;
+            const int64_t slot = slot_of + wave * 32 + n;
+            float *const part = !whole ? span.o + slot * D : a.part_o ? a.part_o + at * D : nullptr;
             l *= sref * (1.0f / kHead);
-            const float f = (whole ? inverse_sum(l) : 1.0f) * (sref * (1.0f / kHead));
+            const float f = (part ? 1.0f : inverse_sum(l)) * (sref * (1.0f / kHead));
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int mrow = 8 * (i / 4) + 4 * half + i % 4;
@@ -1160,10 +1163,10 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
 #pragma unroll
                     for (int e = 0; e < C::DW; ++e) v[e] = (o[e * (C::TP / 32) + g][i] - vz) * f;
                     const int d = (g * 32 + mrow) * C::DW;
-                    if (!whole) {
+                    if (part) {
 #pragma unroll
                         for (int e = 0; e < C::DW; e += 2)
-                            *reinterpret_cast<float2 *>(span.o + part * D + d + e) = float2{v[e], v[e + 1]};
+                            *reinterpret_cast<float2 *>(part + d + e) = float2{v[e], v[e + 1]};
                     } else {
 #pragma unroll
                         for (int e = 0; e < C::DW; e += 2) {
@@ -1174,9 +1177,10 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
                 }
             }
             if (half == 0) {
-                if (!whole) {
-                    span.ml[part * 2] = l == 0.0f ? -__builtin_inff() : m;
-                    span.ml[part * 2 + 1] = l;
+                if (part) {
+                    float *ml = !whole ? span.ml + slot * 2 : a.part_ml + at * 2;
+                    ml[0] = l == 0.0f ? -__builtin_inff() : m;
+                    ml[1] = l;
                 } else if (a.lse) {
                     a.lse[at] = log_sum(m, l);
                 }
@@ -1228,9 +1232,17 @@ LQ_DEVICE void join_parts(const AttnArgs &a, const Span &span, int block, int pa
             v += *reinterpret_cast<const f32x4 *>(span.o + at * D + 4 * c) *
                  __builtin_amdgcn_exp2f(span.ml[2 * at] - mall);
         }
-        v *= inverse_sum(l);
         const uint32_t wt = wr / (uint32_t)group;
         const int64_t at = (rows.begin + wt) * a.q_heads + h * group + (wr - wt * (uint32_t)group);
+        if (a.part_o) {
+            *reinterpret_cast<f32x4 *>(a.part_o + at * D + 4 * c) = v;
+            if (c == 0) {
+                a.part_ml[2 * at] = l == 0.0f ? -__builtin_inff() : mall;
+                a.part_ml[2 * at + 1] = l;
+            }
+            continue;
+        }
+        v *= inverse_sum(l);
         const bf16x2_t b0{(__bf16)v[0], (__bf16)v[1]}, b1{(__bf16)v[2], (__bf16)v[3]};
         *reinterpret_cast<u32x2 *>(a.out + at * D + 4 * c) =
             u32x2{__builtin_bit_cast(uint32_t, b0), __builtin_bit_cast(uint32_t, b1)};
@@ -1269,7 +1281,7 @@ struct Plan {
 constexpr int kFewWaves = 4, kFewStep = 32 * kFewWaves;
 
 Pass pass_of(int row_tile, int64_t rows, int64_t group, int64_t heads, int64_t head_dim, int bits, int64_t b, int64_t kv,
-             int64_t n) {
+             int64_t n, bool whole_rows) {
     Pass p{};
     p.row_tile = row_tile;
     p.least = 1;
@@ -1306,7 +1318,9 @@ Pass pass_of(int row_tile, int64_t rows, int64_t group, int64_t heads, int64_t h
         // average, and short contexts before the rows only.
         constexpr int64_t kCut = 1200;
         const int64_t slots = row_tile == 256 || head_dim == 256 ? 256 : 512, load = likely * heads;
-        const int64_t mean = b == 1 ? kv - (n < kv ? n : kv) / 2 : kv / 2, prior = n < kv ? kv - n : 0;
+        // Rows that see everything have all of it before them.
+        const int64_t after = whole_rows ? 0 : n < kv ? n : kv;
+        const int64_t mean = b == 1 ? kv - after / 2 : kv / 2, prior = kv - after;
         const int64_t idle = (load + slots - 1) / slots * slots - load;
         p.by_unit = load >= 4 * slots || (kv <= load * mean / slots + kCut && (b == 1 ? idle * prior <= kCut * slots : prior <= kCut));
     } else {
@@ -1329,12 +1343,12 @@ Pass pass_of(int row_tile, int64_t rows, int64_t group, int64_t heads, int64_t h
 }
 
 Plan plan_of(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int bits, int64_t b, int64_t room,
-             int64_t max_rows, int64_t max_kv) {
+             int64_t max_rows, int64_t max_kv, bool whole_rows) {
     Plan p{};
     const int64_t n = max_rows <= 0 || max_rows > rows ? rows : max_rows;
     const int64_t kv = max_kv <= 0 || max_kv > room ? room : max_kv;
     const int64_t group = q_heads / heads;
-    auto pass = [&](int row_tile) { return pass_of(row_tile, rows, group, heads, head_dim, bits, b, kv, n); };
+    auto pass = [&](int row_tile) { return pass_of(row_tile, rows, group, heads, head_dim, bits, b, kv, n, whole_rows); };
     p.passes = 1;
     if (n * group <= 16) {
         p.pass[0] = pass(n * group <= 8 ? 8 : 16);
@@ -1352,7 +1366,7 @@ Plan plan_of(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int
         // 300 on one head, 1500 tokens: 49.7 us, 60.6 by the chunk's rows).
         if (b >= 4 && group <= 16 && (rows - n) * group <= 64 * (b - 1)) {
             p.pass[0].least = 17;
-            p.pass[1] = pass_of(16, 0, group, heads, head_dim, bits, b, kv, 1);
+            p.pass[1] = pass_of(16, 0, group, heads, head_dim, bits, b, kv, 1, whole_rows);
             p.pass[1].most = 16;
             p.passes = 2;
         }
@@ -1364,9 +1378,9 @@ Plan plan_of(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int
 }  // namespace
 
 int64_t attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b,
-                                  int64_t max_pages, int64_t page_size, int64_t max_rows, int64_t max_kv) {
+                                  int64_t max_pages, int64_t page_size, int64_t max_rows, int64_t max_kv, bool whole) {
     // of either format: INT4's blocks are as many as INT8's or more
-    return plan_of(rows, q_heads, heads, head_dim, 4, b, max_pages * page_size, max_rows, max_kv).bytes;
+    return plan_of(rows, q_heads, heads, head_dim, 4, b, max_pages * page_size, max_rows, max_kv, whole).bytes;
 }
 
 static Span span_of(const AttnArgs &a, const Pass &p, char *workspace) {
@@ -1424,9 +1438,7 @@ static hipError_t launch_plan(const AttnArgs &a, const Plan &p, hipStream_t st) 
     }
 }
 
-hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st) {
-    const Plan p = plan_of(a.batch.rows, a.q_heads, a.c.heads, a.c.head_dim, a.c.bits, a.batch.b,
-                           a.batch.max_pages << a.c.page_shift, a.max_rows, a.max_kv);
+static hipError_t launch_one(const AttnArgs &a, const Plan &p, hipStream_t st) {
 #define LQ_ATTN(D, BITS, SYM) \
     if (a.c.head_dim == D && a.c.bits == BITS && (a.c.symmetric != 0) == SYM) return launch_plan<D, BITS, SYM>(a, p, st);
 #define LQ_ATTN_D(D) LQ_ATTN(D, 4, false) LQ_ATTN(D, 4, true) LQ_ATTN(D, 8, false) LQ_ATTN(D, 8, true)
@@ -1434,6 +1446,94 @@ hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st) {
 #undef LQ_ATTN_D
 #undef LQ_ATTN
     return hipErrorInvalidValue;
+}
+
+static Plan plan_of(const AttnArgs &a) {
+    return plan_of(a.batch.rows, a.q_heads, a.c.heads, a.c.head_dim, a.c.bits, a.batch.b,
+                   a.batch.max_pages << a.c.page_shift, a.max_rows, a.max_kv, a.batch.whole);
+}
+
+hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st) { return launch_one(a, plan_of(a), st); }
+
+// ---- attention over a shared prefix and over a sequence's own tokens ----
+//
+// The prefix's keys are read once for all rows that share it: its pass takes
+// them as the rows of one sequence that each see everything, in tiles as a
+// prompt's rows are. The own tokens' pass is paged_attention's. Both leave rows
+// relative to their maximum, which this kernel joins, D / 4 lanes a row and head.
+template <int D>
+__global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs own, KvBatch prefix, const float *part_o,
+                                                         const float *part_ml) {
+    constexpr int W = D / 4;
+    const int c = threadIdx.x % W;
+    const KvBatch &bt = own.batch;
+    // rows of some sequence, and those among them with a prefix
+    const int64_t from = bt.starts[0], to = bt.starts[bt.b] < bt.rows ? bt.starts[bt.b] : bt.rows;
+    const int64_t from2 = prefix.starts[0], to2 = prefix.starts[prefix.b];
+    for (int64_t item = (from < 0 ? 0 : from) * own.q_heads + ((int64_t)blockIdx.x * 256 + threadIdx.x) / W;
+         item < to * own.q_heads; item += (int64_t)gridDim.x * (256 / W)) {
+        const int64_t row = item / own.q_heads;
+        const bool shared = row >= from2 && row < to2;
+        const float2 none{-__builtin_inff(), 0.0f};
+        const float2 x = reinterpret_cast<const float2 *>(own.part_ml)[item];
+        const float2 y = shared ? reinterpret_cast<const float2 *>(part_ml)[item] : none;
+        const float m = fmaxf(fmaxf(x.x, y.x), -1e30f);
+        const float fx = __builtin_amdgcn_exp2f(x.x - m), fy = __builtin_amdgcn_exp2f(y.x - m);
+        const float l = x.y * fx + y.y * fy;
+        f32x4 v = *reinterpret_cast<const f32x4 *>(own.part_o + item * D + 4 * c) * fx;
+        if (shared) v += *reinterpret_cast<const f32x4 *>(part_o + item * D + 4 * c) * fy;
+        v *= inverse_sum(l);
+        const bf16x2_t b0{(__bf16)v[0], (__bf16)v[1]}, b1{(__bf16)v[2], (__bf16)v[3]};
+        *reinterpret_cast<u32x2 *>(own.out + item * D + 4 * c) =
+            u32x2{__builtin_bit_cast(uint32_t, b0), __builtin_bit_cast(uint32_t, b1)};
+        if (c == 0 && own.lse) own.lse[item] = log_sum(m, l);
+    }
+}
+
+static int64_t part_bytes(int64_t rows, int64_t q_heads, int64_t floats) {
+    return (rows * q_heads * floats * 4 + 255) / 256 * 256;
+}
+
+int64_t prefix_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t page_size,
+                               int64_t p, int64_t prefix_pages, int64_t max_prefix_rows, int64_t max_prefix, int64_t b,
+                               int64_t max_pages, int64_t max_rows, int64_t max_kv) {
+    const int64_t own = attention_workspace_bytes(rows, q_heads, heads, head_dim, b, max_pages, page_size, max_rows,
+                                                  max_kv, false);
+    if (p == 0) return own;
+    return own + 2 * (part_bytes(rows, q_heads, head_dim) + part_bytes(rows, q_heads, 2)) +
+           attention_workspace_bytes(rows, q_heads, heads, head_dim, p, prefix_pages, page_size, max_prefix_rows,
+                                     max_prefix, true);
+}
+
+hipError_t launch_prefix_attention(const PrefixArgs &a, hipStream_t st) {
+    if (a.prefix.b == 0) return launch_paged_attention(a.own, st);
+    AttnArgs own = a.own, pre = a.own;
+    pre.batch = a.prefix;
+    pre.max_rows = a.max_prefix_rows;
+    pre.max_kv = a.max_prefix;
+    const Plan op = plan_of(own), pp = plan_of(pre);
+    char *ws = static_cast<char *>(a.own.workspace);
+    const int64_t o_bytes = part_bytes(own.batch.rows, own.q_heads, own.c.head_dim);
+    const int64_t ml_bytes = part_bytes(own.batch.rows, own.q_heads, 2);
+    for (AttnArgs *x : {&own, &pre}) {
+        x->part_o = reinterpret_cast<float *>(ws);
+        x->part_ml = reinterpret_cast<float *>(ws + o_bytes);
+        ws += o_bytes + ml_bytes;
+    }
+    own.workspace = ws;
+    pre.workspace = ws + op.bytes;
+    hipError_t e = launch_one(own, op, st);
+    if (e != hipSuccess) return e;
+    if ((e = launch_one(pre, pp, st)) != hipSuccess) return e;
+    const int64_t lanes = own.batch.rows * own.q_heads * (own.c.head_dim / 4);
+    const dim3 grid((uint32_t)(lanes < (1 << 30) ? (lanes + 255) / 256 : 1 << 22));
+    if (own.c.head_dim == 64)
+        hipLaunchKernelGGL(attn_merge_kernel<64>, grid, dim3(256), 0, st, own, pre.batch, pre.part_o, pre.part_ml);
+    else if (own.c.head_dim == 128)
+        hipLaunchKernelGGL(attn_merge_kernel<128>, grid, dim3(256), 0, st, own, pre.batch, pre.part_o, pre.part_ml);
+    else
+        hipLaunchKernelGGL(attn_merge_kernel<256>, grid, dim3(256), 0, st, own, pre.batch, pre.part_o, pre.part_ml);
+    return hipGetLastError();
 }
 
 }  // namespace lq

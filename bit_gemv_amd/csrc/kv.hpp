@@ -19,6 +19,7 @@ struct KvCache {
 struct KvBatch {
     const int32_t *table, *lens, *starts;
     int64_t b, max_pages, rows;
+    int whole = 0;  // the rows are no tokens of the sequence: each sees all that it holds
 };
 
 struct KvWriteArgs {
@@ -50,16 +51,32 @@ struct AttnArgs {
     void *workspace;
     uint16_t *out;
     float *lse;
+    // in the place of out and lse, for a result that is joined with another: the
+    // rows [rows][q_heads][D] relative to their maximum, maximum (log2) and sum
+    float *part_o = nullptr, *part_ml = nullptr;
+};
+
+// Attention over a prefix that several sequences share and over their own
+// tokens: `own` is the whole call, `prefix` the groups of rows that share one.
+struct PrefixArgs {
+    AttnArgs own;
+    KvBatch prefix;
+    int64_t max_prefix_rows, max_prefix;
 };
 
 hipError_t launch_kv_write(const KvWriteArgs &a, hipStream_t st);
 hipError_t launch_kv_read(const KvReadArgs &a, hipStream_t st);
 int64_t attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b,
-                                  int64_t max_pages, int64_t page_size, int64_t max_rows, int64_t max_kv);
+                                  int64_t max_pages, int64_t page_size, int64_t max_rows, int64_t max_kv, bool whole);
+int64_t prefix_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t page_size,
+                               int64_t p, int64_t prefix_pages, int64_t max_prefix_rows, int64_t max_prefix, int64_t b,
+                               int64_t max_pages, int64_t max_rows, int64_t max_kv);
 hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st);
+hipError_t launch_prefix_attention(const PrefixArgs &a, hipStream_t st);
 
 // One sequence's rows: [begin, begin + n) of the row tensors, row begin + i at
-// position first + i. Out-of-range starts are cut to the row tensors.
+// position first + i. Out-of-range starts are cut to the row tensors. Rows that
+// see everything stand behind the last token.
 struct KvRows {
     int64_t begin, n, first, len;  // len: tokens held, cut to the table
 };
@@ -70,9 +87,9 @@ __device__ __forceinline__ KvRows kv_rows(const KvBatch &bt, int64_t seq, int pa
     r.begin = s0 < 0 ? 0 : s0;
     const int64_t end = s1 > bt.rows ? bt.rows : s1;
     r.n = end > r.begin ? end - r.begin : 0;
-    r.first = held - (s1 - r.begin);
     const int64_t room = bt.max_pages << page_shift;
     r.len = held > room ? room : held;
+    r.first = bt.whole ? r.len : held - (s1 - r.begin);
     return r;
 }
 

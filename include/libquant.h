@@ -528,6 +528,54 @@ lq_status paged_attention(const lq_kv_cache *cache, const void *q_bf16, int64_t 
                           void *stream);
 
 /*
+ * cross_attention -- attention of rows that are no tokens of their sequence
+ * over all that it holds: a decoder's rows over an encoder's states, however
+ * many of either (beams of one input are rows of one sequence). Formula,
+ * arguments, arithmetic, workspace (of cross_attention_workspace_bytes) and
+ * errors as paged_attention, but that every row sees the positions 0 ..
+ * kv_lens[i] - 1 of its sequence, wherever it stands; kv_lens[i] counts none of
+ * the rows. The states are written once by kv_cache_write, as the rows of a
+ * prompt. At most 2^30 rows.
+ */
+int64_t cross_attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b,
+                                        int64_t max_pages, int64_t page_size, int64_t max_rows, int64_t max_kv);
+lq_status cross_attention(const lq_kv_cache *cache, const void *q_bf16, int64_t rows, int64_t q_heads,
+                          int64_t q_stride, float scale, const int32_t *block_table, int64_t max_pages,
+                          const int32_t *kv_lens, const int32_t *row_starts, int64_t b, int64_t max_rows,
+                          int64_t max_kv, void *workspace, int64_t workspace_bytes, void *out_bf16, float *lse,
+                          void *stream);
+
+/*
+ * prefix_attention -- paged_attention of sequences that share long prefixes,
+ * each prefix read and multiplied once for all rows of its sequences:
+ *   out[r][h] = sum_j p_j v_hat[j][h / g],  p = softmax_j(scale q[r][h] . k_hat[j][h / g])
+ * over all tokens of r's prefix and the positions up to r's own of r's
+ * sequence, which holds the tokens behind the prefix only (kv_lens, block_table
+ * and row_starts as in paged_attention; kv_lens does not count the prefix).
+ * Prefix i of p holds prefix_lens[i] tokens in the pages of prefix_table
+ * [p][prefix_pages] and belongs to the rows prefix_row_starts[i] ..
+ * prefix_row_starts[i + 1] - 1: the sequences of one prefix lie together in the
+ * batch. Rows outside all of these have no prefix. All in device memory, int32,
+ * prefix_row_starts [p + 1] ascending. Pages may be shared at will: nothing is
+ * written. max_prefix_rows and max_prefix bound the rows and the tokens of one
+ * prefix, as max_rows and max_kv those of one sequence. p = 0 is
+ * paged_attention. Each of the two sums has paged_attention's arithmetic (the
+ * value scales' range counts for each of them by itself); they are joined in
+ * fp32 and rounded once. At most 2^30 rows. Arguments otherwise, workspace and
+ * errors as paged_attention.
+ */
+int64_t prefix_attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim,
+                                         int64_t page_size, int64_t p, int64_t prefix_pages, int64_t max_prefix_rows,
+                                         int64_t max_prefix, int64_t b, int64_t max_pages, int64_t max_rows,
+                                         int64_t max_kv);
+lq_status prefix_attention(const lq_kv_cache *cache, const void *q_bf16, int64_t rows, int64_t q_heads, int64_t q_stride,
+                           float scale, const int32_t *prefix_table, int64_t prefix_pages, const int32_t *prefix_lens,
+                           const int32_t *prefix_row_starts, int64_t p, int64_t max_prefix_rows, int64_t max_prefix,
+                           const int32_t *block_table, int64_t max_pages, const int32_t *kv_lens,
+                           const int32_t *row_starts, int64_t b, int64_t max_rows, int64_t max_kv, void *workspace,
+                           int64_t workspace_bytes, void *out_bf16, float *lse, void *stream);
+
+/*
  * Measurement helper (not a step of the method).
  *
  * lq_hbm_read_probe -- reads `bytes` bytes at `p` once with a streaming-read

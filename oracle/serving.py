@@ -151,3 +151,41 @@ def attention(q, cache, table, kv_lens, row_starts, scale):
                     bound[r, j] = (2.0 ** -8 * np.abs(out[r, j]) + (2.0 ** -11 + 2.0 ** -20 + 4 * delta) * w
                                    + n * 2.0 ** -24 * w2 + n * 2.0 ** -27 * np.abs(v[:n]).max())
     return out, lse, bound
+
+
+def attention_over(q, cache, sets, scale):
+    """Attention of each row over the union of some sets of tokens: sets[r] is a
+    list of (list of pages, tokens held in them), or None for a row that is left
+    alone. float64 (out, lse, bound) as attention; 2^-19 in the place of 2^-20
+    there: sets' results are joined in fp32 by two factors and a sum."""
+    rows, q_heads, d = q.shape
+    group, mid = q_heads // cache.heads, 2.0 ** (cache.bits - 1)
+    out, bound = np.zeros((rows, q_heads, d)), np.zeros((rows, q_heads, d))
+    lse, seen = np.full((rows, q_heads), -np.inf), {}
+
+    def side(pages, h, name, n):
+        key = tuple(pages), h, name
+        if key not in seen:
+            c, s, z = cache.parts(pages, h, name, len(pages) * cache.page_size)
+            seen[key] = (c - z[:, None]) * s[:, None], (np.abs(c - mid) + np.abs(z - mid)[:, None]) * s[:, None]
+        return seen[key][0][:n], seen[key][1][:n]
+
+    for r in range(rows):
+        live = [(pages[:(n + cache.page_size - 1) // cache.page_size], n) for pages, n in sets[r] or [] if n > 0]
+        if not live:
+            continue
+        for h in range(cache.heads):
+            k, kabs = (np.concatenate(x) for x in zip(*(side(p, h, "k", n) for p, n in live)))
+            v, vabs = (np.concatenate(x) for x in zip(*(side(p, h, "v", n) for p, n in live)))
+            for j in range(h * group, (h + 1) * group):
+                x = q[r, j].astype(np.float64)
+                t = scale * (k @ x)
+                m = t.max()
+                p = np.exp(t - m)
+                out[r, j] = p @ v / p.sum()
+                lse[r, j] = m + np.log(p.sum())
+                delta = (d + 8) * 2.0 ** -24 * abs(scale) * (kabs @ np.abs(x)).max()
+                w, w2 = p @ np.abs(v) / p.sum(), p @ vabs / p.sum()
+                bound[r, j] = (2.0 ** -8 * np.abs(out[r, j]) + (2.0 ** -11 + 2.0 ** -19 + 4 * delta) * w
+                               + len(t) * (2.0 ** -24 * w2 + 2.0 ** -27 * np.abs(v).max()))
+    return out, lse, bound
