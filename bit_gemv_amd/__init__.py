@@ -29,7 +29,7 @@ ENTRY_POINTS = ("quantize_groupwise", "dequantize_groupwise", "w4a16_gemv", "w8a
                 "smooth_scale", "quant_per_token_int8", "w8a8_gemm", "act_absmean", "awq_search",
                 "mxfp4_quantize", "mxfp4_gemv", "mxfp4_gemm", "gptq_hessian_factor", "gptq_quantize",
                 "rms_norm_int8", "kv_cache_write", "kv_cache_read", "paged_attention", "cross_attention",
-                "prefix_attention")
+                "prefix_attention", "kv_cache_weigh", "kv_cache_evict")
 
 
 class LibquantError(RuntimeError):
@@ -77,6 +77,8 @@ def load_library(path: Optional[str] = None):
         "kv_cache_read": [P, P, P, I, I64, P, I64, P, P, I64, I64, P],
         "paged_attention": [P, P, I64, I64, I64, F, P, I64, P, P, I64, I64, I64, P, I64, P, P, P],
         "cross_attention": [P, P, I64, I64, I64, F, P, I64, P, P, I64, I64, I64, P, I64, P, P, P],
+        "kv_cache_weigh": [P, P, I64, I64, I64, F, P, P, I64, P, P, I64, I, I64, I64, P, P, P],
+        "kv_cache_evict": [P, P, P, I64, P, I64, I64, I64, P, I64, I64, P, P, P],
         "prefix_attention": [P, P, I64, I64, I64, F] + [P, I64, P, P, I64, I64, I64] * 2 + [P, I64, P, P, P],
     }
     for name, argtypes in sigs.items():
@@ -817,3 +819,72 @@ def prefix_attention_workspace(rows: int, q_heads: int, cache: KVCache, p: int, 
     if need < 0:
         raise LibquantError(LQ_ERR_INVALID_ARG, "prefix_attention", "sizes out of range")
     return need
+
+
+def kv_cache_weigh(q: torch.Tensor, lse: torch.Tensor, cache: KVCache, weights: Optional[torch.Tensor],
+                   block_table: torch.Tensor, kv_lens: torch.Tensor, row_starts: torch.Tensor,
+                   scale: Optional[float] = None, causal: bool = True, max_rows: int = 0, max_kv: int = 0,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Add the attention weight that every cached token receives from the rows q
+    [rows][q_heads][head_dim] to weights (fp32 [pages][heads][page_size], None:
+    zeros): the sum of exp(scale q . k - lse) over the rows that see it and its
+    head's group, lse being what attention returned for these rows. causal: rows
+    are their sequences' last tokens (paged_attention, prefix_attention's own
+    tokens), whose own weights start from 0; otherwise they see the whole sequence
+    (cross_attention, a shared prefix). -> out, by default weights itself."""
+    qs = _rows(cache, q, "q", None)
+    if q.dtype is not _BF16:
+        raise TypeError(f"q must be {_BF16}, got {q.dtype}")
+    rows, q_heads, d = q.shape
+    index = cache._index
+    _on(index, lse, "lse", _F32, (rows, q_heads))
+    shape = cache.k_scales.shape
+    if weights is not None:
+        _on(index, weights, "weights", _F32, shape)
+    if out is None:
+        out = torch.zeros(shape, dtype=_F32, device=cache.device) if weights is None else weights
+    else:
+        _on(index, out, "out", _F32, shape)
+    table, max_pages, lens, starts, b = _batch(index, block_table, kv_lens, row_starts)
+    _launch("kv_cache_weigh", index, cache._live(), q.data_ptr(), rows, q_heads, qs, d ** -0.5 if scale is None else scale,
+            lse.data_ptr(), table, max_pages, lens, starts, b, 1 if causal else 0, max_rows, max_kv,
+            None if weights is None else weights.data_ptr(), out.data_ptr())
+    return out
+
+
+def kv_cache_evict(cache: KVCache, weights: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor, keep: int,
+                   recent: int = 0, to_table: Optional[torch.Tensor] = None, max_kv: int = 0,
+                   kept: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None):
+    """Shrink every sequence of more than `keep` tokens to `keep`: each head's last
+    `recent` and the heaviest of the others by weights (fp32
+    [pages][heads][page_size]), in their order, moved with their weights to the
+    front of to_table's pages (int32 [b][to_pages]; None: block_table's own).
+    -> (new_lens int32 [b], kept int32 [b][heads][keep], -1 behind the last);
+    new_lens may be kv_lens."""
+    index = cache._index
+    if not isinstance(block_table, _Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a tensor [b][max_pages]")
+    b, max_pages = block_table.shape
+    _on(index, weights, "weights", _F32, cache.k_scales.shape)
+    _on(index, block_table, "block_table", _I32, None)
+    _on(index, kv_lens, "kv_lens", _I32, (b,))
+    to_ptr, to_pages = None, 0
+    if to_table is not None:
+        if not isinstance(to_table, _Tensor) or to_table.dim() != 2 or to_table.shape[0] != b:
+            raise ValueError("to_table must be a tensor [b][to_pages]")
+        _on(index, to_table, "to_table", _I32, None)
+        to_ptr, to_pages = to_table.data_ptr(), to_table.shape[1]
+    if keep < 1:
+        raise ValueError(f"keep must be positive, got {keep}")
+    shape = b, cache.heads, keep
+    if kept is None:
+        kept = _empty(shape, (cache.heads * keep, keep, 1), dtype=_I32, device=cache.device)
+    else:
+        _on(index, kept, "kept", _I32, shape)
+    if new_lens is None:
+        new_lens = _empty((b,), (1,), dtype=_I32, device=cache.device)
+    else:
+        _on(index, new_lens, "new_lens", _I32, (b,))
+    _launch("kv_cache_evict", index, cache._live(), weights.data_ptr(), block_table.data_ptr(), max_pages,
+            kv_lens.data_ptr(), b, keep, recent, to_ptr, to_pages, max_kv, kept.data_ptr(), new_lens.data_ptr())
+    return new_lens, kept

@@ -839,6 +839,103 @@ lq_status prefix_attention(const lq_kv_cache *cache, const void *q_bf16, int64_t
     return launched(lq::launch_prefix_attention(a, static_cast<hipStream_t>(stream)), fn);
 }
 
+lq_status kv_cache_weigh(const lq_kv_cache *cache, const void *q_bf16, int64_t rows, int64_t q_heads, int64_t q_stride,
+                         float scale, const float *lse, const int32_t *block_table, int64_t max_pages,
+                         const int32_t *kv_lens, const int32_t *row_starts, int64_t b, int causal, int64_t max_rows,
+                         int64_t max_kv, const float *weights, float *weights_out, void *stream) {
+    const char *fn = "kv_cache_weigh";
+    lq::WeighArgs a{};
+    lq_status st = check_kv(fn, cache, rows, block_table, max_pages, kv_lens, row_starts, b, max_rows, &a.c, &a.batch);
+    if (st != LQ_OK) return st;
+    if (max_kv < 0) return fail(LQ_ERR_INVALID_ARG, "%s: negative size", fn);
+    if (causal != 0 && causal != 1) return fail(LQ_ERR_INVALID_ARG, "%s: causal must be 0 or 1", fn);
+    if ((st = check_heads(fn, cache, q_heads, scale)) != LQ_OK) return st;
+    if (rows == 0 || b == 0 || max_pages == 0) return LQ_OK;
+    if ((st = check_rows(fn, rows, q_heads, true)) != LQ_OK) return st;
+    const int64_t width = q_heads * cache->head_dim;
+    if (q_stride < width || q_stride % 8)
+        return fail(LQ_ERR_INVALID_ARG, "%s: q_stride must be a multiple of 8 and at least q_heads * head_dim", fn);
+    if (q_stride > kMaxElems / rows) return fail(LQ_ERR_UNSUPPORTED, "%s: q_stride too large", fn);
+    if (!q_bf16 || !aligned(q_bf16, 16)) return fail(LQ_ERR_INVALID_ARG, "%s: q null or not 16-byte aligned", fn);
+    if (!lse || !aligned(lse, 4)) return fail(LQ_ERR_INVALID_ARG, "%s: lse null or misaligned", fn);
+    if (!aligned(weights, 16)) return fail(LQ_ERR_INVALID_ARG, "%s: weights not 16-byte aligned", fn);
+    if (!weights_out || !aligned(weights_out, 16))
+        return fail(LQ_ERR_INVALID_ARG, "%s: weights_out null or not 16-byte aligned", fn);
+    const int64_t codes = kv_code_bytes(cache), meta = kv_meta_bytes(cache), zeros = cache->symmetric ? 0 : meta;
+    const Range out{weights_out, meta}, in{weights, weights ? meta : 0};
+    if (any_overlap({out}, {{q_bf16, ((rows - 1) * q_stride + width) * 2}, {lse, rows * q_heads * 4},
+                            {cache->k_codes, codes}, {cache->v_codes, codes}, {cache->k_scales, meta},
+                            {cache->v_scales, meta}, {cache->k_zeros, zeros}, {cache->v_zeros, zeros},
+                            {block_table, b * max_pages * 4}, {kv_lens, b * 4}, {row_starts, (b + 1) * 4}}) ||
+        (weights_out != weights && overlap(out, in)))
+        return fail(LQ_ERR_INVALID_ARG, "%s: an output overlaps an input", fn);
+    if ((st = need_device()) != LQ_OK) return st;
+    a.batch.whole = !causal;
+    a.q = static_cast<const uint16_t *>(q_bf16);
+    a.q_stride = q_stride;
+    a.q_heads = (int)q_heads;
+    a.scale = scale;
+    a.lse = lse;
+    a.weights = weights;
+    a.out = weights_out;
+    a.max_rows = max_rows;
+    a.max_kv = max_kv;
+    return launched(lq::launch_kv_weigh(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+lq_status kv_cache_evict(const lq_kv_cache *cache, float *weights, const int32_t *block_table, int64_t max_pages,
+                         const int32_t *kv_lens, int64_t b, int64_t keep, int64_t recent, const int32_t *to_table,
+                         int64_t to_pages, int64_t max_kv, int32_t *kept, int32_t *new_lens, void *stream) {
+    const char *fn = "kv_cache_evict";
+    lq::EvictArgs a{};
+    lq::KvBatch batch;
+    lq_status st = check_kv(fn, cache, 0, block_table, max_pages, kv_lens, nullptr, b, 0, &a.c, &batch);
+    if (st != LQ_OK) return st;
+    if (!to_table) {  // in place
+        to_table = block_table;
+        to_pages = max_pages;
+    }
+    if (keep < 1 || recent < 0 || recent > keep || to_pages < 0 || max_kv < 0)
+        return fail(LQ_ERR_INVALID_ARG, "%s: keep must be positive, recent in 0..keep, sizes not negative", fn);
+    const int64_t room = max_pages * cache->page_size, to_room = to_pages <= lq::kMaxTokens ? to_pages * cache->page_size : 0;
+    if (keep > lq::kMaxTokens || to_pages > lq::kMaxTokens / cache->page_size || b * cache->heads >= (1 << 22) ||
+        b * cache->heads * keep > kMaxElems)
+        return fail(LQ_ERR_UNSUPPORTED, "%s: keep, to_table or batch too large", fn);
+    if (to_room < (keep < room ? keep : room))
+        return fail(LQ_ERR_INVALID_ARG, "%s: to_table has room for %lld tokens, fewer than stay", fn, (long long)to_room);
+    if (b == 0) return LQ_OK;
+    if ((max_pages > 0 && (!block_table || !aligned(block_table, 4))) || !aligned(to_table, 4) || !kv_lens ||
+        !aligned(kv_lens, 4))
+        return fail(LQ_ERR_INVALID_ARG, "%s: block_table, to_table or kv_lens null or misaligned", fn);
+    if (!weights || !aligned(weights, 16)) return fail(LQ_ERR_INVALID_ARG, "%s: weights null or not 16-byte aligned", fn);
+    if (!kept || !aligned(kept, 4) || !new_lens || !aligned(new_lens, 4))
+        return fail(LQ_ERR_INVALID_ARG, "%s: kept or new_lens null or misaligned", fn);
+    const int64_t codes = kv_code_bytes(cache), meta = kv_meta_bytes(cache), zeros = cache->symmetric ? 0 : meta;
+    const Range lens{kv_lens, b * 4}, out_lens{new_lens, b * 4}, out_kept{kept, b * cache->heads * keep * 4};
+    const Range tables[2] = {{block_table, b * max_pages * 4}, {to_table, b * to_pages * 4}};
+    if (any_overlap({{cache->k_codes, codes}, {cache->v_codes, codes}, {cache->k_scales, meta}, {cache->v_scales, meta},
+                     {cache->k_zeros, zeros}, {cache->v_zeros, zeros}, {weights, meta}, out_kept, out_lens},
+                    {tables[0], tables[1]}) ||
+        any_overlap({{cache->k_codes, codes}, {cache->v_codes, codes}, {cache->k_scales, meta}, {cache->v_scales, meta},
+                     {cache->k_zeros, zeros}, {cache->v_zeros, zeros}, {weights, meta}, out_kept}, {lens}) ||
+        (new_lens != kv_lens && overlap(out_lens, lens)))
+        return fail(LQ_ERR_INVALID_ARG, "%s: an output overlaps an input or another output", fn);
+    if ((st = need_device()) != LQ_OK) return st;
+    a.weights = weights;
+    a.table = block_table;
+    a.lens = kv_lens;
+    a.b = b;
+    a.max_pages = max_pages;
+    a.keep = keep;
+    a.recent = recent;
+    a.to_table = to_table;
+    a.to_pages = to_pages;
+    a.max_kv = max_kv;
+    a.kept = kept;
+    a.new_lens = new_lens;
+    return launched(lq::launch_kv_evict(a, static_cast<hipStream_t>(stream)), fn);
+}
+
 int64_t lq_read_probe_sink_words(void) { return lq::read_probe_sink_words(); }
 
 lq_status lq_hbm_read_probe(const void *p, int64_t bytes, uint32_t *sink, void *stream) {

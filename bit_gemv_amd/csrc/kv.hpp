@@ -64,8 +64,37 @@ struct PrefixArgs {
     int64_t max_prefix_rows, max_prefix;
 };
 
+// The attention weight that cached tokens receive; weights and out fp32 in the
+// scales' layout, weights null: from zero.
+struct WeighArgs {
+    KvCache c;
+    KvBatch batch;
+    const uint16_t *q;
+    int64_t q_stride;
+    int q_heads;
+    float scale;
+    const float *lse, *weights;
+    float *out;
+    int64_t max_rows, max_kv;
+};
+
+// Eviction by weight from the sequences' pages to the front of to_table's.
+struct EvictArgs {
+    KvCache c;
+    float *weights;
+    const int32_t *table, *lens;
+    int64_t b, max_pages;
+    int64_t keep, recent;
+    const int32_t *to_table;
+    int64_t to_pages;
+    int64_t max_kv;
+    int32_t *kept, *new_lens;
+};
+
 hipError_t launch_kv_write(const KvWriteArgs &a, hipStream_t st);
 hipError_t launch_kv_read(const KvReadArgs &a, hipStream_t st);
+hipError_t launch_kv_weigh(const WeighArgs &a, hipStream_t st);
+hipError_t launch_kv_evict(const EvictArgs &a, hipStream_t st);
 int64_t attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b,
                                   int64_t max_pages, int64_t page_size, int64_t max_rows, int64_t max_kv, bool whole);
 int64_t prefix_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t page_size,

@@ -576,6 +576,61 @@ lq_status prefix_attention(const lq_kv_cache *cache, const void *q_bf16, int64_t
                            int64_t workspace_bytes, void *out_bf16, float *lse, void *stream);
 
 /*
+ * kv_cache_weigh -- the attention weight that the cached tokens receive, summed
+ * over the call's rows and the query heads of each key head's group:
+ *   weights_out[slot of j][h] = weights[slot of j][h] + sum_r sum_i exp(scale q[r][i] . k_hat[j][h] - lse[r][i])
+ * over the rows r of j's sequence that see j (causal 1: as in paged_attention,
+ * j up to r's own position; causal 0: all, as in cross_attention) and the heads
+ * i with i / g = h, for every position j of every sequence that has rows. A
+ * causal call's own tokens, which its rows brought into the cache, start from 0
+ * in the place of weights. lse fp32 [rows][q_heads]: what the attention call
+ * returned for these rows (with a shared prefix prefix_attention's, for the
+ * prefix's and the own tokens alike). A row whose lse is not finite (it saw
+ * nothing, or holds a NaN) adds nothing.
+ * weights and weights_out fp32 in the scales' layout [pages][heads][page_size],
+ * 16-byte aligned; weights may be NULL (zeros), and weights_out weights itself.
+ * Slots that hold no position of such a sequence are left as they were. No page
+ * may be held by two sequences of a call: each would write it.
+ * To weigh a prompt by its last rows only, give only those as rows, their
+ * row_starts counting them: positions count from the end.
+ * Weights are relative to their exact value off by at most a few times 2^-24
+ * of the largest |scale q . k_hat| and |lse|, and by 2^-24 for each addition;
+ * sums in a fixed order: equal calls give equal bits. Other arguments and errors
+ * as paged_attention; at most 2^30 rows; no workspace.
+ */
+lq_status kv_cache_weigh(const lq_kv_cache *cache, const void *q_bf16, int64_t rows, int64_t q_heads, int64_t q_stride,
+                         float scale, const float *lse, const int32_t *block_table, int64_t max_pages,
+                         const int32_t *kv_lens, const int32_t *row_starts, int64_t b, int causal, int64_t max_rows,
+                         int64_t max_kv, const float *weights, float *weights_out, void *stream);
+
+/*
+ * kv_cache_evict -- shrink sequences to `keep` tokens by weight. Of a sequence i
+ * of more than keep tokens each key head keeps the last `recent` and, of the
+ * others, the keep - recent of the largest weight (of equal ones the earlier;
+ * NaN is heaviest), in their order; they become the positions 0 .. keep - 1.
+ * Sequences of up to keep tokens keep all. Heads keep different tokens, so
+ * a position no longer stands for one token: rotary or other position codes must
+ * be in the keys already, as a cache that is read by attention has them.
+ * Codes, scales, zeros and weights (fp32 in the scales' layout) move to the
+ * front of to_table's pages: int32 [b][to_pages], or NULL for block_table itself.
+ * It may have a page of block_table only in that page's own place (sequence and
+ * index), and has room for min(keep, max_pages * page_size) tokens. Pages behind
+ * the last token that stayed are free; slots behind it in its page may hold
+ * anything. No page may be held by two sequences of a call, except that without
+ * NULL, pages of block_table that to_table does not have may be shared: they
+ * are only read.
+ * kept out int32 [b][heads][keep]: the positions that stayed, ascending, -1
+ * behind the last. new_lens out int32 [b]: min(kv_lens[i], keep), the kv_lens of
+ * later calls; may be kv_lens. Positions in a page that is not in the pool go
+ * first; where one has to stay, or to_table's page is not in the pool, its slot
+ * holds anything. 1 <= keep, 0 <= recent <= keep; b * heads below 2^22. max_kv as
+ * in paged_attention. weights 16-byte, int32 arrays 4-byte aligned.
+ */
+lq_status kv_cache_evict(const lq_kv_cache *cache, float *weights, const int32_t *block_table, int64_t max_pages,
+                         const int32_t *kv_lens, int64_t b, int64_t keep, int64_t recent, const int32_t *to_table,
+                         int64_t to_pages, int64_t max_kv, int32_t *kept, int32_t *new_lens, void *stream);
+
+/*
  * Measurement helper (not a step of the method).
  *
  * lq_hbm_read_probe -- reads `bytes` bytes at `p` once with a streaming-read

@@ -189,3 +189,72 @@ def attention_over(q, cache, sets, scale):
                 bound[r, j] = (2.0 ** -8 * np.abs(out[r, j]) + (2.0 ** -11 + 2.0 ** -19 + 4 * delta) * w
                                + len(t) * (2.0 ** -24 * w2 + 2.0 ** -27 * np.abs(v).max()))
     return out, lse, bound
+
+
+def weigh(q, lse, cache, weights, table, kv_lens, row_starts, scale, causal=True):
+    """float64 weights after a call over float32 weights [pages][heads][page_size]
+    (NaN in, NaN out where nothing is written) and a bound like them of what fp32
+    may be off. With p a row's weight and x its score, p is off by
+      (D + 8) 2^-24 scale s sum |q| (|c - mid| + |z - mid|)    the score's product
+      6 2^-24 (|x| + |lse|) + 2^-21       its scaling, the difference and exp2
+    relative to itself, and the sum of n of them by n 2^-24, the old weight's
+    addition by 2^-24."""
+    rows, q_heads, d = q.shape
+    group, mid, ps = q_heads // cache.heads, 2.0 ** (cache.bits - 1), cache.page_size
+    out, bound = weights.astype(np.float64), np.zeros(weights.shape)
+    for b, held in enumerate(kv_lens):
+        lo, hi = row_starts[b], row_starts[b + 1]
+        if hi == lo or held <= 0:
+            continue
+        pages, pos = table[b][:(held + ps - 1) // ps], np.arange(held)
+        at = np.asarray(pages)[pos // ps], pos % ps
+        for h in range(cache.heads):
+            c, s, z = cache.parts(pages, h, "k", held)
+            k, kabs = (c - z[:, None]) * s[:, None], (np.abs(c - mid) + np.abs(z - mid)[:, None]) * s[:, None]
+            total, off = np.zeros(held), np.zeros(held)
+            for r in range(lo, hi):
+                n = max(0, held - (hi - r) + 1) if causal else held
+                for j in range(h * group, (h + 1) * group):
+                    if not np.isfinite(lse[r, j]):
+                        continue
+                    y = q[r, j].astype(np.float64)
+                    x = scale * (k[:n] @ y)
+                    p = np.exp(x - lse[r, j])
+                    rel = ((d + 8) * abs(scale) * (kabs[:n] @ np.abs(y)) + 6 * (np.abs(x) + abs(lse[r, j]))) * 2.0 ** -24
+                    total[:n] += p
+                    off[:n] += p * (np.expm1(rel) + 2.0 ** -21)
+            was = out[at[0], h, at[1]]
+            if causal:
+                was = np.where(pos < held - (hi - lo), was, 0.0)
+            out[at[0], h, at[1]] = was + total
+            bound[at[0], h, at[1]] = off + ((hi - lo) * group + 8) * 2.0 ** -24 * (total + np.abs(was))
+    return out, bound
+
+
+def evict(cache, weights, table, kv_lens, keep, recent, to_table=None):
+    """Evicts in place of the oracle's cache and weights; table, to_table: lists of
+    pages of each sequence. Returns (kept [b][heads][keep], new lengths)."""
+    to_table, ps = to_table or table, cache.page_size
+    kept, lens = np.full((len(kv_lens), cache.heads, keep), -1, np.int32), []
+    names = ["k_scales", "v_scales"] + ([] if cache.symmetric else ["k_zeros", "v_zeros"])
+    for b, held in enumerate(kv_lens):
+        lens.append(min(max(held, 0), keep))
+        for h in range(cache.heads):
+            pos = np.arange(max(held, 0))
+            if held > keep:
+                w = np.array([weights[table[b][i // ps], h, i % ps] for i in range(held - recent)], np.float64)
+                # NaN is heaviest; a stable sort of the negatives keeps the earlier of equal ones
+                best = np.argsort(np.where(np.isnan(w), -np.inf, -w), kind="stable")
+                nan_first = np.concatenate([best[np.isnan(w[best])], best[~np.isnan(w[best])]])
+                pos = np.concatenate([np.sort(nan_first[:keep - recent]), np.arange(held - recent, held)])
+            kept[b, h, :len(pos)] = pos
+            src = [(table[b][i // ps], i % ps) for i in pos]
+            k = [cache.k_codes[p, h, o].copy() for p, o in src]
+            v = [cache.v_codes[p, h, o // 4, :, o % 4].copy() for p, o in src]
+            numbers = [[a[p, h, o] for p, o in src] for a in [weights] + [getattr(cache, n) for n in names]]
+            for j in range(len(pos)):
+                p, o = to_table[b][j // ps], j % ps
+                cache.k_codes[p, h, o], cache.v_codes[p, h, o // 4, :, o % 4] = k[j], v[j]
+                for a, x in zip([weights] + [getattr(cache, n) for n in names], numbers):
+                    a[p, h, o] = x[j]
+    return kept, lens

@@ -88,3 +88,79 @@ def test_attention_workspaces(lib):
     assert g(3, 8, 1, 128, 16, 0, 0, 0, 0, 2, 1024, 0, 0) == lib.paged_attention_workspace_bytes(*sizes)
     if NO_GPU:
         assert _prefix(lib, p=0, pt=None, pl=None, ps=None, mp=0, table=None, ws=None, wsb=0) == 4
+
+
+def _weigh(lib, q=E, rows=4, qh=8, qs=1024, scale=0.1, lse=F, table=G, mp=3, lens=H, starts=I, b=2, causal=1, mr=0, mk=0,
+           w=K, out=K, **kw):
+    c = _cache(**kw)
+    return lib.kv_cache_weigh(ctypes.byref(c), q, rows, qh, qs, scale, lse, table, mp, lens, starts, b, causal, mr, mk, w, out,
+                              None)
+
+
+@pytest.mark.parametrize("kwargs,status", CACHE_REFUSALS + BATCH_REFUSALS + [
+    (dict(qh=7), 1), (dict(qh=0), 1), (dict(qs=1023), 1), (dict(qs=512), 1), (dict(qs=1 << 50), 2), (dict(mk=-1), 1),
+    (dict(scale=float("nan")), 1), (dict(causal=2), 1), (dict(causal=-1), 1), (dict(q=None), 1), (dict(q=MIS), 1),
+    (dict(lse=None), 1), (dict(lse=P((12 << 32) + 2)), 1), (dict(w=MIS), 1), (dict(out=None), 1), (dict(out=MIS), 1),
+    (dict(out=A), 1), (dict(out=C), 1), (dict(out=E), 1), (dict(out=F), 1), (dict(out=G), 1), (dict(out=H), 1),
+    (dict(out=P((11 << 32) + 256)), 1),         # partly over the weights
+    (dict(rows=(1 << 30) + 1, qh=1, qs=128, heads=1), 2),
+])
+def test_weigh_refuses(lib, kwargs, status):
+    assert _weigh(lib, **kwargs) == status
+    assert lib.lq_last_error() != b""
+
+
+def test_weigh_empty_and_no_device(lib):
+    assert _weigh(lib, rows=0, table=None, lens=None, starts=None) == 0
+    assert _weigh(lib, b=0, table=None, lens=None, starts=None) == 0
+    assert _weigh(lib, mp=0, table=None) == 0
+    if NO_GPU:
+        for kw in (dict(), dict(w=None), dict(out=L), dict(causal=0), dict(symmetric=0, k_zeros=J, v_zeros=P(13 << 32))):
+            assert _weigh(lib, **kw) == 4
+
+
+def _evict(lib, w=E, table=G, mp=3, lens=H, b=2, keep=20, recent=4, to=None, tp=0, mk=0, kept=I, new=K, **kw):
+    c = _cache(**kw)
+    return lib.kv_cache_evict(ctypes.byref(c), w, table, mp, lens, b, keep, recent, to, tp, mk, kept, new, None)
+
+
+@pytest.mark.parametrize("kwargs,status", CACHE_REFUSALS + [
+    (dict(b=-1), 1), (dict(mp=-1), 1), (dict(b=65536), 2), (dict(mp=1 << 30), 2), (dict(mk=-1), 1),
+    (dict(keep=0), 1), (dict(keep=-3), 1), (dict(recent=-1), 1), (dict(recent=21), 1), (dict(keep=1 << 31), 2),
+    (dict(b=65535, heads=128, pages=1), 2),
+    (dict(table=None), 1), (dict(lens=None), 1), (dict(lens=P((9 << 32) + 2)), 1), (dict(w=None), 1), (dict(w=MIS), 1),
+    (dict(kept=None), 1), (dict(new=None), 1), (dict(new=P((9 << 32) + 2)), 1),
+    (dict(to=L, tp=1), 1),                      # room for 16 of 20 tokens
+    (dict(to=L, tp=-1), 1), (dict(to=L, tp=1 << 30), 2), (dict(to=P((9 << 32) + 2), tp=3), 1),
+    (dict(kept=G), 1), (dict(kept=H), 1), (dict(kept=K), 1), (dict(new=G), 1), (dict(w=A), 1), (dict(w=G), 1),
+    (dict(new=P((8 << 32) + 4)), 1),            # partly over kv_lens
+    (dict(to=L, tp=2, new=L), 1),
+])
+def test_evict_refuses(lib, kwargs, status):
+    assert _evict(lib, **kwargs) == status
+    assert lib.lq_last_error() != b""
+
+
+def test_evict_empty_and_no_device(lib):
+    assert _evict(lib, b=0, table=None, lens=None, w=None) == 0
+    if NO_GPU:
+        for kw in (dict(), dict(new=H), dict(to=L, tp=2), dict(mp=0, table=None), dict(keep=20, mp=1), dict(keep=1 << 20)):
+            assert _evict(lib, **kw) == 4
+
+
+def test_binding_refuses_tensors_on_the_cpu():
+    q = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
+    t = torch.zeros((1, 1), dtype=torch.int32)
+
+    class Cache:
+        _index, head_dim, heads, device, k_scales = 0, 64, 1, "cuda:0", torch.zeros((1, 1, 16))
+
+    for call in (lambda: bg.cross_attention(q, Cache, t, t[0], t[0]),
+                 lambda: bg.kv_cache_weigh(q, q[..., 0].float(), Cache, None, t, t[0], t[0]),
+                 lambda: bg.kv_cache_evict(Cache, Cache.k_scales, t, t[0], 4),
+                 lambda: bg.prefix_attention(q, Cache, t, t[0], t[0], t, t[0], t[0])):
+        with pytest.raises(ValueError, match="GPU|the cache"):
+            call()
+    for bad in (lambda: bg.kv_cache_evict(Cache, q, t[0], t[0], 4), lambda: bg.prefix_attention(q, Cache, t[0], t, t, t, t, t)):
+        with pytest.raises(ValueError, match="must be a tensor"):
+            bad()
