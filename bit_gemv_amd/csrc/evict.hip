@@ -7,9 +7,11 @@
 // narrowed down to the lightest one that stays in three passes over a histogram
 // of 11 or 10 bits; two more passes count and write the positions in order.
 // evict_move_kernel moves codes, scales, zeros and weights to the front of the
-// table's pages. Its tokens move to earlier positions or stay, in order: a batch
-// of tokens is read whole before any of it is written, and what later batches
-// read lies behind what earlier ones write, so a table may be its own target.
+// table's pages. In place tokens move to earlier positions or stay, in order: a
+// batch of tokens is read whole before any of it is written, and what later
+// batches read lies behind what earlier ones write, so one block takes all tokens
+// of a sequence and head, or of some bytes of their codes. Into other pages the
+// tokens are shared out as well.
 #include "common.hpp"
 #include "kv.hpp"
 
@@ -17,8 +19,8 @@ namespace lq {
 
 namespace {
 
-constexpr int kSelect = 1024;   // threads of a selecting block
-constexpr int kHeld = 32768;    // weights held in LDS; longer sequences read the others anew
+constexpr int kSelect = 1024;  // threads of a selecting block
+constexpr int kHeld = 32;      // weights a thread holds; longer sequences read the others anew
 constexpr int kBins = 2048;
 
 // Weights as unsigned numbers that order as they do, -0 as 0; NaN is heaviest.
@@ -38,47 +40,72 @@ LQ_DEVICE int lanes_below(uint64_t mask) {
 }
 
 __global__ __launch_bounds__(kSelect) void evict_select_kernel(EvictArgs a) {
-    __shared__ uint32_t held[kHeld];
     __shared__ uint32_t bins[kBins];
     __shared__ uint32_t sums[2][kSelect / 64];
     __shared__ uint32_t found[2];  // the digit, and how many heavier weights stay
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = blockIdx.x % a.c.heads;
     const int64_t seq = blockIdx.x / a.c.heads;
-    const int64_t len = held_of(a, seq);
+    const int len = (int)held_of(a, seq), keep = (int)a.keep, recent = (int)a.recent;
     int32_t *const kept = a.kept + ((int64_t)seq * a.c.heads + h) * a.keep;
-    const int64_t left = len < a.keep ? len : a.keep;
-    for (int64_t i = left + threadIdx.x; i < a.keep; i += kSelect) kept[i] = -1;
-    if (len <= a.keep) {
-        for (int64_t i = threadIdx.x; i < len; i += kSelect) kept[i] = (int32_t)i;
+    for (int i = (len < keep ? len : keep) + threadIdx.x; i < keep; i += kSelect) kept[i] = -1;
+    if (len <= keep) {
+        for (int i = threadIdx.x; i < len; i += kSelect) kept[i] = i;
         return;
     }
-    const int64_t old = len - a.recent;              // positions to choose among
-    const uint32_t want = (uint32_t)(a.keep - a.recent);
-    for (int64_t i = threadIdx.x; i < a.recent; i += kSelect) kept[want + i] = (int32_t)(old + i);
+    const int old = len - recent;  // positions to choose among
+    const uint32_t want = (uint32_t)(keep - recent);
+    for (int i = threadIdx.x; i < recent; i += kSelect) kept[want + i] = old + i;
     if (want == 0) return;
 
+    // A wave a run of positions, 64 side by side at a time.
+    const int groups = (old + kSelect - 1) / kSelect, first = wave * groups * 64 + lane;
     const int32_t *const table = a.table + seq * a.max_pages;
     const int shift = a.c.page_shift, mask = (1 << shift) - 1;
-    auto weight = [&](int64_t i) {
-        const int64_t page = table[i >> shift];
-        // a position outside the pool goes first
-        if (page < 0 || page >= a.c.pages) return 0u;
-        return order_of(a.weights[((page * a.c.heads + h) << shift) + (i & mask)]);
+    const int pages = (int)a.c.pages;
+    auto weight = [&](int page, int i) {
+        const bool in = (uint32_t)page < (uint32_t)pages;
+        const float w = a.weights[(((int64_t)(in ? page : 0) * a.c.heads + h) << shift) + (i & mask)];
+        return in ? order_of(w) : 0u;  // a position outside the pool goes first
     };
-    const int64_t in_lds = old < kHeld ? old : kHeld;
-    for (int64_t i = threadIdx.x; i < in_lds; i += kSelect) held[i] = weight(i);
-    auto at = [&](int64_t i) { return i < kHeld ? held[i] : weight(i); };
+    uint32_t u[kHeld];
+#pragma unroll
+    for (int r0 = 0; r0 < kHeld; r0 += 8)
+        if (r0 < groups) {  // eight lookups and loads in flight
+            int i[8], page[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                i[r] = first + 64 * (r0 + r);
+                i[r] = i[r] < old ? i[r] : old - 1;
+                page[r] = table[i[r] >> shift];
+            }
+#pragma unroll
+            for (int r = 0; r < 8; ++r) u[r0 + r] = weight(page[r], i[r]);
+        }
+    // f(position's weight, position, whether it is one) for all of the wave's
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int r0 = 0; r0 < kHeld; r0 += 8)
+            if (r0 < groups) {
+#pragma unroll
+                for (int r = r0; r < r0 + 8; ++r) f(u[r], first + 64 * r, r < groups && first + 64 * r < old);
+            }
+        for (int r = kHeld; r < groups; ++r) {
+            const int i = first + 64 * r, c = i < old ? i : old - 1;
+            f(weight(table[c >> shift], c), i, i < old);
+        }
+    };
 
     uint32_t known = 0, known_mask = 0, need = want;
     for (int pass = 0; pass < 3; ++pass) {
-        const int bits = pass < 2 ? 11 : 10, down = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const int down = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const uint32_t digit = pass < 2 ? kBins - 1 : kBins / 2 - 1;
         for (int i = threadIdx.x; i < kBins; i += kSelect) bins[i] = 0;
         __syncthreads();
-        for (int64_t i = threadIdx.x; i < old; i += kSelect) {
-            const uint32_t u = at(i);
-            if ((u & known_mask) == known) atomicAdd(&bins[(u >> down) & (kBins - 1) & ((1u << bits) - 1)], 1u);
-        }
+        each([&](uint32_t x, int, bool in) {
+            if (in && (x & known_mask) == known) atomicAdd(&bins[(x >> down) & digit], 1u);
+        });
         __syncthreads();
         // two bins a thread, from the heaviest down: the one where the count passes need
         const uint32_t hi = bins[kBins - 1 - 2 * threadIdx.x], lo = bins[kBins - 2 - 2 * threadIdx.x];
@@ -90,29 +117,25 @@ __global__ __launch_bounds__(kSelect) void evict_select_kernel(EvictArgs a) {
         }
         if (lane == 63) sums[0][wave] = upto;
         __syncthreads();
-        uint32_t before = 0;
-        for (int w = 0; w < wave; ++w) before += sums[0][w];
-        upto += before;
+        for (int w = 0; w < wave; ++w) upto += sums[0][w];
         const uint32_t heavier = upto - hi - lo;
         if (heavier < need && upto >= need) {
-            const bool first = heavier + hi >= need;
-            found[0] = kBins - (first ? 1 : 2) - 2 * threadIdx.x;
-            found[1] = first ? heavier : heavier + hi;
+            const bool one = heavier + hi >= need;
+            found[0] = kBins - (one ? 1 : 2) - 2 * threadIdx.x;
+            found[1] = one ? heavier : heavier + hi;
         }
         __syncthreads();
         known |= found[0] << down;
-        known_mask |= ((1u << bits) - 1) << down;
+        known_mask |= digit << down;
         need -= found[1];
     }
-    // All weights above `known` stay, and the first `need` of those equal to it.
-    // A wave a run of positions: counts, then places.
-    const int64_t run = ((old + kSelect - 1) / kSelect) * 64, i0 = wave * run, i1 = i0 + run < old ? i0 + run : old;
+    // All weights above `known` stay, and the first `need` of those equal to it:
+    // counts of the waves' runs, then places.
     uint32_t above = 0, equal = 0;
-    for (int64_t i = i0; i < i1; i += 64) {
-        const uint32_t u = i + lane < i1 ? at(i + lane) : 0;
-        above += __popcll(__ballot(i + lane < i1 && u > known));
-        equal += __popcll(__ballot(i + lane < i1 && u == known));
-    }
+    each([&](uint32_t x, int, bool in) {
+        above += __popcll(__ballot(in && x > known));
+        equal += __popcll(__ballot(in && x == known));
+    });
     if (lane == 0) {
         sums[0][wave] = above;
         sums[1][wave] = equal;
@@ -123,129 +146,163 @@ __global__ __launch_bounds__(kSelect) void evict_select_kernel(EvictArgs a) {
         above += sums[0][w];
         equal += sums[1][w];
     }
-    for (int64_t i = i0; i < i1; i += 64) {
-        const bool in = i + lane < i1;
-        const uint32_t u = in ? at(i + lane) : 0;
-        const uint64_t gt = __ballot(in && u > known), eq = __ballot(in && u == known);
+    each([&](uint32_t x, int i, bool in) {
+        const uint64_t gt = __ballot(in && x > known), eq = __ballot(in && x == known);
         const uint32_t e = equal + lanes_below(eq);
         const uint32_t to = above + lanes_below(gt) + (e < need ? e : need);
-        if (in && (u > known || (u == known && e < need))) kept[to] = (int32_t)(i + lane);
+        if (in && (x > known || (x == known && e < need))) kept[to] = i;
         above += __popcll(gt);
         equal += __popcll(eq);
-    }
+    });
 }
 
-// What a block of evict_move_kernel moves: keys' codes, values' codes, or the
-// 4-byte numbers.
-enum { kKeys, kValues, kNumbers, kRoles };
-constexpr int kMove = 256;
+// How the moving is shared out: blocks of a sequence and head take the 4-byte
+// numbers, one of `keys` parts of the keys' code bytes or one of `values` parts
+// of the values', of every `splits`th batch of tokens.
+struct Shares {
+    int keys, values, splits;
+};
+constexpr int kMove = 512;
+constexpr int kBatch = 1024;  // tokens
 
 template <int ROW>  // code bytes of a token
-__global__ __launch_bounds__(kMove) void evict_move_kernel(EvictArgs a) {
+__global__ __launch_bounds__(kMove) void evict_move_kernel(EvictArgs a, Shares sh) {
+    __shared__ int64_t from[kBatch], to[kBatch];  // slots of the head's tokens, or -1
+    const int roles = 1 + sh.keys + sh.values;
     const int h = blockIdx.x % a.c.heads;
-    const int role = blockIdx.x / a.c.heads % kRoles;
-    const int64_t seq = blockIdx.x / a.c.heads / kRoles;
+    const int role = blockIdx.x / a.c.heads % roles;
+    const int split = blockIdx.x / a.c.heads / roles % sh.splits;
+    const int64_t seq = blockIdx.x / a.c.heads / roles / sh.splits;
     const int64_t len = held_of(a, seq);
     const int count = (int)(len < a.keep ? len : a.keep);
-    if (role == kNumbers && h == 0 && threadIdx.x == 0) a.new_lens[seq] = count;
+    if (role == 0 && h == 0 && split == 0 && threadIdx.x == 0) a.new_lens[seq] = count;
     if (len <= a.keep && a.to_table == a.table) return;  // all stays where it is
     const int32_t *const kept = a.kept + ((int64_t)seq * a.c.heads + h) * a.keep;
     const int32_t *const table = a.table + seq * a.max_pages, *const to_table = a.to_table + seq * a.to_pages;
     const int shift = a.c.page_shift, mask = (1 << shift) - 1;
-    // slots of a head's token, or -1
-    auto slot_of = [&](const int32_t *tab, int64_t pos) -> int64_t {
+    auto slot_of = [&](const int32_t *tab, int pos) -> int64_t {
         const int64_t page = tab[pos >> shift];
         return page < 0 || page >= a.c.pages ? -1 : ((page * a.c.heads + h) << shift) + (pos & mask);
     };
-    if (role == kKeys) {
-        constexpr int TPT = ROW / 16, U = 4, T = kMove / TPT * U;  // threads a token, tokens a thread, tokens a batch
-        const int c = threadIdx.x % TPT, t = threadIdx.x / TPT;
-        for (int j0 = 0; j0 < count; j0 += T) {
-            u32x4 v[U];
-            int64_t to[U];
+    for (int64_t at = (int64_t)split * kBatch; at < count; at += (int64_t)sh.splits * kBatch) {
+        const int j0 = (int)at, n = count - j0 < kBatch ? count - j0 : kBatch;
+        __syncthreads();  // nobody reads the last lookups any more
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int j = j0 + t + u * (kMove / TPT);
-                to[u] = -1;
-                if (j < count) {
-                    const int64_t from = slot_of(table, kept[j]);
-                    to[u] = slot_of(to_table, j);
-                    if (from < 0) to[u] = -1;
-                    else v[u] = *reinterpret_cast<const u32x4 *>(a.c.k_codes + from * ROW + 16 * c);
-                }
+        for (int u = 0; u < kBatch / kMove; ++u) {
+            const int i = threadIdx.x + u * kMove;
+            if (i < n) {
+                from[i] = slot_of(table, kept[j0 + i]);
+                to[i] = slot_of(to_table, j0 + i);
+            }
+        }
+        __syncthreads();
+        if (role == 0) {
+            float *const src[5] = {a.weights, a.c.k_scales, a.c.v_scales, a.c.k_zeros, a.c.v_zeros};
+            const int arrays = a.c.symmetric ? 3 : 5;
+            float v[kBatch / kMove][5];
+#pragma unroll
+            for (int u = 0; u < kBatch / kMove; ++u) {
+                const int i = threadIdx.x + u * kMove;
+#pragma unroll
+                for (int x = 0; x < 5; ++x)
+                    if (x < arrays && i < n && from[i] >= 0) v[u][x] = src[x][from[i]];
             }
             __syncthreads();
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (to[u] >= 0) *reinterpret_cast<u32x4 *>(a.c.k_codes + to[u] * ROW + 16 * c) = v[u];
-        }
-    } else if (role == kValues) {
-        constexpr int TPQ = ROW / 4, U = 2, Q = kMove / TPQ * U;  // threads a quad of tokens (16 bytes each), ...
-        const int c = threadIdx.x % TPQ, t = threadIdx.x / TPQ;
-        for (int q0 = 0; 4 * q0 < count; q0 += Q) {
-            u32x4 v[U];
-            int64_t to[U];
+            for (int u = 0; u < kBatch / kMove; ++u) {
+                const int i = threadIdx.x + u * kMove;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int q = q0 + t + u * (kMove / TPQ);
-                to[u] = -1;
-                v[u] = u32x4{0u, 0u, 0u, 0u};
-                if (4 * q < count) {
-                    to[u] = slot_of(to_table, 4 * q);
-                    // byte o of each word is token 4 q + o's
+                for (int x = 0; x < 5; ++x)
+                    if (x < arrays && i < n && from[i] >= 0 && to[i] >= 0) src[x][to[i]] = v[u][x];
+            }
+        } else if (role <= sh.keys) {
+            constexpr int U = 4;
+            const int width = ROW / 16 / sh.keys;                      // threads a token
+            const int c = threadIdx.x % width + (role - 1) * width, t = threadIdx.x / width, step = kMove / width;
+            for (int i0 = 0; i0 < n; i0 += U * step) {
+                u32x4 v[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = i0 + t + u * step;
+                    if (i < n && from[i] >= 0) v[u] = *reinterpret_cast<const u32x4 *>(a.c.k_codes + from[i] * ROW + 16 * c);
+                }
+                __syncthreads();
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = i0 + t + u * step;
+                    if (i < n && from[i] >= 0 && to[i] >= 0)
+                        *reinterpret_cast<u32x4 *>(a.c.k_codes + to[i] * ROW + 16 * c) = v[u];
+                }
+            }
+        } else {
+            // Four tokens of a quad and 16 bytes of their words a thread: byte o of
+            // each word is token o's. Behind the last token the last one again.
+            constexpr int U = 2;
+            const int width = ROW / 4 / sh.values;
+            const int c = threadIdx.x % width + (role - 1 - sh.keys) * width, t = threadIdx.x / width, step = kMove / width;
+            for (int q0 = 0; 4 * q0 < n; q0 += U * step) {
+                u32x4 w[U][4];
+                int64_t s[U][4];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int o = 0; o < 4; ++o) {
-                        const int j = 4 * q + o < count ? 4 * q + o : count - 1;
-                        const int64_t from = slot_of(table, kept[j]);
-                        if (from < 0) continue;
-                        const u32x4 w = *reinterpret_cast<const u32x4 *>(a.c.v_codes + (from >> 2) * (4 * ROW) + 16 * c);
-                        const int down = 8 * (int)(from & 3);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) v[u][i] |= ((w[i] >> down) & 255u) << (8 * o);
+                        const int i = 4 * (q0 + t + u * step) + o;
+                        s[u][o] = from[i < n ? i : n - 1];
+                        w[u][o] = *reinterpret_cast<const u32x4 *>(a.c.v_codes + (s[u][o] < 0 ? 0 : s[u][o] >> 2) * (4 * ROW) + 16 * c);
                     }
+                __syncthreads();
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = 4 * (q0 + t + u * step);
+                    // selectors of two bytes each: the first token's, then the other's
+                    const uint32_t s01 = 0x0C0C0400u + (uint32_t)(s[u][0] & 3) + ((uint32_t)(s[u][1] & 3) << 8);
+                    const uint32_t s23 = 0x04000C0Cu + ((uint32_t)(s[u][2] & 3) << 16) + ((uint32_t)(s[u][3] & 3) << 24);
+                    u32x4 v;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        v[x] = __builtin_amdgcn_perm(w[u][1][x], w[u][0][x], s01) | __builtin_amdgcn_perm(w[u][3][x], w[u][2][x], s23);
+                    if (i < n && to[i] >= 0) *reinterpret_cast<u32x4 *>(a.c.v_codes + (to[i] >> 2) * (4 * ROW) + 16 * c) = v;
                 }
             }
-            __syncthreads();
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (to[u] >= 0) *reinterpret_cast<u32x4 *>(a.c.v_codes + (to[u] >> 2) * (4 * ROW) + 16 * c) = v[u];
-        }
-    } else {
-        float *const src[5] = {a.weights, a.c.k_scales, a.c.v_scales, a.c.k_zeros, a.c.v_zeros};
-        const int n = a.c.symmetric ? 3 : 5;
-        for (int j0 = 0; j0 < count; j0 += kMove) {
-            float v[5];
-            int64_t from = -1, to = -1;
-            const int j = j0 + threadIdx.x;
-            if (j < count) {
-                from = slot_of(table, kept[j]);
-                to = slot_of(to_table, j);
-            }
-#pragma unroll
-            for (int i = 0; i < 5; ++i)
-                if (i < n && from >= 0) v[i] = src[i][from];
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < 5; ++i)
-                if (i < n && from >= 0 && to >= 0) src[i][to] = v[i];
         }
     }
 }
 
 }  // namespace
 
+template <int ROW>
+static hipError_t launch_move(const EvictArgs &a, hipStream_t st) {
+    const int64_t pairs = a.b * a.c.heads, room = a.max_pages << a.c.page_shift;
+    int64_t kv = a.max_kv <= 0 || a.max_kv > room ? room : a.max_kv;
+    if (kv > a.keep) kv = a.keep;  // tokens that may move
+    Shares sh{1, 1, 1};
+    // Two blocks of 512 threads a CU and a few rounds of them: values first, which
+    // read four bytes for one
+    while (sh.values < ROW / 16 && pairs * (sh.keys + sh.values) < 512) {
+        if (sh.keys < sh.values && sh.keys < ROW / 32) sh.keys *= 2;
+        else sh.values *= 2;
+    }
+    if (a.to_table != a.table) {
+        const int64_t most = (kv + kBatch - 1) / kBatch;  // a batch a block
+        const int64_t fill = 2048 / (pairs * (sh.keys + sh.values)) + 1;
+        sh.splits = (int)(fill < most ? fill : most < 1 ? 1 : most);
+    }
+    const uint32_t blocks = (uint32_t)(pairs * (1 + sh.keys + sh.values) * sh.splits);
+    hipLaunchKernelGGL(evict_move_kernel<ROW>, dim3(blocks), dim3(kMove), 0, st, a, sh);
+    return hipGetLastError();
+}
+
 hipError_t launch_kv_evict(const EvictArgs &a, hipStream_t st) {
-    const uint32_t blocks = (uint32_t)(a.b * a.c.heads);
-    hipLaunchKernelGGL(evict_select_kernel, dim3(blocks), dim3(kSelect), 0, st, a);
+    hipLaunchKernelGGL(evict_select_kernel, dim3((uint32_t)(a.b * a.c.heads)), dim3(kSelect), 0, st, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     switch (a.c.head_dim * a.c.bits / 8) {
-        case 32: hipLaunchKernelGGL(evict_move_kernel<32>, dim3(blocks * kRoles), dim3(kMove), 0, st, a); break;
-        case 64: hipLaunchKernelGGL(evict_move_kernel<64>, dim3(blocks * kRoles), dim3(kMove), 0, st, a); break;
-        case 128: hipLaunchKernelGGL(evict_move_kernel<128>, dim3(blocks * kRoles), dim3(kMove), 0, st, a); break;
-        default: hipLaunchKernelGGL(evict_move_kernel<256>, dim3(blocks * kRoles), dim3(kMove), 0, st, a); break;
+        case 32: return launch_move<32>(a, st);
+        case 64: return launch_move<64>(a, st);
+        case 128: return launch_move<128>(a, st);
+        default: return launch_move<256>(a, st);
     }
-    return hipGetLastError();
 }
 
 }  // namespace lq
