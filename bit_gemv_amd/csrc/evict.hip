@@ -19,8 +19,7 @@ namespace lq {
 
 namespace {
 
-constexpr int kSelect = 1024;  // threads of a selecting block
-constexpr int kHeld = 32;      // weights a thread holds; longer sequences read the others anew
+constexpr int kHeld = 32;  // weights a thread holds; longer sequences read the others anew
 constexpr int kBins = 2048;
 
 // Weights as unsigned numbers that order as they do, -0 as 0; NaN is heaviest.
@@ -39,28 +38,29 @@ LQ_DEVICE int lanes_below(uint64_t mask) {
     return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
 }
 
-__global__ __launch_bounds__(kSelect) void evict_select_kernel(EvictArgs a) {
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void evict_select_kernel(EvictArgs a) {
     __shared__ uint32_t bins[kBins];
-    __shared__ uint32_t sums[2][kSelect / 64];
-    __shared__ uint32_t found[2];  // the digit, and how many heavier weights stay
+    __shared__ uint32_t sums[2][THREADS / 64];
+    __shared__ uint32_t found[3];  // the digit, how many heavier weights stay, whether all of its do
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h = blockIdx.x % a.c.heads;
     const int64_t seq = blockIdx.x / a.c.heads;
     const int len = (int)held_of(a, seq), keep = (int)a.keep, recent = (int)a.recent;
     int32_t *const kept = a.kept + ((int64_t)seq * a.c.heads + h) * a.keep;
-    for (int i = (len < keep ? len : keep) + threadIdx.x; i < keep; i += kSelect) kept[i] = -1;
+    for (int i = (len < keep ? len : keep) + threadIdx.x; i < keep; i += THREADS) kept[i] = -1;
     if (len <= keep) {
-        for (int i = threadIdx.x; i < len; i += kSelect) kept[i] = i;
+        for (int i = threadIdx.x; i < len; i += THREADS) kept[i] = i;
         return;
     }
     const int old = len - recent;  // positions to choose among
     const uint32_t want = (uint32_t)(keep - recent);
-    for (int i = threadIdx.x; i < recent; i += kSelect) kept[want + i] = old + i;
+    for (int i = threadIdx.x; i < recent; i += THREADS) kept[want + i] = old + i;
     if (want == 0) return;
 
     // A wave a run of positions, 64 side by side at a time.
-    const int groups = (old + kSelect - 1) / kSelect, first = wave * groups * 64 + lane;
+    const int groups = (old + THREADS - 1) / THREADS, first = wave * groups * 64 + lane;
     const int32_t *const table = a.table + seq * a.max_pages;
     const int shift = a.c.page_shift, mask = (1 << shift) - 1;
     const int pages = (int)a.c.pages;
@@ -69,31 +69,42 @@ __global__ __launch_bounds__(kSelect) void evict_select_kernel(EvictArgs a) {
         const float w = a.weights[(((int64_t)(in ? page : 0) * a.c.heads + h) << shift) + (i & mask)];
         return in ? order_of(w) : 0u;  // a position outside the pool goes first
     };
-    uint32_t u[kHeld];
+    // Places of the run behind the last position hold 0 as well: of equal ones
+    // they come last, and there are enough before them.
+    uint32_t u[kHeld] = {};
+    int entry[kHeld / 16];  // pages of 1024 positions, at most 64, one a lane
 #pragma unroll
-    for (int r0 = 0; r0 < kHeld; r0 += 8)
-        if (r0 < groups) {  // eight lookups and loads in flight
-            int i[8], page[8];
+    for (int c = 0; c < kHeld / 16; ++c) {
+        const int page0 = ((first - lane) >> shift) + (1024 * c >> shift) + lane, last = (old - 1) >> shift;
+        entry[c] = 16 * c < groups ? table[page0 < last ? page0 : last] : 0;
+    }
+    uint32_t none = 0;  // bit r: u[r] is no weight
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                i[r] = first + 64 * (r0 + r);
-                i[r] = i[r] < old ? i[r] : old - 1;
-                page[r] = table[i[r] >> shift];
+    for (int r0 = 0; r0 < kHeld; r0 += 4)
+        if (r0 < groups) {  // no load is waited for here
+#pragma unroll
+            for (int r = r0; r < r0 + 4; ++r) {
+                const int i = first + 64 * r, page0 = ((first - lane) >> shift) + (1024 * (r / 16) >> shift);
+                const int page = __shfl(entry[r / 16], (i >> shift) - page0);
+                const bool in = (uint32_t)page < (uint32_t)pages;
+                u[r] = __float_as_uint(a.weights[(((int64_t)(in ? page : 0) * a.c.heads + h) << shift) + (i & mask)]);
+                none |= (in && i < old ? 0u : 1u) << r;
             }
-#pragma unroll
-            for (int r = 0; r < 8; ++r) u[r0 + r] = weight(page[r], i[r]);
         }
-    // f(position's weight, position, whether it is one) for all of the wave's
+#pragma unroll
+    for (int r0 = 0; r0 < kHeld; r0 += 4)
+        if (r0 < groups) {
+#pragma unroll
+            for (int r = r0; r < r0 + 4; ++r) u[r] = (none >> r) & 1u ? 0u : order_of(__uint_as_float(u[r]));
+        }
+    // f(position's weight, position) for all of the wave's
     auto each = [&](auto f) {
 #pragma unroll
-        for (int r0 = 0; r0 < kHeld; r0 += 8)
-            if (r0 < groups) {
-#pragma unroll
-                for (int r = r0; r < r0 + 8; ++r) f(u[r], first + 64 * r, r < groups && first + 64 * r < old);
-            }
+        for (int r = 0; r < kHeld; ++r)
+            if (r < groups) f(u[r], first + 64 * r);
         for (int r = kHeld; r < groups; ++r) {
             const int i = first + 64 * r, c = i < old ? i : old - 1;
-            f(weight(table[c >> shift], c), i, i < old);
+            f(i < old ? weight(table[c >> shift], c) : 0u, i);
         }
     };
 
@@ -101,15 +112,19 @@ __global__ __launch_bounds__(kSelect) void evict_select_kernel(EvictArgs a) {
     for (int pass = 0; pass < 3; ++pass) {
         const int down = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const uint32_t digit = pass < 2 ? kBins - 1 : kBins / 2 - 1;
-        for (int i = threadIdx.x; i < kBins; i += kSelect) bins[i] = 0;
+        for (int i = threadIdx.x; i < kBins; i += THREADS) bins[i] = 0;
         __syncthreads();
-        each([&](uint32_t x, int, bool in) {
-            if (in && (x & known_mask) == known) atomicAdd(&bins[(x >> down) & digit], 1u);
+        each([&](uint32_t x, int) {
+            if ((x & known_mask) == known) atomicAdd(&bins[(x >> down) & digit], 1u);
         });
         __syncthreads();
-        // two bins a thread, from the heaviest down: the one where the count passes need
-        const uint32_t hi = bins[kBins - 1 - 2 * threadIdx.x], lo = bins[kBins - 2 - 2 * threadIdx.x];
-        uint32_t upto = hi + lo;
+        // runs of bins a thread, from the heaviest down: the one where the count
+        // passes need
+        constexpr int PER = kBins / THREADS;
+        uint32_t n[PER], upto = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) upto += n[i] = bins[kBins - 1 - PER * threadIdx.x - i];
+        const uint32_t mine = upto;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const uint32_t v = __shfl_up(upto, d);
@@ -117,24 +132,36 @@ __global__ __launch_bounds__(kSelect) void evict_select_kernel(EvictArgs a) {
         }
         if (lane == 63) sums[0][wave] = upto;
         __syncthreads();
-        for (int w = 0; w < wave; ++w) upto += sums[0][w];
-        const uint32_t heavier = upto - hi - lo;
+#pragma unroll
+        for (int w = 0; w < THREADS / 64; ++w) upto += w < wave ? sums[0][w] : 0;
+        uint32_t heavier = upto - mine;
         if (heavier < need && upto >= need) {
-            const bool one = heavier + hi >= need;
-            found[0] = kBins - (one ? 1 : 2) - 2 * threadIdx.x;
-            found[1] = one ? heavier : heavier + hi;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                if (heavier < need && heavier + n[i] >= need) {
+                    found[0] = kBins - 1 - PER * threadIdx.x - i;
+                    found[1] = heavier;
+                    found[2] = heavier + n[i] == need;
+                }
+                heavier += n[i];
+            }
         }
         __syncthreads();
         known |= found[0] << down;
         known_mask |= digit << down;
         need -= found[1];
+        if (found[2] && known != 0) {  // all with these digits stay: all above the next lower number
+            known -= 1;
+            need = 0;
+            break;
+        }
     }
     // All weights above `known` stay, and the first `need` of those equal to it:
     // counts of the waves' runs, then places.
     uint32_t above = 0, equal = 0;
-    each([&](uint32_t x, int, bool in) {
-        above += __popcll(__ballot(in && x > known));
-        equal += __popcll(__ballot(in && x == known));
+    each([&](uint32_t x, int) {
+        above += __popcll(__ballot(x > known));
+        equal += __popcll(__ballot(x == known));
     });
     if (lane == 0) {
         sums[0][wave] = above;
@@ -142,15 +169,16 @@ __global__ __launch_bounds__(kSelect) void evict_select_kernel(EvictArgs a) {
     }
     __syncthreads();
     above = equal = 0;
-    for (int w = 0; w < wave; ++w) {
-        above += sums[0][w];
-        equal += sums[1][w];
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w) {
+        above += w < wave ? sums[0][w] : 0;
+        equal += w < wave ? sums[1][w] : 0;
     }
-    each([&](uint32_t x, int i, bool in) {
-        const uint64_t gt = __ballot(in && x > known), eq = __ballot(in && x == known);
+    each([&](uint32_t x, int i) {
+        const uint64_t gt = __ballot(x > known), eq = __ballot(x == known);
         const uint32_t e = equal + lanes_below(eq);
         const uint32_t to = above + lanes_below(gt) + (e < need ? e : need);
-        if (in && (x > known || (x == known && e < need))) kept[to] = i;
+        if (x > known || (x == known && e < need)) kept[to] = i;
         above += __popcll(gt);
         equal += __popcll(eq);
     });
@@ -293,9 +321,19 @@ static hipError_t launch_move(const EvictArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
+template <int THREADS>
+static hipError_t launch_select(const EvictArgs &a, hipStream_t st) {
+    hipLaunchKernelGGL(evict_select_kernel<THREADS>, dim3((uint32_t)(a.b * a.c.heads)), dim3(THREADS), 0, st, a);
+    return hipGetLastError();
+}
+
 hipError_t launch_kv_evict(const EvictArgs &a, hipStream_t st) {
-    hipLaunchKernelGGL(evict_select_kernel, dim3((uint32_t)(a.b * a.c.heads)), dim3(kSelect), 0, st, a);
-    hipError_t e = hipGetLastError();
+    // Fewer waves meet at fewer barriers, more hold longer sequences. 256, 512
+    // and 1024 threads: 1003 tokens 6.4, 7.8 and 8.7 us; up to 8192 (16 sequences
+    // of 8 heads) 17.7, 15.0 and 16.3; up to 30000 (6 of 32) 180, 74 and 28.
+    const int64_t room = a.max_pages << a.c.page_shift, kv = a.max_kv <= 0 || a.max_kv > room ? room : a.max_kv;
+    hipError_t e = kv <= 4096 ? launch_select<256>(a, st) : kv <= 512 * kHeld ? launch_select<512>(a, st)
+                                                                              : launch_select<1024>(a, st);
     if (e != hipSuccess) return e;
     switch (a.c.head_dim * a.c.bits / 8) {
         case 32: return launch_move<32>(a, st);
