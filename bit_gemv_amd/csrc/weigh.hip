@@ -13,6 +13,8 @@
 #include "codes.hpp"
 #include "kv.hpp"
 
+#include <type_traits>
+
 namespace lq {
 
 namespace {
@@ -256,202 +258,243 @@ __global__ __launch_bounds__(64 * kWaves, 3) void weigh_few_kernel(WeighArgs a, 
     }
 }
 
-// ---- many rows: KT keys in a block's registers, rows streamed past them ----
+// ---- many rows: keys in the waves' registers, rows streamed past them ----
 //
 // The codes less their zeros are integers of up to 9 bits, which bf16 holds
-// exactly, so the rows are multiplied as they lie. The block turns the codes
-// into operands once, through LDS, and all four waves keep all of them; wave w
-// takes the row tiles w, w + 4, ..., the next one's loads in flight.
-template <int D, int BITS, int KT>
+// exactly, so the rows are multiplied as they lie. Each wave turns the codes of
+// TILES x 16 keys into operands once and keeps them; WK waves have keys of their
+// own and 4 / WK waves take turns at the rows, whose tiles the block brings
+// through two buffers in LDS. A lane's operands are one run of its key's bytes:
+// of the products' D terms step s takes the 8-element chunks g S + s.
+template <int D, int BITS, int TILES, int WK>
 struct Many {
-    static constexpr int kRow = D * BITS / 8;
-    static constexpr int TPK = 64 * kWaves / KT;     // threads a key
-    static constexpr int PIECES = D / TPK / 8;       // operands of 8 codes a thread
-    static constexpr int WORDS = kRow / TPK / 4;     // code words a thread
-    static constexpr int S = D / 32;                 // MFMAs per 16 keys
-    static constexpr int TILES = KT / 16;
+    static constexpr int WR = kWaves / WK;
+    static constexpr int KT = 16 * TILES * WK;        // keys of a block
+    static constexpr int S = D / 32;                  // MFMAs per 16 keys
+    static constexpr int RT = WR == 1 ? 2 : 1;        // row tiles of a wave and stage
+    static constexpr int ROWS = 16 * WR * RT;         // rows of a stage
+    static constexpr int CHUNKS = D / 8;              // of 8 elements, a row
+    static constexpr int LOADS = ROWS * CHUNKS / (64 * kWaves);  // chunks a thread and stage
+    static constexpr int WORDS = S * BITS / 4;        // code words of a lane and key
     static constexpr float kMid = (float)(1 << (BITS - 1));
-    struct Rows {
-        u32x4 raw[S];
-        float lse;
+    struct Stage {
+        u32x4 ops[WR * RT][S][64];  // lane (n, g) in the place g 16 + (n ^ its chunk mod 16)
+        float minus[ROWS];          // -lse in log2, -inf for a row that adds nothing
+        int sees[ROWS];             // last position it sees
+    };
+    struct Load {
+        u32x4 raw[LOADS];
+        float lse[LOADS];
     };
 };
 
-template <int D, int BITS, bool SYM, int KT>
-__global__ __launch_bounds__(64 * kWaves, 2) void weigh_many_kernel(WeighArgs a, int cap) {
-    using C = Many<D, BITS, KT>;
-    __shared__ bf16x8 ops[C::TILES][C::S][64];
-    __shared__ float key_scale[KT], rest[KT], part[kWaves][KT];
-    __shared__ int64_t slots[KT];  // -1: not a key
-    __shared__ int wide;
+template <int D, int BITS, bool SYM, int TILES, int WK>
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void weigh_many_kernel(WeighArgs a, int cap) {
+    using C = Many<D, BITS, TILES, WK>;
+    __shared__ typename C::Stage stage[2];
+    __shared__ float part[C::WR][C::KT], rest[kWaves][16 * TILES];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
+    const int wk = wave % WK, wr = wave / WK;
     const int h = blockIdx.x % a.c.heads;
-    const int group = a.q_heads / a.c.heads;
+    const uint32_t group = (uint32_t)a.q_heads / (uint32_t)a.c.heads;
     const int shift = a.c.page_shift, ps_mask = (1 << shift) - 1;
-    const int my_key = threadIdx.x / C::TPK, my_part = threadIdx.x % C::TPK;
-    const uint32_t dtok = 16 * kWaves / (uint32_t)group, drem = 16 * kWaves % (uint32_t)group;
+    const int pages = (int)a.c.pages;
+    // the chunks this thread brings of a stage: one of its row, of every few rows
+    constexpr int kStep = 64 * kWaves / C::CHUNKS;
+    const int my_row = threadIdx.x / C::CHUNKS, my_chunk = threadIdx.x % C::CHUNKS;
+    const uint32_t dtok = C::ROWS / group, drem = C::ROWS % group;
 
-    const Steps<KT> sched(a.batch, shift, lane);
+    const Steps<C::KT> sched(a.batch, shift, lane);
     const int64_t all = sched.total();
     for (int64_t pos = blockIdx.x / a.c.heads; pos < all; pos += cap) {
         const Place place = sched.at(pos);
         const KvRows &rows = place.rows;
         const int32_t *const table = a.batch.table + place.seq * a.batch.max_pages;
-        const int k0 = (int)(pos - place.start) * KT;
-        const uint32_t total = (uint32_t)rows.n * (uint32_t)group;
+        const int k0 = (int)(pos - place.start) * C::KT;
+        const uint32_t total = (uint32_t)rows.n * group;
         // rows before the first key see none of them
         const int64_t late = k0 - rows.first;
-        const uint32_t row0 = late <= 0 ? 0 : late < rows.n ? (uint32_t)late * (uint32_t)group : total;
-        const uint32_t tile0 = row0 / 16, tiles = (total + 15) / 16;
+        const uint32_t row0 = late <= 0 ? 0 : late < rows.n ? (uint32_t)late * group : total;
+        const int stages = (int)((total - row0 + C::ROWS - 1) / C::ROWS);
 
-        if (threadIdx.x == 0) wide = 0;
-        __syncthreads();  // nobody reads the last step's keys any more
-        {
-            const int key = k0 + my_key, kc = key < rows.len ? key : (int)rows.len - 1;
-            int64_t page = table[kc >> shift];
-            const bool in = key < rows.len && page >= 0 && page < a.c.pages;
-            page = in ? page : 0;
-            const int64_t slot = ((page * a.c.heads + h) << shift) + (kc & ps_mask);
-            const uint32_t *src = reinterpret_cast<const uint32_t *>(a.c.k_codes + slot * C::kRow) + my_part * C::WORDS;
-            uint32_t w[C::WORDS];
+        // the way of this thread's rows from stage to stage
+        uint32_t rr[C::LOADS], tok[C::LOADS], rem[C::LOADS];
+#pragma unroll
+        for (int i = 0; i < C::LOADS; ++i) {
+            rr[i] = row0 + my_row + i * kStep;
+            tok[i] = rr[i] / group;
+            rem[i] = rr[i] - tok[i] * group;
+        }
+        auto load = [&](typename C::Load &x) {
+#pragma unroll
+            for (int i = 0; i < C::LOADS; ++i) {
+                const bool live = rr[i] < total;
+                const int64_t row = rows.begin + (live ? tok[i] : 0);
+                const int qh = h * (int)group + (live ? (int)rem[i] : 0);
+                x.lse[i] = live ? a.lse[row * a.q_heads + qh] : __builtin_inff();
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(a.q + row * a.q_stride + (int64_t)qh * D + 8 * my_chunk);
+                x.raw[i] = v;
+            }
+        };
+        auto store = [&](const typename C::Load &x, typename C::Stage &to) {
+#pragma unroll
+            for (int i = 0; i < C::LOADS; ++i) {
+                // a row that has seen no key, or a NaN, counts as zeros with a weight of nothing
+                const bool ok = fabsf(x.lse[i]) < __builtin_inff();
+                const int row = my_row + i * kStep, cg = my_chunk / C::S, cs = my_chunk % C::S;
+                to.ops[row / 16][cs][cg * 16 + ((row ^ my_chunk) & 15)] = ok ? x.raw[i] : u32x4{0u, 0u, 0u, 0u};
+                if (my_chunk == 0) {
+                    to.minus[row] = ok ? -x.lse[i] * kLog2e : -__builtin_inff();
+                    to.sees[row] = (int)(rows.first + tok[i]);
+                }
+                rr[i] += C::ROWS;
+                tok[i] += dtok;
+                rem[i] += drem;
+                if (rem[i] >= group) {
+                    rem[i] -= group;
+                    ++tok[i];
+                }
+            }
+        };
+        typename C::Load x;
+        if (stages > 0) load(x);
+
+        // the wave's keys: key 16 k + n of its own in lanes n
+        const int kw = k0 + 16 * TILES * wk;
+        int page[TILES];
+        float scale[TILES], zero[TILES], acc[TILES];
+        uint32_t w[TILES][C::WORDS];
+#pragma unroll
+        for (int k = 0; k < TILES; ++k) {
+            const int key = kw + 16 * k + n, kc = key < rows.len ? key : (int)rows.len - 1;
+            page[k] = table[kc >> shift];
+        }
+#pragma unroll
+        for (int k = 0; k < TILES; ++k) {
+            const int key = kw + 16 * k + n, kc = key < rows.len ? key : (int)rows.len - 1;
+            const bool in = key < rows.len && (uint32_t)page[k] < (uint32_t)pages;
+            page[k] = in ? page[k] : -1;
+            const int64_t slot = (((int64_t)(in ? page[k] : 0) * a.c.heads + h) << shift) + (kc & ps_mask);
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(a.c.k_codes) + (slot * 4 + g) * C::WORDS;
 #pragma unroll
             for (int i = 0; i < C::WORDS; i += 4) {
                 if constexpr (C::WORDS >= 4) {
                     const u32x4 v = *reinterpret_cast<const u32x4 *>(src + i);
-                    w[i] = v[0]; w[i + 1] = v[1]; w[i + 2] = v[2]; w[i + 3] = v[3];
-                } else if constexpr (C::WORDS == 2) {
-                    const u32x2 v = *reinterpret_cast<const u32x2 *>(src);
-                    w[0] = v[0]; w[1] = v[1];
+                    w[k][i] = v[0]; w[k][i + 1] = v[1]; w[k][i + 2] = v[2]; w[k][i + 3] = v[3];
                 } else {
-                    w[0] = src[0];
+                    const u32x2 v = *reinterpret_cast<const u32x2 *>(src);
+                    w[k][0] = v[0]; w[k][1] = v[1];
                 }
             }
-            float near = C::kMid, left = 0.0f;
-            if (!SYM) {
-                const float z = in ? a.c.k_zeros[slot] : 0.0f;
-                near = fminf(fmaxf(rintf(z), 0.0f), 2.0f * C::kMid - 1.0f);
-                left = z - near;
-                if (left != 0.0f) wide = 1;
-            }
-            if (my_part == 0) {
-                slots[my_key] = in ? slot : -1;
-                key_scale[my_key] = in ? a.c.k_scales[slot] * (a.scale * kLog2e) : 0.0f;
-                rest[my_key] = left;
-            }
-#pragma unroll
-            for (int i = 0; i < C::PIECES; ++i) {
-                bf16x8 f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t c = BITS == 8 ? (w[(2 * i + e / 4) % C::WORDS] >> (8 * (e % 4))) & 255u
-                                                 : (w[i % C::WORDS] >> (4 * e)) & 15u;
-                    f[e] = (__bf16)((float)c - near);
-                }
-                const int e0 = my_part * (D / C::TPK) + 8 * i;
-                ops[my_key / 16][e0 / 32][(e0 % 32) / 8 * 16 + my_key % 16] = f;
-            }
-        }
-        __syncthreads();
-        bf16x8 kf[C::TILES][C::S];
-        float cs[C::TILES], acc[C::TILES];
-#pragma unroll
-        for (int k = 0; k < C::TILES; ++k) {
-            cs[k] = key_scale[16 * k + n];
+            scale[k] = a.c.k_scales[slot];
+            if (!SYM) zero[k] = a.c.k_zeros[slot];
             acc[k] = 0.0f;
-#pragma unroll
-            for (int s = 0; s < C::S; ++s) kf[k][s] = ops[k][s][lane];
         }
-        const bool any_wide = !SYM && wide;
-
-        // the lane's row as an operand, and its way to the wave's next tile
-        uint32_t rr = (tile0 + wave) * 16 + n;
-        uint32_t tok = rr / (uint32_t)group, rem = rr - tok * (uint32_t)group;
-        auto load = [&](typename C::Rows &x) {
-            const bool live = rr < total;
-            const int64_t row = rows.begin + (live ? tok : 0);
-            const int qh = h * group + (live ? (int)rem : 0);
-            x.lse = live ? a.lse[row * a.q_heads + qh] : __builtin_inff();
-            const uint16_t *qp = a.q + row * a.q_stride + (int64_t)qh * D + 8 * g;
+        bf16x8 kf[TILES][C::S];
+        bool any_wide = false;
+#pragma unroll
+        for (int k = 0; k < TILES; ++k) {
+            scale[k] = page[k] >= 0 ? scale[k] * (a.scale * kLog2e) : 0.0f;
+            float near = C::kMid;
+            if constexpr (!SYM) {
+                const float z = page[k] >= 0 ? zero[k] : 0.0f;
+                near = fminf(fmaxf(rintf(z), 0.0f), 2.0f * C::kMid - 1.0f);
+                const float left = z - near;
+                any_wide |= left != 0.0f;
+                rest[wave][16 * k + n] = left;
+            }
 #pragma unroll
             for (int s = 0; s < C::S; ++s)
-                x.raw[s] = live ? *reinterpret_cast<const u32x4 *>(qp + 32 * s) : u32x4{0u, 0u, 0u, 0u};
-        };
-        typename C::Rows x;
-        if (tile0 + wave < tiles) load(x);
-        for (uint32_t tile = tile0 + wave; tile < tiles; tile += kWaves) {
-            bf16x8 qf[C::S];
-            // a row that has seen no key, or a NaN, counts as zeros with a weight of nothing
-            const bool ok = fabsf(x.lse) < __builtin_inff();
-            const float minus = ok ? -x.lse * kLog2e : -__builtin_inff();
-            if (__any(!ok)) {
 #pragma unroll
-                for (int s = 0; s < C::S; ++s) x.raw[s] = ok ? x.raw[s] : u32x4{0u, 0u, 0u, 0u};
-            }
-#pragma unroll
-            for (int s = 0; s < C::S; ++s) qf[s] = __builtin_bit_cast(bf16x8, x.raw[s]);
-            float nl[4], qs[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) nl[i] = __shfl(minus, 4 * g + i);
-            if (any_wide) {
-                f32x4 v{0.0f, 0.0f, 0.0f, 0.0f};
-                bf16x8 ones;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ones[e] = (__bf16)1.0f;
-#pragma unroll
-                for (int s = 0; s < C::S; ++s) v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[s], ones, v, 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) qs[i] = v[i];
-            }
-            const int64_t sees = rows.first + tok;
-            // keys that some row of the tile does not see
-            const bool masked = k0 + KT - 1 > __builtin_amdgcn_readfirstlane((int)sees);
-            int last[4] = {0, 0, 0, 0};
-            if (masked) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) last[i] = __shfl((int)sees, 4 * g + i);
-            }
-            rr += 16 * kWaves;
-            tok += dtok;
-            rem += drem;
-            if (rem >= (uint32_t)group) {
-                rem -= group;
-                ++tok;
-            }
-            if (tile + kWaves < tiles) load(x);
-#pragma unroll
-            for (int k = 0; k < C::TILES; ++k) {
-                f32x4 t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int s = 0; s < C::S; ++s) t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[s], kf[k][s], t, 0, 0, 0);
-                if (any_wide) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) t[i] = __builtin_fmaf(-rest[16 * k + n], qs[i], t[i]);
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t c = BITS == 8 ? (w[k][2 * s + e / 4] >> (8 * (e % 4))) & 255u : (w[k][s] >> (4 * e)) & 15u;
+                    kf[k][s][e] = (__bf16)((float)c - near);
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float p = __builtin_amdgcn_exp2f(__builtin_fmaf(t[i], cs[k], nl[i]));
-                    if (masked) p = k0 + 16 * k + n > last[i] ? 0.0f : p;
-                    acc[k] += p;
-                }
-            }
         }
-#pragma unroll
-        for (int k = 0; k < C::TILES; ++k) {
-            acc[k] = add_halves32(add_halves16(acc[k]));
-            if (g == 0) part[wave][16 * k + n] = acc[k];
-        }
+        any_wide = !SYM && __any(any_wide);
+        if (stages > 0) store(x, stage[0]);
+        if (stages > 1) load(x);
         __syncthreads();
-        if (threadIdx.x < KT && slots[threadIdx.x] >= 0) {
-            float sum = 0.0f;
+
+        for (int st = 0; st < stages; ++st) {
+            const typename C::Stage &b = stage[st & 1];
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) sum += part[w][threadIdx.x];
-            // the call's own tokens start from nothing
-            const int64_t slot = slots[threadIdx.x];
-            const bool old = a.weights && k0 + (int)threadIdx.x < rows.first;
-            a.out[slot] = (old ? a.weights[slot] : 0.0f) + sum;
+            for (int r = 0; r < C::RT; ++r) {
+                const int tile = wr * C::RT + r;
+                bf16x8 qf[C::S];
+#pragma unroll
+                for (int s = 0; s < C::S; ++s)
+                    qf[s] = __builtin_bit_cast(bf16x8, b.ops[tile][s][g * 16 + ((n ^ (g * C::S + s)) & 15)]);
+                const f32x4 nl = *reinterpret_cast<const f32x4 *>(&b.minus[16 * tile + 4 * g]);
+                // keys that some row of the tile does not see
+                const bool masked = kw + 16 * TILES - 1 > __builtin_amdgcn_readfirstlane(b.sees[16 * tile]);
+                auto weigh = [&](auto masked_keys, auto wide_zeros) {
+                    int last[4];
+                    f32x4 qs{0.0f, 0.0f, 0.0f, 0.0f};  // the rows' sums
+                    if constexpr (masked_keys) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) last[i] = b.sees[16 * tile + 4 * g + i];
+                    }
+                    if constexpr (wide_zeros) {
+                        bf16x8 ones;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) ones[e] = (__bf16)1.0f;
+#pragma unroll
+                        for (int s = 0; s < C::S; ++s) qs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[s], ones, qs, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int k = 0; k < TILES; ++k) {
+                        f32x4 t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int s = 0; s < C::S; ++s) t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[s], kf[k][s], t, 0, 0, 0);
+                        if constexpr (wide_zeros) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) t[i] = __builtin_fmaf(-rest[wave][16 * k + n], qs[i], t[i]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float p = __builtin_amdgcn_exp2f(__builtin_fmaf(t[i], scale[k], nl[i]));
+                            if constexpr (masked_keys) p = kw + 16 * k + n > last[i] ? 0.0f : p;
+                            acc[k] += p;
+                        }
+                    }
+                };
+                if (any_wide) weigh(std::true_type{}, std::true_type{});
+                else if (masked) weigh(std::true_type{}, std::false_type{});
+                else weigh(std::false_type{}, std::false_type{});
+            }
+            if (st + 1 < stages) store(x, stage[(st + 1) & 1]);
+            if (st + 2 < stages) load(x);
+            lds_barrier();  // the next stage is written, and this one read by all
         }
+#pragma unroll
+        for (int k = 0; k < TILES; ++k) acc[k] = add_halves32(add_halves16(acc[k]));
+        if constexpr (C::WR > 1) {
+#pragma unroll
+            for (int k = 0; k < TILES; ++k)
+                if (g == 0) part[wr][16 * (TILES * wk + k) + n] = acc[k];
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < TILES; ++k) {
+                acc[k] = 0.0f;
+#pragma unroll
+                for (int r = 0; r < C::WR; ++r) acc[k] += part[r][16 * (TILES * wk + k) + n];
+            }
+        }
+        if (wr == 0) {
+#pragma unroll
+            for (int k = 0; k < TILES; ++k)
+                if (g == k % 4 && page[k] >= 0) {
+                    const int key = kw + 16 * k + n;
+                    const int64_t slot = (((int64_t)page[k] * a.c.heads + h) << shift) + (key & ps_mask);
+                    // the call's own tokens start from nothing
+                    const bool old = a.weights && key < rows.first;
+                    a.out[slot] = (old ? a.weights[slot] : 0.0f) + acc[k];
+                }
+        }
+        if constexpr (C::WR > 1) __syncthreads();  // the parts are read
     }
 }
 
@@ -474,15 +517,14 @@ static hipError_t launch(const WeighArgs &a, hipStream_t st) {
         hipLaunchKernelGGL((weigh_few_kernel<D, BITS, SYM>), dim3((uint32_t)(cap * heads)), dim3(64 * kWaves), 0, st, a, cap);
         return hipGetLastError();
     }
-    constexpr int KT = D == 256 ? 64 : 128;
-    if (blocks(KT, 1 << 20) * heads >= 512) {
-        const int cap = blocks(KT, 1 << 16);
-        hipLaunchKernelGGL((weigh_many_kernel<D, BITS, SYM, KT>), dim3((uint32_t)(cap * heads)), dim3(64 * kWaves), 0, st, a, cap);
-    } else {
-        const int cap = blocks(32, 1 << 16);
-        hipLaunchKernelGGL((weigh_many_kernel<D, BITS, SYM, 32>), dim3((uint32_t)(cap * heads)), dim3(64 * kWaves), 0, st, a, cap);
-    }
-    return hipGetLastError();
+    auto many = [&](auto kernel, int64_t keys) {
+        const int cap = blocks(keys, 1 << 16);
+        hipLaunchKernelGGL(kernel, dim3((uint32_t)(cap * heads)), dim3(64 * kWaves), 0, st, a, cap);
+        return hipGetLastError();
+    };
+    constexpr int TILES = D == 256 ? 2 : 4;
+    if (blocks(TILES * 64, 1 << 20) * heads >= 512) return many(weigh_many_kernel<D, BITS, SYM, TILES, 4>, TILES * 64);
+    return many(weigh_many_kernel<D, BITS, SYM, 2, 1>, 32);
 }
 
 hipError_t launch_kv_weigh(const WeighArgs &a, hipStream_t st) {
