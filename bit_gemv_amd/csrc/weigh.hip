@@ -80,8 +80,9 @@ struct Steps {
 
 // ---- few rows: keys streamed past one tile of 16 rows ----
 //
-// Wave w of a block walks its span's 32-key tiles w, w + 4, ...; the next
-// tile's codes are asked for as soon as this one's have been multiplied.
+// Wave w of a block walks its span's 32-key tiles w, w + 4, ..., the next two
+// tiles' codes on their way: a tile's registers take the one after the next as
+// soon as it has been multiplied.
 template <int D, int BITS>
 struct Few {
     static constexpr int kRow = D * BITS / 8;    // code bytes of a key
@@ -97,6 +98,7 @@ struct Few {
     };
 };
 constexpr int kFewStep = 32 * kWaves;
+constexpr int kLate = 64, kEarly = 4;  // tiles a wave holds the sums of, and up to which it holds none
 
 template <int D, int BITS, bool SYM>
 __global__ __launch_bounds__(64 * kWaves, 3) void weigh_few_kernel(WeighArgs a, int cap) {
@@ -111,6 +113,9 @@ __global__ __launch_bounds__(64 * kWaves, 3) void weigh_few_kernel(WeighArgs a, 
     const int pages = (int)a.c.pages;
     const uint32_t k_off = n * C::kRow + g * (C::VEC * 4);
     const uint32_t magic = fp16_magic();
+    // weights of a wave's tiles, and the slots of their two groups of 16 keys
+    __shared__ float held[kWaves][kLate * 32];
+    __shared__ int64_t held_at[kWaves][kLate * 2];
 
     const Steps<kFewStep> sched(a.batch, shift, lane);
     const int64_t all = sched.total(), share = uniform_div(all + cap - 1, cap);
@@ -139,6 +144,11 @@ __global__ __launch_bounds__(64 * kWaves, 3) void weigh_few_kernel(WeighArgs a, 
             pid1 = table[k1 >> shift];
             asm volatile("" : "+v"(pid0), "+v"(pid1));  // waited for here, not behind later loads
         };
+        // Stores among the loads cost HBM more than their bytes (64 sequences, 21 MB
+        // of weights beside 700 MB of keys: 169 us; 158 with the weights held in LDS
+        // and written at the end of a run, 135 without any). Short runs, whose time
+        // is latency, write each tile's.
+        const bool late = its > kEarly;
         // One tile of 16 rows, as the launch's rule expects; more of them go
         // over the keys again and add to what the one before has written.
         for (uint32_t tile = 0; tile * 16 < total; ++tile) {
@@ -170,12 +180,13 @@ __global__ __launch_bounds__(64 * kWaves, 3) void weigh_few_kernel(WeighArgs a, 
                 x.w = before ? before[(g & 1 ? at.slot1 : at.slot0) + n] : 0.0f;
                 return at;
             };
-            typename C::Tile x;
-            At at{0, 0, 0, 0};
+            typename C::Tile xa, xb;  // two tiles of the wave are on their way at any time
+            At ata{0, 0, 0, 0}, atb{0, 0, 0, 0};
             if (its > 0) {
                 load_pages(0);
-                at = load(x, 0);
+                ata = load(xa, 0);
             }
+            if (its > 1) atb = load(xb, 1);
             // this lane's row as an operand; a row that has seen no key, or a NaN,
             // counts as zeros with a weight of nothing
             const uint32_t rr = tile * 16 + n;
@@ -212,7 +223,7 @@ __global__ __launch_bounds__(64 * kWaves, 3) void weigh_few_kernel(WeighArgs a, 
             }
             const int safe = (int)(rows.first + tile * 16 / (uint32_t)group);  // every row sees up to here
 
-            for (int it = 0; it < its; ++it) {
+            auto step = [&](typename C::Tile &x, At &at, int it) {
                 f32x4 t[2];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
@@ -240,7 +251,7 @@ __global__ __launch_bounds__(64 * kWaves, 3) void weigh_few_kernel(WeighArgs a, 
                 const int64_t slot = (g & 1 ? at.slot1 : at.slot0) + n;
                 const bool masked = at.key0 + 15 > safe || at.key1 + 15 > safe;
                 const float was = key < rows.first || tile ? x.w : 0.0f;  // the call's own tokens start from nothing
-                if (it + 1 < its) at = load(x, it + 1);
+                if (it + 2 < its) at = load(x, it + 2);
                 float sum[2] = {0.0f, 0.0f};
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
@@ -252,7 +263,26 @@ __global__ __launch_bounds__(64 * kWaves, 3) void weigh_few_kernel(WeighArgs a, 
                     }
                 sum[0] = add_halves32(add_halves16(sum[0]));
                 sum[1] = add_halves32(add_halves16(sum[1]));
-                if (g < 2 && key < kstop) a.out[slot] = was + (g ? sum[1] : sum[0]);
+                const float mine = was + (g & 1 ? sum[1] : sum[0]);
+                if (late) {
+                    if (g < 2) held[wave][it % kLate * 32 + 16 * g + n] = mine;
+                    if (g < 2 && n == 0) held_at[wave][it % kLate * 2 + g] = key < kstop ? slot : -1;
+                } else if (g < 2 && key < kstop) {
+                    a.out[slot] = mine;
+                }
+            };
+            auto write = [&](int it0, int it1) {  // the held weights of tiles it0 to it1, two at a time
+#pragma unroll 4
+                for (int i = it0; i < it1; i += 2) {
+                    const int tile_of = i + (g >> 1), key = first_key + kFewStep * tile_of + 16 * (g & 1) + n;
+                    const int64_t at16 = held_at[wave][tile_of % kLate * 2 + (g & 1)];
+                    if (tile_of < it1 && key < kstop && at16 >= 0) a.out[at16 + n] = held[wave][i % kLate * 32 + lane];
+                }
+            };
+            for (int it = 0; it < its; it += 2) {
+                step(xa, ata, it);
+                if (it + 1 < its) step(xb, atb, it + 1);
+                if (late && (it + 2 >= its || (it + 2) % kLate == 0)) write(it - it % kLate, it + 2 < its ? it + 2 : its);
             }
         }
     }
@@ -293,6 +323,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void weigh_many_kern
     using C = Many<D, BITS, TILES, WK>;
     __shared__ typename C::Stage stage[2];
     __shared__ float part[C::WR][C::KT], rest[kWaves][16 * TILES];
+    __shared__ int key_page[kWaves][16 * TILES];  // -1: not a key
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
@@ -305,6 +336,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void weigh_many_kern
     constexpr int kStep = 64 * kWaves / C::CHUNKS;
     const int my_row = threadIdx.x / C::CHUNKS, my_chunk = threadIdx.x % C::CHUNKS;
     const uint32_t dtok = C::ROWS / group, drem = C::ROWS % group;
+    const int64_t dq = dtok * a.q_stride + drem * D;
+    const int dl = (int)(dtok * a.q_heads + drem);
 
     const Steps<C::KT> sched(a.batch, shift, lane);
     const int64_t all = sched.total();
@@ -319,47 +352,86 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void weigh_many_kern
         const uint32_t row0 = late <= 0 ? 0 : late < rows.n ? (uint32_t)late * group : total;
         const int stages = (int)((total - row0 + C::ROWS - 1) / C::ROWS);
 
-        // the way of this thread's rows from stage to stage
-        uint32_t rr[C::LOADS], tok[C::LOADS], rem[C::LOADS];
+        // This thread's rows go on by ROWS from stage to stage: dtok tokens and drem
+        // heads, or a token more and the group's heads fewer.
+        const uint16_t *const q0 = a.q + rows.begin * a.q_stride + (int64_t)h * group * D;
+        const float *const lse0 = a.lse + rows.begin * a.q_heads + (int64_t)h * group;
+        const uint16_t *qp[C::LOADS];
+        const float *lp[C::LOADS];
+        uint32_t rem[C::LOADS];
+        int sees[C::LOADS];
 #pragma unroll
         for (int i = 0; i < C::LOADS; ++i) {
-            rr[i] = row0 + my_row + i * kStep;
-            tok[i] = rr[i] / group;
-            rem[i] = rr[i] - tok[i] * group;
+            const uint32_t rr = row0 + my_row + i * kStep, tok = rr / group;
+            rem[i] = rr - tok * group;
+            sees[i] = (int)(rows.first + tok);
+            qp[i] = q0 + tok * a.q_stride + rem[i] * D + 8 * my_chunk;
+            lp[i] = lse0 + (int64_t)tok * a.q_heads + rem[i];
         }
-        auto load = [&](typename C::Load &x) {
+        auto load = [&](typename C::Load &x, int st) {
+            if (total - row0 >= (uint32_t)(st + 1) * C::ROWS) {
 #pragma unroll
-            for (int i = 0; i < C::LOADS; ++i) {
-                const bool live = rr[i] < total;
-                const int64_t row = rows.begin + (live ? tok[i] : 0);
-                const int qh = h * (int)group + (live ? (int)rem[i] : 0);
-                x.lse[i] = live ? a.lse[row * a.q_heads + qh] : __builtin_inff();
-                const u32x4 v = *reinterpret_cast<const u32x4 *>(a.q + row * a.q_stride + (int64_t)qh * D + 8 * my_chunk);
-                x.raw[i] = v;
+                for (int i = 0; i < C::LOADS; ++i) {
+                    x.lse[i] = *lp[i];
+                    x.raw[i] = *reinterpret_cast<const u32x4 *>(qp[i]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < C::LOADS; ++i) {
+                    const bool live = row0 + (uint32_t)st * C::ROWS + my_row + i * kStep < total;
+                    x.lse[i] = live ? *lp[i] : __builtin_inff();
+                    x.raw[i] = live ? *reinterpret_cast<const u32x4 *>(qp[i]) : u32x4{0u, 0u, 0u, 0u};
+                }
             }
         };
-        auto store = [&](const typename C::Load &x, typename C::Stage &to) {
+        auto store = [&](typename C::Load &x, typename C::Stage &to) {
+            bool ok[C::LOADS], all_ok = true;
 #pragma unroll
             for (int i = 0; i < C::LOADS; ++i) {
-                // a row that has seen no key, or a NaN, counts as zeros with a weight of nothing
-                const bool ok = fabsf(x.lse[i]) < __builtin_inff();
-                const int row = my_row + i * kStep, cg = my_chunk / C::S, cs = my_chunk % C::S;
-                to.ops[row / 16][cs][cg * 16 + ((row ^ my_chunk) & 15)] = ok ? x.raw[i] : u32x4{0u, 0u, 0u, 0u};
-                if (my_chunk == 0) {
-                    to.minus[row] = ok ? -x.lse[i] * kLog2e : -__builtin_inff();
-                    to.sees[row] = (int)(rows.first + tok[i]);
+                ok[i] = fabsf(x.lse[i]) < __builtin_inff();
+                all_ok &= ok[i];
+            }
+            // a row that has seen no key, or a NaN, counts as zeros with a weight of nothing
+            if (!__all(all_ok)) {
+#pragma unroll
+                for (int i = 0; i < C::LOADS; ++i) {
+                    x.raw[i] = ok[i] ? x.raw[i] : u32x4{0u, 0u, 0u, 0u};
+                    x.lse[i] = ok[i] ? x.lse[i] : __builtin_inff();
                 }
-                rr[i] += C::ROWS;
-                tok[i] += dtok;
-                rem[i] += drem;
-                if (rem[i] >= group) {
-                    rem[i] -= group;
-                    ++tok[i];
+            }
+#pragma unroll
+            for (int i = 0; i < C::LOADS; ++i) {
+                const int row = my_row + i * kStep;
+                to.ops[row / 16][my_chunk % C::S][my_chunk / C::S * 16 + ((row ^ my_chunk) & 15)] = x.raw[i];
+            }
+            if (my_chunk == 0) {
+#pragma unroll
+                for (int i = 0; i < C::LOADS; ++i) {
+                    to.minus[my_row + i * kStep] = -x.lse[i] * kLog2e;
+                    to.sees[my_row + i * kStep] = sees[i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < C::LOADS; ++i) {
+                qp[i] += dq;
+                lp[i] += dl;
+                sees[i] += (int)dtok;
+            }
+            if (drem) {
+#pragma unroll
+                for (int i = 0; i < C::LOADS; ++i) {
+                    rem[i] += drem;
+                    if (rem[i] >= group) {
+                        rem[i] -= group;
+                        qp[i] += a.q_stride - (int64_t)group * D;
+                        lp[i] += a.q_heads - (int)group;
+                        ++sees[i];
+                    }
                 }
             }
         };
         typename C::Load x;
-        if (stages > 0) load(x);
+        if (stages > 0) load(x, 0);
 
         // the wave's keys: key 16 k + n of its own in lanes n
         const int kw = k0 + 16 * TILES * wk;
@@ -396,6 +468,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void weigh_many_kern
         bool any_wide = false;
 #pragma unroll
         for (int k = 0; k < TILES; ++k) {
+            key_page[wave][16 * k + n] = page[k];
             scale[k] = page[k] >= 0 ? scale[k] * (a.scale * kLog2e) : 0.0f;
             float near = C::kMid;
             if constexpr (!SYM) {
@@ -407,17 +480,35 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void weigh_many_kern
             }
 #pragma unroll
             for (int s = 0; s < C::S; ++s)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t c = BITS == 8 ? (w[k][2 * s + e / 4] >> (8 * (e % 4))) & 255u : (w[k][s] >> (4 * e)) & 15u;
-                    kf[k][s][e] = (__bf16)((float)c - near);
+            {
+                // INT4: even elements are the low nibbles of the bytes, odd ones the
+                // high (hidden from the compiler, which otherwise shifts every code
+                // by itself instead of converting bytes)
+                uint32_t lo = w[k][(BITS == 8 ? 2 * s : s) % C::WORDS], hi = w[k][(BITS == 8 ? 2 * s + 1 : s) % C::WORDS];
+                if constexpr (BITS == 4) {
+                    lo = lo & 0x0F0F0F0Fu;
+                    hi = hi >> 4 & 0x0F0F0F0Fu;
+                    asm volatile("" : "+v"(lo), "+v"(hi));
                 }
+                u32x4 pairs;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t c0 = BITS == 8 ? (e < 2 ? lo : hi) >> 16 * (e % 2) : lo >> 8 * e;
+                    const uint32_t c1 = BITS == 8 ? (e < 2 ? lo : hi) >> (16 * (e % 2) + 8) : hi >> 8 * e;
+                    const bf16x2_t v{(__bf16)((float)(c0 & 255u) - near), (__bf16)((float)(c1 & 255u) - near)};
+                    pairs[e] = __builtin_bit_cast(uint32_t, v);
+                }
+                kf[k][s] = __builtin_bit_cast(bf16x8, pairs);
+            }
         }
         any_wide = !SYM && __any(any_wide);
         if (stages > 0) store(x, stage[0]);
-        if (stages > 1) load(x);
+        if (stages > 1) load(x, 1);
         __syncthreads();
 
+        // rows from here on see all of the wave's keys
+        const int64_t beyond = kw + 16 * TILES - 1 - rows.first;
+        const uint32_t safe = beyond <= 0 ? 0 : beyond < rows.n ? (uint32_t)beyond * group : total;
         for (int st = 0; st < stages; ++st) {
             const typename C::Stage &b = stage[st & 1];
 #pragma unroll
@@ -429,7 +520,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void weigh_many_kern
                     qf[s] = __builtin_bit_cast(bf16x8, b.ops[tile][s][g * 16 + ((n ^ (g * C::S + s)) & 15)]);
                 const f32x4 nl = *reinterpret_cast<const f32x4 *>(&b.minus[16 * tile + 4 * g]);
                 // keys that some row of the tile does not see
-                const bool masked = kw + 16 * TILES - 1 > __builtin_amdgcn_readfirstlane(b.sees[16 * tile]);
+                const bool masked = row0 + st * C::ROWS + 16 * tile < safe;
                 auto weigh = [&](auto masked_keys, auto wide_zeros) {
                     int last[4];
                     f32x4 qs{0.0f, 0.0f, 0.0f, 0.0f};  // the rows' sums
@@ -466,7 +557,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void weigh_many_kern
                 else weigh(std::false_type{}, std::false_type{});
             }
             if (st + 1 < stages) store(x, stage[(st + 1) & 1]);
-            if (st + 2 < stages) load(x);
+            if (st + 2 < stages) load(x, st + 2);
             lds_barrier();  // the next stage is written, and this one read by all
         }
 #pragma unroll
@@ -486,9 +577,9 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void weigh_many_kern
         if (wr == 0) {
 #pragma unroll
             for (int k = 0; k < TILES; ++k)
-                if (g == k % 4 && page[k] >= 0) {
+                if (const int p = key_page[wave][16 * k + n]; g == k % 4 && p >= 0) {
                     const int key = kw + 16 * k + n;
-                    const int64_t slot = (((int64_t)page[k] * a.c.heads + h) << shift) + (key & ps_mask);
+                    const int64_t slot = (((int64_t)p * a.c.heads + h) << shift) + (key & ps_mask);
                     // the call's own tokens start from nothing
                     const bool old = a.weights && key < rows.first;
                     a.out[slot] = (old ? a.weights[slot] : 0.0f) + acc[k];
