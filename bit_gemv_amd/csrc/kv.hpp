@@ -51,8 +51,9 @@ struct AttnArgs {
     void *workspace;
     uint16_t *out;
     float *lse;
-    // in the place of out and lse, for a result that is joined with another: the
-    // rows [rows][q_heads][D] relative to their maximum, maximum (log2) and sum
+    // in the place of out and lse, for a result that is joined with another: whole
+    // units' rows [rows][q_heads][D] relative to their maximum, maximum (log2) and
+    // sum; cut units' parts stay in the workspace
     float *part_o = nullptr, *part_ml = nullptr;
 };
 

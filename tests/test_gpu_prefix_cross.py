@@ -157,6 +157,26 @@ def test_prefix_decode(bits, sym):
                 hints=({}, dict(max_rows=1, max_kv=90, max_prefix=700, max_prefix_rows=n)))
 
 
+@pytest.mark.parametrize("group,d", [(7, 64), (5, 128), (3, 256)])
+def test_prefix_tiles_end_inside_a_group(group, d):
+    """Rows beside each other in different tiles, units cut into parts and whole
+    ones, of the prefix and of the own tokens, one prefix and several."""
+    seqs = [(90, 70), (60, 50), (300, 90), (40, 40), (33, 1)]
+    for prefixes in ([(500, 5)], [(500, 2), (260, 3)]):
+        _prefix(seqs, prefixes, d, 8, False, heads=1, group=group, seed=group, wide=512,
+                hints=({}, dict(max_rows=90, max_kv=300), dict(max_prefix=500, max_prefix_rows=260)))
+
+
+def test_prefix_of_more_than_64_sequences():
+    """Past what a wave looks up at once: single rows, and a few chunks."""
+    for page, n in ((16, 70), (64, 150)):
+        seqs = [(1 + (7 * i) % 40, 3 if i % 40 == 1 else 1) for i in range(n)]
+        _prefix(seqs, [(130, 20), (70, n - 25)], 64, 8, True, page=page, heads=1, group=2, seed=n, skip=5,
+                hints=({}, dict(max_rows=3, max_kv=40, max_prefix=130, max_prefix_rows=n)))
+        many = [(0, 0)] * 66 + [(20, 2), (30, 1)]
+        _prefix(many, [(10, 1)] * 66 + [(200, 2)], 64, 8, True, page=page, heads=1, group=2, seed=n)
+
+
 @pytest.mark.parametrize("group", [1, 3, 7, 16, 20])
 def test_prefix_head_layouts(group):
     _prefix([(37, 1), (50, 11), (20, 20)], [(90, 2), (17, 1)], 64, 8, True, heads=1 if group > 8 else 3, group=group, seed=group)
