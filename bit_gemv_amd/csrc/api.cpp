@@ -898,7 +898,7 @@ lq_status kv_cache_evict(const lq_kv_cache *cache, float *weights, const int32_t
     if (keep < 1 || recent < 0 || recent > keep || to_pages < 0 || max_kv < 0)
         return fail(LQ_ERR_INVALID_ARG, "%s: keep must be positive, recent in 0..keep, sizes not negative", fn);
     const int64_t room = max_pages * cache->page_size, to_room = to_pages <= lq::kMaxTokens ? to_pages * cache->page_size : 0;
-    if (keep > lq::kMaxTokens || to_pages > lq::kMaxTokens / cache->page_size || b * cache->heads >= (1 << 22) ||
+    if (keep > lq::kMaxTokens || to_pages > lq::kMaxTokens / cache->page_size || b * cache->heads >= (1 << 21) ||
         b * cache->heads * keep > kMaxElems)
         return fail(LQ_ERR_UNSUPPORTED, "%s: keep, to_table or batch too large", fn);
     if (to_room < (keep < room ? keep : room))

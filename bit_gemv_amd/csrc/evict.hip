@@ -202,10 +202,11 @@ __global__ __launch_bounds__(kMove) void evict_move_kernel(EvictArgs a, Shares s
     const int split = blockIdx.x / a.c.heads / roles % sh.splits;
     const int64_t seq = blockIdx.x / a.c.heads / roles / sh.splits;
     const int64_t len = held_of(a, seq);
-    const int count = (int)(len < a.keep ? len : a.keep);
+    const int count = (int)(len < a.keep ? len : a.keep);  // the same of new_lens
     if (role == 0 && h == 0 && split == 0 && threadIdx.x == 0) a.new_lens[seq] = count;
-    if (len <= a.keep && a.to_table == a.table) return;  // all stays where it is
     const int32_t *const kept = a.kept + ((int64_t)seq * a.c.heads + h) * a.keep;
+    // all stays where it is; by the positions, as new_lens may be the lengths
+    if (a.to_table == a.table && (count == 0 || kept[count - 1] == count - 1)) return;
     const int32_t *const table = a.table + seq * a.max_pages, *const to_table = a.to_table + seq * a.to_pages;
     const int shift = a.c.page_shift, mask = (1 << shift) - 1;
     auto slot_of = [&](const int32_t *tab, int pos) -> int64_t {

@@ -153,6 +153,11 @@ __global__ __launch_bounds__(64 * kWaves, 3) void weigh_few_kernel(WeighArgs a, 
         // over the keys again and add to what the one before has written.
         for (uint32_t tile = 0; tile * 16 < total; ++tile) {
             const float *const before = tile ? a.out : a.weights;
+            if (tile) {  // other lanes of the wave wrote some of it
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            }
             struct At {
                 int64_t slot0, slot1;  // of the tile's two groups of 16 keys
                 int key0, key1;        // their first keys; past any key for a page outside the pool
@@ -272,6 +277,9 @@ __global__ __launch_bounds__(64 * kWaves, 3) void weigh_few_kernel(WeighArgs a, 
                 }
             };
             auto write = [&](int it0, int it1) {  // the held weights of tiles it0 to it1, two at a time
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 #pragma unroll 4
                 for (int i = it0; i < it1; i += 2) {
                     const int tile_of = i + (g >> 1), key = first_key + kFewStep * tile_of + 16 * (g & 1) + n;
@@ -609,7 +617,9 @@ static hipError_t launch(const WeighArgs &a, hipStream_t st) {
         return hipGetLastError();
     }
     auto many = [&](auto kernel, int64_t keys) {
-        const int cap = blocks(keys, 1 << 16);
+        // more steps than that are walked: with no bound of the lengths most of a
+        // wide table's steps may hold nothing
+        const int cap = blocks(keys, 1 << 12);
         hipLaunchKernelGGL(kernel, dim3((uint32_t)(cap * heads)), dim3(64 * kWaves), 0, st, a, cap);
         return hipGetLastError();
     };

@@ -586,7 +586,7 @@ lq_status prefix_attention(const lq_kv_cache *cache, const void *q_bf16, int64_t
  * in the place of weights. lse fp32 [rows][q_heads]: what the attention call
  * returned for these rows (with a shared prefix prefix_attention's, for the
  * prefix's and the own tokens alike). A row whose lse is not finite (it saw
- * nothing, or holds a NaN) adds nothing.
+ * nothing, or holds a NaN) adds nothing; q of the others must be finite.
  * weights and weights_out fp32 in the scales' layout [pages][heads][page_size],
  * 16-byte aligned; weights may be NULL (zeros), and weights_out weights itself.
  * Slots that hold no position of such a sequence are left as they were. No page
@@ -623,7 +623,7 @@ lq_status kv_cache_weigh(const lq_kv_cache *cache, const void *q_bf16, int64_t r
  * behind the last. new_lens out int32 [b]: min(kv_lens[i], keep), the kv_lens of
  * later calls; may be kv_lens. Positions in a page that is not in the pool go
  * first; where one has to stay, or to_table's page is not in the pool, its slot
- * holds anything. 1 <= keep, 0 <= recent <= keep; b * heads below 2^22. max_kv as
+ * holds anything. 1 <= keep, 0 <= recent <= keep; b * heads below 2^21. max_kv as
  * in paged_attention. weights 16-byte, int32 arrays 4-byte aligned.
  */
 lq_status kv_cache_evict(const lq_kv_cache *cache, float *weights, const int32_t *block_table, int64_t max_pages,

@@ -268,6 +268,33 @@ def test_evict_ignores_pages_outside_the_pool():
     assert host(lens).tolist() == [80]
 
 
+def test_lengths_updated_in_place_by_many_sequences():
+    """More blocks than run at once read the lengths that others replace."""
+    heads, d, n, keep = 8, 64, 260, 20
+    rng = np.random.default_rng(2)
+    b = Batch([(40 + i % 30, 0) for i in range(n)], 16, rng)
+    c = bg.KVCache.empty(b.pages, 16, heads, d)
+    c.k_codes.copy_(torch.from_numpy(rng.integers(0, 256, c.k_codes.shape, dtype=np.uint8)))
+    for t in (c.v_codes, c.k_scales, c.v_scales):
+        t.fill_(3)
+    w = dev(rng.random(c.k_scales.shape, dtype=np.float32))
+    table, lens, _ = b.on_gpu()
+    before, k0, w0 = lens.clone(), host(c.k_codes).copy(), host(w).copy()
+    say("evict, lengths in place")
+    _, kept = bg.kv_cache_evict(c, w, table, lens, keep, 3, new_lens=lens)
+    assert bool((lens == keep).all())
+    kept, k1, w1 = host(kept), host(c.k_codes), host(w)
+    for i in range(n):
+        for h in range(heads):
+            old = [w0[b.lists[i][t // 16], h, t % 16] for t in range(b.kv[i])]
+            best = sorted(range(b.kv[i] - 3), key=lambda t: (-old[t], t))[:keep - 3]
+            assert kept[i, h].tolist() == sorted(best) + list(range(b.kv[i] - 3, b.kv[i])), (i, h)
+            for j, t in enumerate(kept[i, h]):
+                at, src = (b.lists[i][j // 16], h, j % 16), (b.lists[i][t // 16], h, t % 16)
+                assert np.array_equal(k1[at], k0[src]) and w1[at] == w0[src], (i, h, j)
+    assert host(before).tolist() == b.kv
+
+
 def test_shared_pages_are_read_only_when_moved_elsewhere():
     """Two sequences over the same pages, evicted into pages of their own."""
     rng = np.random.default_rng(1)
