@@ -77,7 +77,7 @@ def load_library(path: Optional[str] = None):
         "kv_cache_read": [P, P, P, I, I64, P, I64, P, P, I64, I64, P],
         "paged_attention": [P, P, I64, I64, I64, F, P, I64, P, P, I64, I64, I64, P, I64, P, P, P],
         "cross_attention": [P, P, I64, I64, I64, F, P, I64, P, P, I64, I64, I64, P, I64, P, P, P],
-        "kv_cache_weigh": [P, P, I64, I64, I64, F, P, P, I64, P, P, I64, I, I64, I64, P, P, P],
+        "kv_cache_weigh": [P, P, I64, I64, I64, F, P, P, I64, P, P, I64, I, I64, I64, P, P, P, I64, P],
         "kv_cache_evict": [P, P, P, I64, P, I64, I64, I64, P, I64, I64, P, P, P],
         "prefix_attention": [P, P, I64, I64, I64, F] + [P, I64, P, P, I64, I64, I64] * 2 + [P, I64, P, P, P],
     }
@@ -100,6 +100,8 @@ def load_library(path: Optional[str] = None):
     lib.paged_attention_workspace_bytes.restype = ctypes.c_int64
     lib.cross_attention_workspace_bytes.argtypes = [I64] * 9
     lib.cross_attention_workspace_bytes.restype = ctypes.c_int64
+    lib.kv_cache_weigh_workspace_bytes.argtypes = [I64] * 9
+    lib.kv_cache_weigh_workspace_bytes.restype = ctypes.c_int64
     lib.prefix_attention_workspace_bytes.argtypes = [I64] * 13
     lib.prefix_attention_workspace_bytes.restype = ctypes.c_int64
     lib.lq_read_probe_sink_words.argtypes = []
@@ -824,14 +826,15 @@ def prefix_attention_workspace(rows: int, q_heads: int, cache: KVCache, p: int, 
 def kv_cache_weigh(q: torch.Tensor, lse: torch.Tensor, cache: KVCache, weights: Optional[torch.Tensor],
                    block_table: torch.Tensor, kv_lens: torch.Tensor, row_starts: torch.Tensor,
                    scale: Optional[float] = None, causal: bool = True, max_rows: int = 0, max_kv: int = 0,
-                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Add the attention weight that every cached token receives from the rows q
     [rows][q_heads][head_dim] to weights (fp32 [pages][heads][page_size], None:
     zeros): the sum of exp(scale q . k - lse) over the rows that see it and its
     head's group, lse being what attention returned for these rows. causal: rows
     are their sequences' last tokens (paged_attention, prefix_attention's own
     tokens), whose own weights start from 0; otherwise they see the whole sequence
-    (cross_attention, a shared prefix). -> out, by default weights itself."""
+    (cross_attention, a shared prefix). workspace: uint8, of at least
+    kv_cache_weigh_workspace(...) bytes. -> out, by default weights itself."""
     qs = _rows(cache, q, "q", None)
     if q.dtype is not _BF16:
         raise TypeError(f"q must be {_BF16}, got {q.dtype}")
@@ -846,10 +849,30 @@ def kv_cache_weigh(q: torch.Tensor, lse: torch.Tensor, cache: KVCache, weights: 
     else:
         _on(index, out, "out", _F32, shape)
     table, max_pages, lens, starts, b = _batch(index, block_table, kv_lens, row_starts)
+    ws_ptr, ws_bytes = None, 0
+    if workspace is None:
+        ws_bytes = (_lib or load_library()).kv_cache_weigh_workspace_bytes(rows, q_heads, cache.heads, d, b, max_pages,
+                                                                           cache.page_size, max_rows, max_kv)
+        if ws_bytes > 0:
+            workspace = _empty((ws_bytes,), (1,), dtype=_U8, device=cache.device)
+            ws_ptr = workspace.data_ptr()
+    else:
+        _on(index, workspace, "workspace", _U8, None)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
     _launch("kv_cache_weigh", index, cache._live(), q.data_ptr(), rows, q_heads, qs, d ** -0.5 if scale is None else scale,
             lse.data_ptr(), table, max_pages, lens, starts, b, 1 if causal else 0, max_rows, max_kv,
-            None if weights is None else weights.data_ptr(), out.data_ptr())
+            None if weights is None else weights.data_ptr(), out.data_ptr(), ws_ptr, ws_bytes)
     return out
+
+
+def kv_cache_weigh_workspace(rows: int, q_heads: int, cache: KVCache, b: int, max_pages: int, max_rows: int = 0,
+                             max_kv: int = 0) -> int:
+    """Bytes of workspace kv_cache_weigh needs for these sizes."""
+    need = load_library().kv_cache_weigh_workspace_bytes(rows, q_heads, cache.heads, cache.head_dim, b, max_pages,
+                                                         cache.page_size, max_rows, max_kv)
+    if need < 0:
+        raise LibquantError(LQ_ERR_INVALID_ARG, "kv_cache_weigh", "sizes out of range")
+    return need
 
 
 def kv_cache_evict(cache: KVCache, weights: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor, keep: int,

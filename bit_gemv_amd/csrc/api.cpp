@@ -839,10 +839,19 @@ lq_status prefix_attention(const lq_kv_cache *cache, const void *q_bf16, int64_t
     return launched(lq::launch_prefix_attention(a, static_cast<hipStream_t>(stream)), fn);
 }
 
+int64_t kv_cache_weigh_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b,
+                                       int64_t max_pages, int64_t page_size, int64_t max_rows, int64_t max_kv) {
+    if (!attention_sizes(rows, q_heads, heads, head_dim, b, max_pages, page_size, max_rows, max_kv) || rows > kMaxWholeRows)
+        return -1;
+    if (rows == 0 || b == 0 || max_pages == 0) return 0;
+    return lq::weigh_workspace_bytes(rows, q_heads, heads, head_dim, b, max_pages, page_size, max_rows, max_kv);
+}
+
 lq_status kv_cache_weigh(const lq_kv_cache *cache, const void *q_bf16, int64_t rows, int64_t q_heads, int64_t q_stride,
                          float scale, const float *lse, const int32_t *block_table, int64_t max_pages,
                          const int32_t *kv_lens, const int32_t *row_starts, int64_t b, int causal, int64_t max_rows,
-                         int64_t max_kv, const float *weights, float *weights_out, void *stream) {
+                         int64_t max_kv, const float *weights, float *weights_out, void *workspace,
+                         int64_t workspace_bytes, void *stream) {
     const char *fn = "kv_cache_weigh";
     lq::WeighArgs a{};
     lq_status st = check_kv(fn, cache, rows, block_table, max_pages, kv_lens, row_starts, b, max_rows, &a.c, &a.batch);
@@ -861,14 +870,20 @@ lq_status kv_cache_weigh(const lq_kv_cache *cache, const void *q_bf16, int64_t r
     if (!aligned(weights, 16)) return fail(LQ_ERR_INVALID_ARG, "%s: weights not 16-byte aligned", fn);
     if (!weights_out || !aligned(weights_out, 16))
         return fail(LQ_ERR_INVALID_ARG, "%s: weights_out null or not 16-byte aligned", fn);
+    const int64_t need = lq::weigh_workspace_bytes(rows, q_heads, cache->heads, cache->head_dim, b, max_pages,
+                                                   cache->page_size, max_rows, max_kv);
+    if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
+        return fail(LQ_ERR_INVALID_ARG, "%s: workspace null, not 256-byte aligned or smaller than %lld bytes", fn,
+                    (long long)need);
     const int64_t codes = kv_code_bytes(cache), meta = kv_meta_bytes(cache), zeros = cache->symmetric ? 0 : meta;
     const Range out{weights_out, meta}, in{weights, weights ? meta : 0};
-    if (any_overlap({out}, {{q_bf16, ((rows - 1) * q_stride + width) * 2}, {lse, rows * q_heads * 4},
+    if (any_overlap({out, {workspace, need}},
+                    {{q_bf16, ((rows - 1) * q_stride + width) * 2}, {lse, rows * q_heads * 4},
                             {cache->k_codes, codes}, {cache->v_codes, codes}, {cache->k_scales, meta},
                             {cache->v_scales, meta}, {cache->k_zeros, zeros}, {cache->v_zeros, zeros},
                             {block_table, b * max_pages * 4}, {kv_lens, b * 4}, {row_starts, (b + 1) * 4}}) ||
-        (weights_out != weights && overlap(out, in)))
-        return fail(LQ_ERR_INVALID_ARG, "%s: an output overlaps an input", fn);
+        overlap({workspace, need}, in) || (weights_out != weights && overlap(out, in)))
+        return fail(LQ_ERR_INVALID_ARG, "%s: an output overlaps an input or another output", fn);
     if ((st = need_device()) != LQ_OK) return st;
     a.batch.whole = !causal;
     a.q = static_cast<const uint16_t *>(q_bf16);
@@ -880,6 +895,7 @@ lq_status kv_cache_weigh(const lq_kv_cache *cache, const void *q_bf16, int64_t r
     a.out = weights_out;
     a.max_rows = max_rows;
     a.max_kv = max_kv;
+    a.workspace = workspace;
     return launched(lq::launch_kv_weigh(a, static_cast<hipStream_t>(stream)), fn);
 }
 

@@ -1201,11 +1201,15 @@ Pass pass_of(int row_tile, int64_t rows, int64_t group, int64_t heads, int64_t h
         // average, and short contexts before the rows only.
         constexpr int64_t kCut = 1200;
         const int64_t slots = row_tile == 256 || head_dim == 256 ? 256 : 512, load = likely * heads;
-        // Rows that see everything have all of it before them.
-        const int64_t after = whole_rows ? 0 : n < kv ? n : kv;
-        const int64_t mean = b == 1 ? kv - after / 2 : kv / 2, prior = kv - after;
+        const int64_t mean = b == 1 ? kv - (n < kv ? n : kv) / 2 : kv / 2, prior = n < kv ? kv - n : 0;
         const int64_t idle = (load + slots - 1) / slots * slots - load;
         p.by_unit = load >= 4 * slots || (kv <= load * mean / slots + kCut && (b == 1 ? idle * prior <= kCut * slots : prior <= kCut));
+        // Rows that see everything: units of one length, so the last round's idle
+        // blocks against the cut. Measured, spans and units, 64 / 8 heads of 128: 1100
+        // and 647 rows over 8000 555 and 571 us, 16 x 60 over 1500 76 and 65, 2000
+        // over 1500 203 and 185, 512 over 4096 106 and 138; 8 x 200 over 1500, 32 /
+        // 32 heads 77 and 62; 4 x 500 over 3000, 14 / 2 heads of 64 48 and 78.
+        if (whole_rows) p.by_unit = idle * kv <= kCut * slots;
     } else {
         // Decode batches of short contexts, which would spend longer on the
         // second launch, and of up to 2048 tokens where units fill the card. Spans

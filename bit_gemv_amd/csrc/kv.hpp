@@ -77,6 +77,7 @@ struct WeighArgs {
     const float *lse, *weights;
     float *out;
     int64_t max_rows, max_kv;
+    void *workspace;
 };
 
 // Eviction by weight from the sequences' pages to the front of to_table's.
@@ -94,6 +95,8 @@ struct EvictArgs {
 
 hipError_t launch_kv_write(const KvWriteArgs &a, hipStream_t st);
 hipError_t launch_kv_read(const KvReadArgs &a, hipStream_t st);
+int64_t weigh_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b, int64_t max_pages,
+                              int64_t page_size, int64_t max_rows, int64_t max_kv);
 hipError_t launch_kv_weigh(const WeighArgs &a, hipStream_t st);
 hipError_t launch_kv_evict(const EvictArgs &a, hipStream_t st);
 int64_t attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b,

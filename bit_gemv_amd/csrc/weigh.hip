@@ -300,23 +300,24 @@ __global__ __launch_bounds__(64 * kWaves, 3) void weigh_few_kernel(WeighArgs a, 
 //
 // The codes less their zeros are integers of up to 9 bits, which bf16 holds
 // exactly, so the rows are multiplied as they lie. Each wave turns the codes of
-// TILES x 16 keys into operands once and keeps them; WK waves have keys of their
-// own and 4 / WK waves take turns at the rows, whose tiles the block brings
-// through two buffers in LDS. A lane's operands are one run of its key's bytes:
-// of the products' D terms step s takes the 8-element chunks g S + s.
-template <int D, int BITS, int TILES, int WK>
+// TILES x 16 keys of its own into operands once and keeps them; the block brings
+// the rows, 32 at a time, through two buffers in LDS. A lane's operands are one
+// run of its key's bytes: of the products' D terms step s takes the 8-element
+// chunks g S + s. Where a block for each run of keys would not fill the card,
+// `splits` blocks share its rows, leave their sums in the workspace, and
+// weigh_join_kernel adds them up.
+template <int D, int BITS>
 struct Many {
-    static constexpr int WR = kWaves / WK;
-    static constexpr int KT = 16 * TILES * WK;        // keys of a block
+    static constexpr int TILES = D == 256 ? 2 : 4;
+    static constexpr int KT = 16 * TILES * kWaves;    // keys of a block
     static constexpr int S = D / 32;                  // MFMAs per 16 keys
-    static constexpr int RT = WR == 1 ? 2 : 1;        // row tiles of a wave and stage
-    static constexpr int ROWS = 16 * WR * RT;         // rows of a stage
+    static constexpr int RT = 2, ROWS = 16 * RT;      // row tiles and rows of a stage
     static constexpr int CHUNKS = D / 8;              // of 8 elements, a row
     static constexpr int LOADS = ROWS * CHUNKS / (64 * kWaves);  // chunks a thread and stage
     static constexpr int WORDS = S * BITS / 4;        // code words of a lane and key
     static constexpr float kMid = (float)(1 << (BITS - 1));
     struct Stage {
-        u32x4 ops[WR * RT][S][64];  // lane (n, g) in the place g 16 + (n ^ its chunk mod 16)
+        u32x4 ops[RT][S][64];  // lane (n, g) in the place g 16 + (n ^ its chunk mod 16)
         float minus[ROWS];          // -lse in log2, -inf for a row that adds nothing
         int sees[ROWS];             // last position it sees
     };
@@ -326,16 +327,24 @@ struct Many {
     };
 };
 
-template <int D, int BITS, bool SYM, int TILES, int WK>
-__global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void weigh_many_kernel(WeighArgs a, int cap) {
-    using C = Many<D, BITS, TILES, WK>;
+// How the many-row kernel's work is shared out: `cap` blocks a key head walk the
+// steps, the first `cut` of which `splits` blocks each share.
+struct Shares {
+    int64_t cap, cut;
+    int splits;
+    float *parts;  // [cut][splits][heads][keys of a step]
+};
+
+template <int D, int BITS, bool SYM>
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void weigh_many_kernel(WeighArgs a, Shares sh) {
+    using C = Many<D, BITS>;
+    constexpr int TILES = C::TILES;
     __shared__ typename C::Stage stage[2];
-    __shared__ float part[C::WR][C::KT], rest[kWaves][16 * TILES];
+    __shared__ float rest[kWaves][16 * TILES];
     __shared__ int key_page[kWaves][16 * TILES];  // -1: not a key
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
-    const int wk = wave % WK, wr = wave / WK;
     const int h = blockIdx.x % a.c.heads;
     const uint32_t group = (uint32_t)a.q_heads / (uint32_t)a.c.heads;
     const int shift = a.c.page_shift, ps_mask = (1 << shift) - 1;
@@ -349,7 +358,11 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void weigh_many_kern
 
     const Steps<C::KT> sched(a.batch, shift, lane);
     const int64_t all = sched.total();
-    for (int64_t pos = blockIdx.x / a.c.heads; pos < all; pos += cap) {
+    // items: the cut steps' splits, then whole steps
+    const int64_t cut = all < sh.cut ? all : sh.cut, items = cut * sh.splits + (all - cut);
+    for (int64_t item = blockIdx.x / a.c.heads; item < items; item += sh.cap) {
+        const bool split = item < cut * sh.splits;
+        const int64_t pos = split ? item / sh.splits : item - cut * (sh.splits - 1);
         const Place place = sched.at(pos);
         const KvRows &rows = place.rows;
         const int32_t *const table = a.batch.table + place.seq * a.batch.max_pages;
@@ -357,8 +370,14 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void weigh_many_kern
         const uint32_t total = (uint32_t)rows.n * group;
         // rows before the first key see none of them
         const int64_t late = k0 - rows.first;
-        const uint32_t row0 = late <= 0 ? 0 : late < rows.n ? (uint32_t)late * group : total;
-        const int stages = (int)((total - row0 + C::ROWS - 1) / C::ROWS);
+        uint32_t row0 = late <= 0 ? 0 : late < rows.n ? (uint32_t)late * group : total;
+        int stages = (int)((total - row0 + C::ROWS - 1) / C::ROWS);
+        if (split) {
+            const int64_t share = item - pos * sh.splits;
+            const int from = (int)(share * stages / sh.splits), to = (int)((share + 1) * stages / sh.splits);
+            row0 += (uint32_t)from * C::ROWS;
+            stages = to - from;
+        }
 
         // This thread's rows go on by ROWS from stage to stage: dtok tokens and drem
         // heads, or a token more and the group's heads fewer.
@@ -442,7 +461,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void weigh_many_kern
         if (stages > 0) load(x, 0);
 
         // the wave's keys: key 16 k + n of its own in lanes n
-        const int kw = k0 + 16 * TILES * wk;
+        const int kw = k0 + 16 * TILES * wave;
         int page[TILES];
         float scale[TILES], zero[TILES], acc[TILES];
         uint32_t w[TILES][C::WORDS];
@@ -487,8 +506,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void weigh_many_kern
                 rest[wave][16 * k + n] = left;
             }
 #pragma unroll
-            for (int s = 0; s < C::S; ++s)
-            {
+            for (int s = 0; s < C::S; ++s) {
                 // INT4: even elements are the low nibbles of the bytes, odd ones the
                 // high (hidden from the compiler, which otherwise shifts every code
                 // by itself instead of converting bytes)
@@ -521,20 +539,19 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void weigh_many_kern
             const typename C::Stage &b = stage[st & 1];
 #pragma unroll
             for (int r = 0; r < C::RT; ++r) {
-                const int tile = wr * C::RT + r;
                 bf16x8 qf[C::S];
 #pragma unroll
                 for (int s = 0; s < C::S; ++s)
-                    qf[s] = __builtin_bit_cast(bf16x8, b.ops[tile][s][g * 16 + ((n ^ (g * C::S + s)) & 15)]);
-                const f32x4 nl = *reinterpret_cast<const f32x4 *>(&b.minus[16 * tile + 4 * g]);
+                    qf[s] = __builtin_bit_cast(bf16x8, b.ops[r][s][g * 16 + ((n ^ (g * C::S + s)) & 15)]);
+                const f32x4 nl = *reinterpret_cast<const f32x4 *>(&b.minus[16 * r + 4 * g]);
                 // keys that some row of the tile does not see
-                const bool masked = row0 + st * C::ROWS + 16 * tile < safe;
+                const bool masked = row0 + st * C::ROWS + 16 * r < safe;
                 auto weigh = [&](auto masked_keys, auto wide_zeros) {
                     int last[4];
                     f32x4 qs{0.0f, 0.0f, 0.0f, 0.0f};  // the rows' sums
                     if constexpr (masked_keys) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) last[i] = b.sees[16 * tile + 4 * g + i];
+                        for (int i = 0; i < 4; ++i) last[i] = b.sees[16 * r + 4 * g + i];
                     }
                     if constexpr (wide_zeros) {
                         bf16x8 ones;
@@ -569,32 +586,60 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void weigh_many_kern
             lds_barrier();  // the next stage is written, and this one read by all
         }
 #pragma unroll
-        for (int k = 0; k < TILES; ++k) acc[k] = add_halves32(add_halves16(acc[k]));
-        if constexpr (C::WR > 1) {
-#pragma unroll
-            for (int k = 0; k < TILES; ++k)
-                if (g == 0) part[wr][16 * (TILES * wk + k) + n] = acc[k];
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < TILES; ++k) {
-                acc[k] = 0.0f;
-#pragma unroll
-                for (int r = 0; r < C::WR; ++r) acc[k] += part[r][16 * (TILES * wk + k) + n];
+        for (int k = 0; k < TILES; ++k) {
+            const float sum = add_halves32(add_halves16(acc[k]));
+            if (g != k % 4) continue;
+            if (split) {
+                sh.parts[(item * a.c.heads + h) * C::KT + 16 * (TILES * wave + k) + n] = sum;
+            } else if (const int p = key_page[wave][16 * k + n]; p >= 0) {
+                const int key = kw + 16 * k + n;
+                const int64_t slot = (((int64_t)p * a.c.heads + h) << shift) + (key & ps_mask);
+                // the call's own tokens start from nothing
+                const bool old = a.weights && key < rows.first;
+                a.out[slot] = (old ? a.weights[slot] : 0.0f) + sum;
             }
         }
-        if (wr == 0) {
-#pragma unroll
-            for (int k = 0; k < TILES; ++k)
-                if (const int p = key_page[wave][16 * k + n]; g == k % 4 && p >= 0) {
-                    const int key = kw + 16 * k + n;
-                    const int64_t slot = (((int64_t)p * a.c.heads + h) << shift) + (key & ps_mask);
-                    // the call's own tokens start from nothing
-                    const bool old = a.weights && key < rows.first;
-                    a.out[slot] = (old ? a.weights[slot] : 0.0f) + acc[k];
-                }
-        }
-        if constexpr (C::WR > 1) __syncthreads();  // the parts are read
     }
+}
+
+// Adds the splits' sums of the cut steps up, in order: a block a step and head,
+// a thread a key.
+template <int KT>
+__global__ __launch_bounds__(KT) void weigh_join_kernel(WeighArgs a, Shares sh) {
+    const int h = blockIdx.x % a.c.heads;
+    const int64_t pos = blockIdx.x / a.c.heads;
+    const int shift = a.c.page_shift;
+    const Steps<KT> sched(a.batch, shift, threadIdx.x & 63);
+    if (pos >= sched.total()) return;
+    const Place place = sched.at(pos);
+    const int64_t key = (pos - place.start) * KT + threadIdx.x;
+    if (key >= place.rows.len) return;
+    const int64_t page = kv_page(a.batch, place.seq, key, shift, a.c.pages);
+    if (page < 0) return;
+    const int64_t slot = ((page * a.c.heads + h) << shift) + (key & ((1 << shift) - 1));
+    float sum = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < sh.splits; ++i) sum += sh.parts[((pos * sh.splits + i) * a.c.heads + h) * KT + threadIdx.x];
+    const bool old = a.weights && key < place.rows.first;
+    a.out[slot] = (old ? a.weights[slot] : 0.0f) + sum;
+}
+
+// The steps of KT keys that the bounds allow for and, where that many blocks do
+// not fill the card, how many share each one's rows.
+struct Cut {
+    int64_t steps;
+    int splits;
+};
+Cut cut_of(int64_t rows, int64_t group, int64_t heads, int64_t head_dim, int64_t b, int64_t room, int64_t max_rows,
+           int64_t max_kv) {
+    const int64_t n = max_rows <= 0 || max_rows > rows ? rows : max_rows, kv = max_kv <= 0 || max_kv > room ? room : max_kv;
+    if (n * group <= 16) return {0, 1};
+    const int64_t keys = head_dim == 256 ? Many<256, 8>::KT : Many<128, 8>::KT;
+    const int64_t steps = b * ((kv + keys - 1) / keys < 1 ? 1 : (kv + keys - 1) / keys);
+    // Two rounds of the three blocks a CU has room for, each of 128 rows or more.
+    const int64_t fill = 1536 / (steps * heads), most = (n * group + 127) / 128;
+    const int64_t splits = fill < most ? fill : most;
+    return {splits > 1 ? steps : 0, splits > 1 ? (int)splits : 1};
 }
 
 }  // namespace
@@ -605,27 +650,34 @@ static hipError_t launch(const WeighArgs &a, hipStream_t st) {
     const int64_t room = a.batch.max_pages << a.c.page_shift;
     const int64_t n = a.max_rows <= 0 || a.max_rows > a.batch.rows ? a.batch.rows : a.max_rows;
     const int64_t kv = a.max_kv <= 0 || a.max_kv > room ? room : a.max_kv;
-    // blocks a key head: no more than steps of work, nor than `most` in all
-    auto blocks = [&](int64_t step, int64_t most) {
-        const int64_t steps = b * ((kv + step - 1) / step < 1 ? 1 : (kv + step - 1) / step);
+    // blocks a key head: no more than `each` for each step of work, nor than `most` in all
+    auto blocks = [&](int64_t step, int64_t each, int64_t most) {
+        const int64_t steps = b * ((kv + step - 1) / step < 1 ? 1 : (kv + step - 1) / step) * each;
         const int64_t cap = (most + heads - 1) / heads;
-        return (int)(cap < steps ? cap : steps);
+        return cap < steps ? cap : steps;
     };
     if (n * group <= 16) {
-        const int cap = blocks(kFewStep, 768);
+        const int cap = (int)blocks(kFewStep, 1, 768);
         hipLaunchKernelGGL((weigh_few_kernel<D, BITS, SYM>), dim3((uint32_t)(cap * heads)), dim3(64 * kWaves), 0, st, a, cap);
         return hipGetLastError();
     }
-    auto many = [&](auto kernel, int64_t keys) {
-        // more steps than that are walked: with no bound of the lengths most of a
-        // wide table's steps may hold nothing
-        const int cap = blocks(keys, 1 << 12);
-        hipLaunchKernelGGL(kernel, dim3((uint32_t)(cap * heads)), dim3(64 * kWaves), 0, st, a, cap);
-        return hipGetLastError();
-    };
-    constexpr int TILES = D == 256 ? 2 : 4;
-    if (blocks(TILES * 64, 1 << 20) * heads >= 512) return many(weigh_many_kernel<D, BITS, SYM, TILES, 4>, TILES * 64);
-    return many(weigh_many_kernel<D, BITS, SYM, 2, 1>, 32);
+    constexpr int KT = Many<D, BITS>::KT;
+    const Cut c = cut_of(a.batch.rows, group, heads, D, b, room, a.max_rows, a.max_kv);
+    // more steps than that are walked: with no bound of the lengths most of a wide
+    // table's steps may hold nothing
+    const Shares sh{blocks(KT, c.splits, 1 << 12), c.steps, c.splits, static_cast<float *>(a.workspace)};
+    hipLaunchKernelGGL((weigh_many_kernel<D, BITS, SYM>), dim3((uint32_t)(sh.cap * heads)), dim3(64 * kWaves), 0, st, a, sh);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || c.splits == 1) return e;
+    hipLaunchKernelGGL(weigh_join_kernel<KT>, dim3((uint32_t)(c.steps * heads)), dim3(KT), 0, st, a, sh);
+    return hipGetLastError();
+}
+
+int64_t weigh_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b, int64_t max_pages,
+                              int64_t page_size, int64_t max_rows, int64_t max_kv) {
+    const Cut c = cut_of(rows, q_heads / heads, heads, head_dim, b, max_pages * page_size, max_rows, max_kv);
+    const int64_t keys = head_dim == 256 ? Many<256, 8>::KT : Many<128, 8>::KT;
+    return c.steps * c.splits * heads * keys * 4;
 }
 
 hipError_t launch_kv_weigh(const WeighArgs &a, hipStream_t st) {

@@ -595,13 +595,17 @@ lq_status prefix_attention(const lq_kv_cache *cache, const void *q_bf16, int64_t
  * row_starts counting them: positions count from the end.
  * Weights are relative to their exact value off by at most a few times 2^-24
  * of the largest |scale q . k_hat| and |lse|, and by 2^-24 for each addition;
- * sums in a fixed order: equal calls give equal bits. Other arguments and errors
- * as paged_attention; at most 2^30 rows; no workspace.
+ * sums in a fixed order: equal calls give equal bits. workspace (of
+ * kv_cache_weigh_workspace_bytes), other arguments and errors as
+ * paged_attention; at most 2^30 rows.
  */
+int64_t kv_cache_weigh_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b,
+                                       int64_t max_pages, int64_t page_size, int64_t max_rows, int64_t max_kv);
 lq_status kv_cache_weigh(const lq_kv_cache *cache, const void *q_bf16, int64_t rows, int64_t q_heads, int64_t q_stride,
                          float scale, const float *lse, const int32_t *block_table, int64_t max_pages,
                          const int32_t *kv_lens, const int32_t *row_starts, int64_t b, int causal, int64_t max_rows,
-                         int64_t max_kv, const float *weights, float *weights_out, void *stream);
+                         int64_t max_kv, const float *weights, float *weights_out, void *workspace,
+                         int64_t workspace_bytes, void *stream);
 
 /*
  * kv_cache_evict -- shrink sequences to `keep` tokens by weight. Of a sequence i

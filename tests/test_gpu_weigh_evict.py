@@ -81,8 +81,8 @@ def _weigh(seqs, d, bits, sym, page=16, heads=2, group=4, seed=0, causal=True, h
 @pytest.mark.parametrize("bits,sym", FORMATS)
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_weigh_formats(d, bits, sym, causal):
-    """Bounds that choose each kernel, right and wrong: rows streamed past 32 keys
-    and past 64 or 128 (a wide table and no bound), keys past 16 rows."""
+    """Bounds that choose each kernel, right and wrong: rows streamed past keys,
+    shared by blocks and (a wide table and no bound) not; keys past 16 rows."""
     _weigh(SEQS, d, bits, sym, seed=d + bits, causal=causal, hints=((0, 0), (70, 261), (4, 261), (1, 17)))
     _weigh(SEQS, d, bits, sym, seed=d + bits, causal=causal, wide=512, hints=((0, 0), (1, 0)))
 
@@ -106,6 +106,16 @@ def test_weigh_pages_and_long_sequences(page):
     _weigh([(1300, 1), (270, 18), (257, 257), (5, 2)], 64, 8, True, page=page, heads=1, group=2, seed=page,
            hints=((0, 0), (1, 1300)))
     _weigh([(9001, 2)], 64, 4, False, page=page, heads=1, group=1, seed=page, hints=((2, 9001), (40, 9001)))
+
+
+@pytest.mark.parametrize("d,bits,sym", [(64, 8, True), (128, 4, False), (256, 8, False)])
+def test_weigh_shared_rows(d, bits, sym):
+    """Runs of keys whose rows several blocks share: whole prompts, chunks, rows
+    that see all; bounds of the lengths too small, so that only some runs are."""
+    seqs = [(300, 300), (500, 130), (40, 40), (700, 7), (0, 3)]
+    for causal in (True, False):
+        _weigh(seqs, d, bits, sym, seed=d, heads=1, group=3, causal=causal, hints=((0, 0), (300, 700), (300, 200), (40, 1)),
+               wide=64)
 
 
 @pytest.mark.parametrize("bits", [4, 8])
@@ -372,10 +382,14 @@ def test_guard(d, bits, sym):
         w = Guarded(meta, torch.float32)
         w.t.zero_()
         say(f"guard kv_cache_weigh D={d} {mr, mk}")
+        need = bg.kv_cache_weigh_workspace(b.rows, 6, c, 4, table.shape[1], mr, mk)
+        ws = Guarded((max(need, 256),), torch.uint8)
         for causal in (1, 0):
             _ok(lib.kv_cache_weigh(c._ref, _p(q), b.rows, 6, 6 * d, ctypes.c_float(d ** -0.5), _p(lse), _p(table),
-                                   table.shape[1], _p(lens), _p(starts), 4, causal, mr, mk, w.ptr(), w.ptr(), _st()), "weigh")
+                                   table.shape[1], _p(lens), _p(starts), 4, causal, mr, mk, w.ptr(), w.ptr(), ws.ptr(), need,
+                                   _st()), "weigh")
         w.check("weights")
+        ws.check("workspace")
     kept, new = Guarded((4, 2, 77), torch.int32), Guarded((4,), torch.int32)
     say(f"guard kv_cache_evict D={d}")
     _ok(lib.kv_cache_evict(c._ref, w.ptr(), _p(table), table.shape[1], _p(lens), 4, 77, 9, None, 0, 0, kept.ptr(), new.ptr(),

@@ -91,10 +91,10 @@ def test_attention_workspaces(lib):
 
 
 def _weigh(lib, q=E, rows=4, qh=8, qs=1024, scale=0.1, lse=F, table=G, mp=3, lens=H, starts=I, b=2, causal=1, mr=0, mk=0,
-           w=K, out=K, **kw):
+           w=K, out=K, ws=N, wsb=1 << 31, **kw):
     c = _cache(**kw)
     return lib.kv_cache_weigh(ctypes.byref(c), q, rows, qh, qs, scale, lse, table, mp, lens, starts, b, causal, mr, mk, w, out,
-                              None)
+                              ws, wsb, None)
 
 
 @pytest.mark.parametrize("kwargs,status", CACHE_REFUSALS + BATCH_REFUSALS + [
@@ -108,6 +108,22 @@ def _weigh(lib, q=E, rows=4, qh=8, qs=1024, scale=0.1, lse=F, table=G, mp=3, len
 def test_weigh_refuses(lib, kwargs, status):
     assert _weigh(lib, **kwargs) == status
     assert lib.lq_last_error() != b""
+
+
+def test_weigh_workspace(lib):
+    f = lib.kv_cache_weigh_workspace_bytes
+    for bad in ((-1, 8, 2, 128, 2, 3, 16, 0, 0), (4, 7, 2, 128, 2, 3, 16, 0, 0), (4, 8, 2, 128, -1, 3, 16, 0, 0),
+                (4, 8, 2, 128, 2, 3, 16, -1, 0), (4, 8, 2, 128, 2, 3, 0, 0, 0), ((1 << 30) + 1, 1, 1, 128, 2, 3, 16, 0, 0)):
+        assert f(*bad) == -1
+    assert f(0, 8, 2, 128, 2, 3, 16, 0, 0) == 0 and f(4, 8, 2, 128, 2, 0, 16, 0, 0) == 0
+    assert f(1000, 8, 8, 128, 1000, 100, 16, 1, 0) == 0         # single rows: no sums to add up
+    need = f(400, 8, 1, 128, 1, 64, 16, 0, 0)                    # 4 steps of 256 keys, 25 runs of 128 rows
+    assert need == 4 * 25 * 256 * 4
+    c = dict(rows=400, qh=8, heads=1, mp=64, b=1, pages=2048)
+    assert _weigh(lib, **c, wsb=need - 1) == 1 and _weigh(lib, **c, ws=None) == 1 and _weigh(lib, **c, ws=MIS) == 1
+    assert _weigh(lib, **c, ws=E) == 1 and _weigh(lib, **c, ws=K) == 1 and _weigh(lib, **c, ws=K, out=L) == 1
+    if NO_GPU:
+        assert _weigh(lib, **c, wsb=need) == 4
 
 
 def test_weigh_empty_and_no_device(lib):
