@@ -730,7 +730,7 @@ lq_status attention(const char *fn, bool whole, const lq_kv_cache *cache, const 
     if ((st = check_heads(fn, cache, q_heads, scale)) != LQ_OK) return st;
     if (rows == 0 || b == 0) return LQ_OK;
     if ((st = check_rows(fn, rows, q_heads, whole)) != LQ_OK) return st;
-    a.batch.whole = whole;
+    a.whole = whole;
     a.q = static_cast<const uint16_t *>(q_bf16);
     a.q_stride = q_stride;
     a.q_heads = (int)q_heads;
@@ -817,7 +817,6 @@ lq_status prefix_attention(const lq_kv_cache *cache, const void *q_bf16, int64_t
     if ((st = check_heads(fn, cache, q_heads, scale)) != LQ_OK) return st;
     if (rows == 0 || b == 0) return LQ_OK;
     if ((st = check_rows(fn, rows, q_heads, true)) != LQ_OK) return st;
-    a.prefix.whole = 1;
     a.max_prefix_rows = max_prefix_rows;
     a.max_prefix = max_prefix;
     a.own.q = static_cast<const uint16_t *>(q_bf16);
@@ -885,7 +884,7 @@ lq_status kv_cache_weigh(const lq_kv_cache *cache, const void *q_bf16, int64_t r
         overlap({workspace, need}, in) || (weights_out != weights && overlap(out, in)))
         return fail(LQ_ERR_INVALID_ARG, "%s: an output overlaps an input or another output", fn);
     if ((st = need_device()) != LQ_OK) return st;
-    a.batch.whole = !causal;
+    a.whole = !causal;
     a.q = static_cast<const uint16_t *>(q_bf16);
     a.q_stride = q_stride;
     a.q_heads = (int)q_heads;

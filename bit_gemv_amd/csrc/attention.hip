@@ -60,11 +60,15 @@ LQ_DEVICE float pow2_floor(float v) { return __uint_as_float(__float_as_uint(v) 
 // host needs to know no more than bounds. A block walks the pieces of units
 // in its span: whole units are written out, a unit's part (the span's first or
 // last piece) goes to the workspace and attn_join_kernel joins the parts.
+// kByUnit: every unit counts as one step, blocks take whole units. kWhole and
+// kApart: AttnArgs' whole and apart. (In one number: further arguments take scalar
+// registers all along, and decode of 16 sequences in INT4 3 % more time.)
+enum { kByUnit = 1, kWhole = 2, kApart = 4 };
 struct Span {
     float *o;   // [2 cap][heads][rows of a tile][D], relative to the part's maximum
     float *ml;  // [2 cap][heads][rows of a tile][2]: maximum (log2) and sum
     int cap;
-    int by_unit;           // every unit counts as one step: blocks take whole units
+    int form;              // kByUnit, kWhole, kApart
     uint32_t least, most;  // sequences of another number of query rows (all heads of a group) are not looked at
 };
 
@@ -96,12 +100,12 @@ struct Schedule {
         Lane x{};
         x.steps = 1;
         if (seq < bt.b) {
-            x.rows = kv_rows(bt, seq, shift);
+            x.rows = kv_rows(bt, seq, shift, span.form & kWhole);
             const uint32_t all_rows = (uint32_t)x.rows.n * (uint32_t)group;
             if (all_rows >= span.least && all_rows <= span.most) {
                 int64_t keys = x.rows.first + x.rows.n < x.rows.len ? x.rows.first + x.rows.n : x.rows.len;
                 keys = keys < 1 ? 1 : keys;  // a unit without keys is still written
-                x.steps = span.by_unit ? 1 : (int)((keys + STEP - 1) / STEP);
+                x.steps = span.form & kByUnit ? 1 : (int)((keys + STEP - 1) / STEP);
                 x.all = (int64_t)((all_rows + row_tile - 1) / (uint32_t)row_tile) * x.steps;
             }
         }
@@ -135,7 +139,7 @@ struct Schedule {
                 // Whole units: the largest first, so that the last to start are
                 // short (a prompt of 4096, 501 us in turn, 398 so).
                 const uint32_t tiles = (uint32_t)uniform_div(readlane64(x.all, src), p.steps);
-                p.tile = span.by_unit ? tiles - 1 - j : j & 1 ? tiles - 1 - (j >> 1) : j >> 1;
+                p.tile = span.form & kByUnit ? tiles - 1 - j : j & 1 ? tiles - 1 - (j >> 1) : j >> 1;
                 p.rows.begin = readlane64(x.rows.begin, src);
                 p.rows.n = readlane64(x.rows.n, src);
                 p.rows.first = readlane64(x.rows.first, src);
@@ -236,7 +240,7 @@ __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void at
         int64_t kend64 = rows.first + last_row + 1;
         kend64 = kend64 > rows.len ? rows.len : kend64;
         const int kend = kend64 < 0 ? 0 : (int)kend64;
-        if (span.by_unit) step1 = (kend + kStride - 1) / kStride;
+        if (span.form & kByUnit) step1 = (kend + kStride - 1) / kStride;
         const int kbeg = step0 * kStride < kend ? step0 * kStride : kend;
         const int kstop = (int64_t)step1 * kStride < kend ? step1 * kStride : kend;
         const int top = (kstop - 1) & ~15;  // the piece's last 16 keys
@@ -525,7 +529,9 @@ __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void at
             const uint32_t wt = wr / (uint32_t)group;
             const int64_t at = (rows.begin + wt) * a.q_heads + h * group + (wr - wt * (uint32_t)group);
             // relative to the maximum in fp32, or the result
-            float *const part = !whole ? span.o + (slot_of + r) * D : a.part_o ? a.part_o + at * D : nullptr;
+            float *const part = !whole              ? span.o + (slot_of + r) * D
+                                : span.form & kApart ? reinterpret_cast<float *>(a.out) + at * D
+                                                     : nullptr;
             const float norm = part ? 1.0f : inverse_sum(lr);
 #pragma unroll
             for (int d = 4 * c; d < D; d += 4 * kTeam) {
@@ -543,7 +549,7 @@ __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void at
             }
             if (c == 0) {
                 if (part) {
-                    float *ml = !whole ? span.ml + (slot_of + r) * 2 : a.part_ml + at * 2;
+                    float *ml = !whole ? span.ml + (slot_of + r) * 2 : a.lse + at * 2;
                     ml[0] = lr == 0.0f ? -__builtin_inff() : mr;
                     ml[1] = lr;
                 } else if (a.lse) {
@@ -686,7 +692,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
         int64_t kend64 = rows.first + block_last + 1;
         kend64 = kend64 > rows.len ? rows.len : kend64;
         const int kend = kend64 < 0 ? 0 : (int)kend64;
-        if (span.by_unit) step1 = (kend + C::KT - 1) / C::KT;
+        if (span.form & kByUnit) step1 = (kend + C::KT - 1) / C::KT;
         const int kbeg = step0 * C::KT < kend ? step0 * C::KT : kend;
         const int kstop = (int64_t)step1 * C::KT < kend ? step1 * C::KT : kend;
         const int its = (kstop - kbeg + C::KT - 1) / C::KT;
@@ -1041,7 +1047,9 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
         if (live) {
             const int64_t at = (rows.begin + tok) * a.q_heads + qh;
             const int64_t slot = slot_of + wave * 32 + n;
-            float *const part = !whole ? span.o + slot * D : a.part_o ? a.part_o + at * D : nullptr;
+            float *const part = !whole              ? span.o + slot * D
+                                : span.form & kApart ? reinterpret_cast<float *>(a.out) + at * D
+                                                     : nullptr;
             l *= sref * (1.0f / kHead);
             const float f = (part ? 1.0f : inverse_sum(l)) * (sref * (1.0f / kHead));
 #pragma unroll
@@ -1069,7 +1077,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
             }
             if (half == 0) {
                 if (part) {
-                    float *ml = !whole ? span.ml + slot * 2 : a.part_ml + at * 2;
+                    float *ml = !whole ? span.ml + slot * 2 : a.lse + at * 2;
                     ml[0] = l == 0.0f ? -__builtin_inff() : m;
                     ml[1] = l;
                 } else if (a.lse) {
@@ -1272,7 +1280,8 @@ int64_t attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, 
 
 static Span span_of(const AttnArgs &a, const Pass &p, char *workspace) {
     float *o = reinterpret_cast<float *>(workspace);
-    return {o, o + (int64_t)2 * p.cap * a.c.heads * p.row_tile * a.c.head_dim, p.cap, p.by_unit, p.least, p.most};
+    const int form = (p.by_unit ? kByUnit : 0) | (a.whole ? kWhole : 0) | (a.apart ? kApart : 0);
+    return {o, o + (int64_t)2 * p.cap * a.c.heads * p.row_tile * a.c.head_dim, p.cap, form, p.least, p.most};
 }
 static uint32_t borders_of(const AttnArgs &a, const Pass &p) {  // and key heads: blocks of the join
     return p.by_unit ? 0 : (uint32_t)((p.cap - 1) * a.c.heads);
@@ -1303,13 +1312,13 @@ static hipError_t launch_pass(const AttnArgs &a, const Pass &p, const Pass *few,
             const Span small = span_of(a, *few, ws + p.bytes);
             e = launch_tiles<D, BITS, SYM, 16>(a, *few, small, st);
             const uint32_t blocks = borders * kJoinY + borders_of(a, *few);
-            if (e != hipSuccess || blocks == 0 || a.part_o) return e;
+            if (e != hipSuccess || blocks == 0 || a.apart) return e;
             hipLaunchKernelGGL((attn_join_both_kernel<D, ROWS, step, kFewStep>), dim3(blocks), dim3(256), 0, st, a, span,
                                small, (int)borders);
             return hipGetLastError();
         }
     }
-    if (borders == 0 || a.part_o) return e;
+    if (borders == 0 || a.apart) return e;
     hipLaunchKernelGGL((attn_join_kernel<D, ROWS, step>), dim3(borders, ROWS < 128 ? 1 : kJoinY), dim3(256), 0, st, a, span);
     return hipGetLastError();
 }
@@ -1337,7 +1346,7 @@ static hipError_t launch_one(const AttnArgs &a, const Plan &p, hipStream_t st) {
 
 static Plan plan_of(const AttnArgs &a) {
     return plan_of(a.batch.rows, a.q_heads, a.c.heads, a.c.head_dim, a.c.bits, a.batch.b,
-                   a.batch.max_pages << a.c.page_shift, a.max_rows, a.max_kv, a.batch.whole);
+                   a.batch.max_pages << a.c.page_shift, a.max_rows, a.max_kv, a.whole);
 }
 
 hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st) { return launch_one(a, plan_of(a), st); }
@@ -1356,7 +1365,7 @@ struct Launched {
 struct Source {
     KvBatch batch;
     Launched launch[2];
-    int launches;
+    int launches, whole;
     const float *o, *ml;  // whole units' rows
 };
 
@@ -1376,7 +1385,7 @@ LQ_DEVICE Found find_row(const Source &s, const KvRows &x0, int64_t row, int shi
     uint32_t rows = 0;
     for (int64_t s0 = 0; s0 < bt.b && seq < 0; s0 += 64) {
         KvRows x = x0;
-        if (s0 > 0) x = s0 + lane < bt.b ? kv_rows(bt, s0 + lane, shift) : KvRows{0, 0, 0, 0};
+        if (s0 > 0) x = s0 + lane < bt.b ? kv_rows(bt, s0 + lane, shift, s.whole) : KvRows{0, 0, 0, 0};
         const uint64_t in = __ballot(row >= x.begin && row < x.begin + x.n);
         if (in) {
             const int src = __ffsll((unsigned long long)in) - 1;
@@ -1393,14 +1402,14 @@ LQ_DEVICE Found find_row(const Source &s, const KvRows &x0, int64_t row, int shi
     int64_t sum = 0;  // as Schedule adds the sequences' steps up
     for (int64_t s0 = 0; s0 < bt.b; s0 += 64) {
         KvRows x = x0;
-        if (s0 > 0) x = s0 + lane < bt.b ? kv_rows(bt, s0 + lane, shift) : KvRows{0, 0, 0, 0};
+        if (s0 > 0) x = s0 + lane < bt.b ? kv_rows(bt, s0 + lane, shift, s.whole) : KvRows{0, 0, 0, 0};
         int64_t all = 0;
         int steps = 1;
         const uint32_t n = (uint32_t)x.n * (uint32_t)group;
         if (s0 + lane < bt.b && n >= l.span.least && n <= l.span.most) {
             int64_t keys = x.first + x.n < x.len ? x.first + x.n : x.len;
             keys = keys < 1 ? 1 : keys;
-            steps = l.span.by_unit ? 1 : (int)((keys + l.step - 1) / l.step);
+            steps = l.span.form & kByUnit ? 1 : (int)((keys + l.step - 1) / l.step);
             all = (int64_t)((n + (1u << l.log_tile) - 1) >> l.log_tile) * steps;
         }
         const int64_t upto = sum + scan64(all);
@@ -1433,7 +1442,7 @@ LQ_DEVICE Parts parts_of(const Source &s, const Found &f, int64_t row, const Att
     const uint32_t rr = (uint32_t)(row - f.begin) * (uint32_t)group + head;
     const uint32_t tile = rr >> la.log_tile, r = rr & ((1u << la.log_tile) - 1);
     // the unit's place among its sequence's, as Schedule orders them
-    const uint32_t j = la.span.by_unit ? f.tiles - 1 - tile : 2 * tile < f.tiles ? 2 * tile : 2 * (f.tiles - 1 - tile) + 1;
+    const uint32_t j = la.span.form & kByUnit ? f.tiles - 1 - tile : 2 * tile < f.tiles ? 2 * tile : 2 * (f.tiles - 1 - tile) + 1;
     const int64_t start = f.start + (int64_t)j * f.steps;
     const int64_t first = lane_div(start, f.share), last = lane_div(start + f.steps - 1, f.share);
     const bool whole = first == last;
@@ -1497,7 +1506,7 @@ __global__ __launch_bounds__(256) void attn_finish_kernel(AttnArgs a, Source own
     const int heads = SPLIT ? a.q_heads : a.c.heads, group = a.q_heads / a.c.heads, shift = a.c.page_shift;
     const KvRows none{0, 0, 0, 0};
     const KvRows x0 = lane < own.batch.b ? kv_rows(own.batch, lane, shift) : none;
-    const KvRows y0 = lane < prefix.batch.b ? kv_rows(prefix.batch, lane, shift) : none;
+    const KvRows y0 = lane < prefix.batch.b ? kv_rows(prefix.batch, lane, shift, prefix.whole) : none;
     const int h = SPLIT ? blockIdx.x % heads / group : blockIdx.x % heads;
     int64_t row = (int64_t)(blockIdx.x / heads) * run;
     const int64_t end = row + run < a.batch.rows ? row + run : a.batch.rows;
@@ -1561,23 +1570,26 @@ hipError_t launch_prefix_attention(const PrefixArgs &a, hipStream_t st) {
     if (a.prefix.b == 0) return launch_paged_attention(a.own, st);
     AttnArgs side[2] = {a.own, a.own};
     side[1].batch = a.prefix;
+    side[1].whole = 1;
     side[1].max_rows = a.max_prefix_rows;
     side[1].max_kv = a.max_prefix;
     Source source[2];
     char *ws = static_cast<char *>(a.own.workspace);
     for (int i = 0; i < 2; ++i) {
         AttnArgs &x = side[i];
-        x.part_o = reinterpret_cast<float *>(ws);
+        x.apart = 1;
+        x.out = reinterpret_cast<uint16_t *>(ws);
+        x.lse = reinterpret_cast<float *>(ws + part_bytes(x.batch.rows, x.q_heads, x.c.head_dim));
         const Plan p = plan_of(x);
-        x.part_ml = reinterpret_cast<float *>(ws + part_bytes(x.batch.rows, x.q_heads, x.c.head_dim));
         ws += part_bytes(x.batch.rows, x.q_heads, x.c.head_dim) + part_bytes(x.batch.rows, x.q_heads, 2);
         x.workspace = ws;
         ws += p.bytes;
         Source &s = source[i];
         s.batch = x.batch;
         s.launches = p.passes;
-        s.o = x.part_o;
-        s.ml = x.part_ml;
+        s.whole = x.whole;
+        s.o = reinterpret_cast<float *>(x.out);
+        s.ml = x.lse;
         for (int k = 0; k < p.passes; ++k) {
             const Pass &q = p.pass[k];
             s.launch[k] = {span_of(x, q, static_cast<char *>(x.workspace) + (k ? p.pass[0].bytes : 0)),

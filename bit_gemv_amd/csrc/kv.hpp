@@ -19,7 +19,6 @@ struct KvCache {
 struct KvBatch {
     const int32_t *table, *lens, *starts;
     int64_t b, max_pages, rows;
-    int whole = 0;  // the rows are no tokens of the sequence: each sees all that it holds
 };
 
 struct KvWriteArgs {
@@ -51,10 +50,11 @@ struct AttnArgs {
     void *workspace;
     uint16_t *out;
     float *lse;
-    // in the place of out and lse, for a result that is joined with another: whole
-    // units' rows [rows][q_heads][D] relative to their maximum, maximum (log2) and
-    // sum; cut units' parts stay in the workspace
-    float *part_o = nullptr, *part_ml = nullptr;
+    int whole = 0;  // the rows are no tokens of the sequence: each sees all that it holds
+    // For a result that is joined with another: whole units' rows relative to their
+    // maximum, fp32, go to out, their maximum (log2) and sum to lse, [rows][q_heads][2];
+    // cut units' parts stay in the workspace.
+    int apart = 0;
 };
 
 // Attention over a prefix that several sequences share and over their own
@@ -78,6 +78,7 @@ struct WeighArgs {
     float *out;
     int64_t max_rows, max_kv;
     void *workspace;
+    int whole;  // as AttnArgs'
 };
 
 // Eviction by weight from the sequences' pages to the front of to_table's.
@@ -114,7 +115,7 @@ struct KvRows {
     int64_t begin, n, first, len;  // len: tokens held, cut to the table
 };
 
-__device__ __forceinline__ KvRows kv_rows(const KvBatch &bt, int64_t seq, int page_shift) {
+__device__ __forceinline__ KvRows kv_rows(const KvBatch &bt, int64_t seq, int page_shift, bool whole = false) {
     const int64_t s0 = bt.starts[seq], s1 = bt.starts[seq + 1], held = bt.lens[seq];
     KvRows r;
     r.begin = s0 < 0 ? 0 : s0;
@@ -122,7 +123,7 @@ __device__ __forceinline__ KvRows kv_rows(const KvBatch &bt, int64_t seq, int pa
     r.n = end > r.begin ? end - r.begin : 0;
     const int64_t room = bt.max_pages << page_shift;
     r.len = held > room ? room : held;
-    r.first = bt.whole ? r.len : held - (s1 - r.begin);
+    r.first = whole ? r.len : held - (s1 - r.begin);
     return r;
 }
 

@@ -37,19 +37,20 @@ struct Steps {
         int64_t steps, upto;
     };
     const KvBatch &bt;
+    const bool whole;
     const int shift, lane;
     Lane first;
 
     LQ_DEVICE Lane load(int64_t seq, int64_t before) const {
         Lane x{};
         if (seq < bt.b) {
-            x.rows = kv_rows(bt, seq, shift);
+            x.rows = kv_rows(bt, seq, shift, whole);
             x.steps = x.rows.n > 0 && x.rows.len > 0 ? (x.rows.len + STEP - 1) / STEP : 0;
         }
         x.upto = before + scan64(x.steps);
         return x;
     }
-    LQ_DEVICE Steps(const KvBatch &b, int sh, int l) : bt(b), shift(sh), lane(l) { first = load(l, 0); }
+    LQ_DEVICE Steps(const WeighArgs &a, int l) : bt(a.batch), whole(a.whole), shift(a.c.page_shift), lane(l) { first = load(l, 0); }
     LQ_DEVICE int64_t total() const {
         int64_t sum = readlane64(first.upto, 63);
         for (int64_t s0 = 64; s0 < bt.b; s0 += 64) sum = readlane64(load(s0 + lane, sum).upto, 63);
@@ -117,7 +118,7 @@ __global__ __launch_bounds__(64 * kWaves, 3) void weigh_few_kernel(WeighArgs a, 
     __shared__ float held[kWaves][kLate * 32];
     __shared__ int64_t held_at[kWaves][kLate * 2];
 
-    const Steps<kFewStep> sched(a.batch, shift, lane);
+    const Steps<kFewStep> sched(a, lane);
     const int64_t all = sched.total(), share = uniform_div(all + cap - 1, cap);
     const int64_t begin = block * share, end = begin + share < all ? begin + share : all;
     for (int64_t pos = begin; pos < end;) {
@@ -356,7 +357,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 3) void weigh_many_kern
     const int64_t dq = dtok * a.q_stride + drem * D;
     const int dl = (int)(dtok * a.q_heads + drem);
 
-    const Steps<C::KT> sched(a.batch, shift, lane);
+    const Steps<C::KT> sched(a, lane);
     const int64_t all = sched.total();
     // items: the cut steps' splits, then whole steps
     const int64_t cut = all < sh.cut ? all : sh.cut, items = cut * sh.splits + (all - cut);
@@ -609,7 +610,7 @@ __global__ __launch_bounds__(KT) void weigh_join_kernel(WeighArgs a, Shares sh) 
     const int h = blockIdx.x % a.c.heads;
     const int64_t pos = blockIdx.x / a.c.heads;
     const int shift = a.c.page_shift;
-    const Steps<KT> sched(a.batch, shift, threadIdx.x & 63);
+    const Steps<KT> sched(a, threadIdx.x & 63);
     if (pos >= sched.total()) return;
     const Place place = sched.at(pos);
     const int64_t key = (pos - place.start) * KT + threadIdx.x;
