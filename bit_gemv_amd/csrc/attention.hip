@@ -1357,7 +1357,10 @@ hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st) { return la
 // them as the rows of one sequence that each see everything, in tiles as a
 // prompt's rows are. The own tokens' pass is paged_attention's. Both leave whole
 // units as rows relative to their maximum and cut ones as parts, and
-// attn_finish_kernel joins what either has of a row.
+// attn_finish_kernel joins what either has of a row: one launch of 12 us for 64
+// sequences of 64 heads, where joins of each pass and a merge took 26, and of 7 for
+// 4, where they took 17. 64 rows behind 8192 shared tokens: own tokens (up to 1024
+// each) 22 us, bound by HBM, the prefix 41, by the matrix units, of 75 in all.
 struct Launched {
     Span span;
     int log_tile, step;  // rows of a tile (log2), keys of a step
@@ -1599,7 +1602,10 @@ hipError_t launch_prefix_attention(const PrefixArgs &a, hipStream_t st) {
         const hipError_t e = launch_one(x, p, st);
         if (e != hipSuccess) return e;
     }
-    // few rows: teams beside each other for the parts as well
+    // Few rows: teams beside each other for the parts as well. With and without,
+    // rows of 64 / 8 heads: 4 behind 2011 tokens 24.5 and 32.3 us a call, 16 behind
+    // 4096 48.0 and 50.7, 64 behind 8192 94.0 and 74.8. 2048, 1024 and 512 blocks of
+    // 439296 threads' work: 19.3, 21.7 and 26.2.
     const int64_t rows = a.own.batch.rows, heads = a.own.c.heads;
     auto finish = [&](auto split_kernel, auto kernel) {
         if (rows * a.own.q_heads <= 1024) {
