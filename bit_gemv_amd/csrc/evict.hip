@@ -10,8 +10,8 @@
 // table's pages. In place tokens move to earlier positions or stay, in order: a
 // batch of tokens is read whole before any of it is written, and what later
 // batches read lies behind what earlier ones write, so one block takes all tokens
-// of a sequence and head, or of some bytes of their codes. Into other pages the
-// tokens are shared out as well. Bound by HBM with scattered rows of 64 or 128 bytes
+// of a sequence and head, or of some bytes of their codes. Into other pages
+// batches are shared out as well, unless some of them are the sequence's own. Bound by HBM with scattered rows of 64 or 128 bytes
 // and quads of values of which one token in two to four stays: 16 sequences of up to
 // 8192 tokens to 2048, 8 heads, INT8, 46 us for 178 MB, 3.9 TB/s; 6 of up to 30000 to
 // 4000, 32 heads, INT4, 108 us for 437 MB.
@@ -199,6 +199,7 @@ constexpr int kBatch = 1024;  // tokens
 template <int ROW>  // code bytes of a token
 __global__ __launch_bounds__(kMove) void evict_move_kernel(EvictArgs a, Shares sh) {
     __shared__ int64_t from[kBatch], to[kBatch];  // slots of the head's tokens, or -1
+    __shared__ int own;                           // to_table has pages of the table
     const int roles = 1 + sh.keys + sh.values;
     const int h = blockIdx.x % a.c.heads;
     const int role = blockIdx.x / a.c.heads % roles;
@@ -216,7 +217,14 @@ __global__ __launch_bounds__(kMove) void evict_move_kernel(EvictArgs a, Shares s
         const int64_t page = tab[pos >> shift];
         return page < 0 || page >= a.c.pages ? -1 : ((page * a.c.heads + h) << shift) + (pos & mask);
     };
-    for (int64_t at = (int64_t)split * kBatch; at < count; at += (int64_t)sh.splits * kBatch) {
+    // to_table may hold some of the table's pages, in their own places: what a batch
+    // writes there lies before what later ones read, and one block takes them all.
+    // Found out beside the first batch's lookups, for half a microsecond of 47
+    // or 109 (one or two in front of them).
+    bool ask = sh.splits > 1 && count > kBatch;
+    int splits = sh.splits;
+    if (threadIdx.x == 0) own = 0;
+    for (int64_t at = (int64_t)split * kBatch; at < count; at += (int64_t)splits * kBatch) {
         const int j0 = (int)at, n = count - j0 < kBatch ? count - j0 : kBatch;
         __syncthreads();  // nobody reads the last lookups any more
 #pragma unroll
@@ -227,7 +235,15 @@ __global__ __launch_bounds__(kMove) void evict_move_kernel(EvictArgs a, Shares s
                 to[i] = slot_of(to_table, j0 + i);
             }
         }
+        if (ask)
+            for (int i = threadIdx.x; i <= (count - 1) >> shift; i += kMove)
+                if (table[i] == to_table[i]) own = 1;
         __syncthreads();
+        if (ask && own) {
+            if (split > 0) return;
+            splits = 1;
+        }
+        ask = false;
         if (role == 0) {
             float *const src[5] = {a.weights, a.c.k_scales, a.c.v_scales, a.c.k_zeros, a.c.v_zeros};
             const int arrays = a.c.symmetric ? 3 : 5;

@@ -325,6 +325,36 @@ def test_shared_pages_are_read_only_when_moved_elsewhere():
         assert_same_bits(host(getattr(gpu, n))[b.lists[0]], getattr(ref, n)[b.lists[0]], n)
 
 
+@pytest.mark.parametrize("bits,sym", FORMATS)
+def test_some_pages_stay_in_their_place(bits, sym):
+    """to_table with fresh pages beside some of the sequence's own: batches of
+    tokens are then moved in order, beside a sequence that moves altogether."""
+    rng = np.random.default_rng(bits)
+    page, keep = 16, 4000
+    b = Batch([(9000, 0), (5000, 0), (keep, 0), (keep, 0)], page, rng)
+    ref = new_cache(b, page, 2, 64, bits, sym)
+    for t in (ref.k_codes, ref.v_codes):
+        t[:] = rng.integers(0, 256, t.shape, dtype=np.uint8)
+    for t in (ref.k_scales, ref.v_scales, ref.k_zeros, ref.v_zeros):
+        if t is not None:
+            t[:] = rng.random(t.shape, dtype=np.float32)
+    w = _weights(ref, rng)
+    mixed = [old if i % 3 else new for i, (old, new) in enumerate(zip(b.lists[0], b.lists[2]))]
+    to = [mixed, b.lists[3]]
+    gpu, wg = to_gpu(ref), dev(w)
+    say(f"evict, some pages stay, bits={bits} sym={sym}")
+    table = dev(np.ascontiguousarray(b.table[:2]))
+    lens, kept = bg.kv_cache_evict(gpu, wg, table, _i32([9000, 5000]), keep, 100, to_table=_i32(to))
+    want_kept, want_lens = serving.evict(ref, w, b.lists[:2], [9000, 5000], keep, 100, to)
+    assert host(lens).tolist() == want_lens
+    assert_same_bits(host(kept), want_kept, "kept")
+    want = _state(ref, w)
+    for name in want:
+        got = host(wg if name == "weights" else getattr(gpu, name))
+        for pages in to:
+            assert np.array_equal(got[pages], want[name][pages], equal_nan=True), name
+
+
 def test_graph_of_a_decode_step_with_eviction():
     """Write, attention, weigh and evict captured once and replayed while lengths
     grow and shrink in device memory: every replay gives the eager calls' bits."""
