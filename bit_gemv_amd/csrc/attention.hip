@@ -182,6 +182,12 @@ struct Few {
     static constexpr int STEPS = D / 32;             // score MFMAs per 16 keys
     static constexpr int TILES = D / 16;             // output MFMA tiles
     static constexpr float kMid = (float)(1 << (BITS - 1));
+    // Keys by streaming loads, as the values, but for asymmetric ones of 128 bytes.
+    // Streaming and ordinary, INT8 asymmetric: 24 sequences up to 1500 on 32 heads
+    // 52.3 and 46.4 us, 64 of 32 heads 121 and 112, 24 up to 6000 on 8 heads 55.1 and
+    // 50.6, 96 up to 200 47.1 and 48.1; symmetric 64 up to 16384 221 and 226, 24 up to
+    // 6000 41.7 and 44.0; INT4 16 up to 8192 32.4 and 34.6; 64 bytes 24.6 and 25.8.
+    static constexpr bool kStreamKeys = SYM || kRow != 128;
 
     struct Tile {
         uint32_t k[2][KW], v[2][KW];
@@ -277,7 +283,7 @@ __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void at
             for (int u = 0; u < 2; ++u) {
                 const uint8_t *kp = a.c.k_codes + slots[u] * C::kRow;
 #pragma unroll
-                for (int j = 0; j < C::NV; ++j) load_words<C::VEC, true>(x.k[u] + j * C::VEC, kp + j * 64 + k_off);
+                for (int j = 0; j < C::NV; ++j) load_words<C::VEC, C::kStreamKeys>(x.k[u] + j * C::VEC, kp + j * 64 + k_off);
             }
 #pragma unroll
             for (int u = 0; u < C::US; ++u) {
