@@ -8,7 +8,7 @@
 // to one block, which goes through all rows that see it, or to a few that share
 // the rows and leave sums that a second launch adds up: no atomics, sums in a
 // fixed order. Single tokens are bound by HBM: 64 sequences of up to 16384 tokens,
-// 8 heads of 128, INT8, 154 us for 772 MB. Chunks are bound by the matrix and the
+// 8 heads of 128, INT8, 156 us for 772 MB. Chunks are bound by the matrix and the
 // vector units, whose times add up: of 64 scores of 128 elements a wave's products
 // take 16 clocks, exponentials 8, scaling and sum 8. The last 500 rows of three
 // prompts of up to 6000 tokens, 32 heads of 128, INT4: 66 us, 0.67 PFLOP/s.
@@ -86,8 +86,9 @@ struct Steps {
 // Wave w of a block walks its span's 32-key tiles w, w + 4, ..., the next two
 // tiles' codes on their way: a tile's registers take the one after the next as
 // soon as it has been multiplied. Two tiles on their way and one: 158 and 173 us
-// for 64 sequences of up to 16384 tokens. Ordinary loads and streaming ones: 154 and
-// 157, and 16.3 and 17.1 for 64 up to 4000.
+// for 64 sequences of up to 16384 tokens. Streaming loads and ordinary ones: 157 and
+// 154, but 32 sequences up to 8000 38.3 and 39.6 (INT4 26.5 and 28.3, 64-wide 22.8
+// and 25.8).
 template <int D, int BITS>
 struct Few {
     static constexpr int kRow = D * BITS / 8;    // code bytes of a key
@@ -183,7 +184,7 @@ __global__ __launch_bounds__(64 * kWaves, 3) void weigh_few_kernel(WeighArgs a, 
                     (u ? at.slot1 : at.slot0) = slot;
                     const uint8_t *kp = a.c.k_codes + slot * C::kRow;
 #pragma unroll
-                    for (int j = 0; j < C::NV; ++j) load_words<C::VEC, false>(x.k[u] + j * C::VEC, kp + j * 64 + k_off);
+                    for (int j = 0; j < C::NV; ++j) load_words<C::VEC, true>(x.k[u] + j * C::VEC, kp + j * 64 + k_off);
                     x.sk[u] = a.c.k_scales[slot + n];
                     if (!SYM) x.zk[u] = a.c.k_zeros[slot + n];
                 }
