@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libquant.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["api.cpp", "quantize.hip", "gemv.hip", "gemv_shared.hip", "gemv8.hip", "gemm.hip", "smooth.hip", "w8a8.hip", "awq.hip", "mx.hip", "gptq.hip", "probe.hip",
-           "norm.hip", "kvcache.hip", "attention.hip", "weigh.hip", "evict.hip"]
+           "norm.hip", "kvcache.hip", "attention.hip", "cross.hip", "weigh.hip", "evict.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -45,6 +45,7 @@ EXTRA = {
     "gemv_shared.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "awq.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "cross.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "weigh.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 

@@ -744,7 +744,8 @@ lq_status attention(const char *fn, bool whole, const lq_kv_cache *cache, const 
                                                        cache->page_size, max_rows, max_kv, whole);
     st = check_attention(fn, cache, q_bf16, q_stride, need, workspace, workspace_bytes, out_bf16, lse, {}, a);
     if (st != LQ_OK) return st;
-    return launched(lq::launch_paged_attention(a, static_cast<hipStream_t>(stream)), fn);
+    const hipStream_t on = static_cast<hipStream_t>(stream);
+    return launched(whole ? lq::launch_cross_attention(a, on) : lq::launch_paged_attention(a, on), fn);
 }
 
 int64_t attention_workspace(bool whole, int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b,

@@ -105,7 +105,8 @@ int64_t attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, 
 int64_t prefix_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t page_size,
                                int64_t p, int64_t prefix_pages, int64_t max_prefix_rows, int64_t max_prefix, int64_t b,
                                int64_t max_pages, int64_t max_rows, int64_t max_kv);
-hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st);
+hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st);  // neither whole nor apart
+hipError_t launch_cross_attention(const AttnArgs &a, hipStream_t st);
 hipError_t launch_prefix_attention(const PrefixArgs &a, hipStream_t st);
 
 // One sequence's rows: [begin, begin + n) of the row tensors, row begin + i at
