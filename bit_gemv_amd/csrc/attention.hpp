@@ -186,12 +186,12 @@ struct Few {
     static constexpr int STEPS = D / 32;             // score MFMAs per 16 keys
     static constexpr int TILES = D / 16;             // output MFMA tiles
     static constexpr float kMid = (float)(1 << (BITS - 1));
-    // Keys by streaming loads, as the values, but for asymmetric ones of 128 bytes.
-    // Streaming and ordinary, INT8 asymmetric: 24 sequences up to 1500 on 32 heads
-    // 52.3 and 46.4 us, 64 of 32 heads 121 and 112, 24 up to 6000 on 8 heads 55.1 and
-    // 50.6, 96 up to 200 47.1 and 48.1; symmetric 64 up to 16384 221 and 226, 24 up to
-    // 6000 41.7 and 44.0; INT4 16 up to 8192 32.4 and 34.6; 64 bytes 24.6 and 25.8.
-    static constexpr bool kStreamKeys = SYM || kRow != 128;
+    // Keys come by streaming loads, as the values, but asymmetric INT8 ones of 128-wide
+    // heads by either (pass_of). Streaming and ordinary, symmetric: 64 sequences up to
+    // 16384 tokens 221 and 226 us, 24 up to 6000 41.7 and 44.0; INT4 16 up to 8192 32.4
+    // and 34.6; asymmetric of 64 bytes 24.6 and 25.8; asymmetric INT4 of 256-wide heads,
+    // 256 up to 60 146 and 149, 24 up to 6000 48.7 and 50.1, 64 up to 400 17.9 and 16.4.
+    static constexpr bool kEither = !SYM && BITS == 8 && D == 128;
 
     struct Tile {
         uint32_t k[2][KW], v[2][KW];
@@ -202,7 +202,7 @@ struct Few {
 };
 constexpr int kNoKey = 0x7FFFFF00;
 
-template <int D, int BITS, bool SYM, int ROWS, int WAVES, bool FORMS>
+template <int D, int BITS, bool SYM, int ROWS, int WAVES, bool STREAM, bool FORMS>
 __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void attn_few_kernel(AttnArgs a, Span span) {
     using C = Few<D, BITS, SYM, ROWS>;
     constexpr int LDO = D + 4;
@@ -287,7 +287,7 @@ __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void at
             for (int u = 0; u < 2; ++u) {
                 const uint8_t *kp = a.c.k_codes + slots[u] * C::kRow;
 #pragma unroll
-                for (int j = 0; j < C::NV; ++j) load_words<C::VEC, C::kStreamKeys>(x.k[u] + j * C::VEC, kp + j * 64 + k_off);
+                for (int j = 0; j < C::NV; ++j) load_words<C::VEC, STREAM>(x.k[u] + j * C::VEC, kp + j * 64 + k_off);
             }
 #pragma unroll
             for (int u = 0; u < C::US; ++u) {
@@ -1171,6 +1171,7 @@ __global__ __launch_bounds__(256) void attn_join_both_kernel(AttnArgs a, Span sp
 // rows, blocks a key head and workspace.
 struct Pass {
     int row_tile, cap, by_unit;
+    int stream;  // keys by streaming loads, where Few::kEither
     uint32_t least, most;
     int64_t bytes;
 };
@@ -1237,6 +1238,14 @@ Pass pass_of(int row_tile, int64_t rows, int64_t group, int64_t heads, int64_t h
         // 2000 41.3 and 39.7 (INT4 asymmetric: 16 18.2 and 24.1, 32 24.4 and 24.9,
         // 64 35.2 and 30.7).
         p.by_unit = kv <= 1024 || (kv <= 2048 && likely * heads >= 256);
+        // Streaming keys win where the card goes through more than a round of whole
+        // units of a few steps each. Streaming and ordinary loads, asymmetric INT8, 96
+        // sequences of 32 heads: up to 128 tokens 36.3 and 35.9 us, 200 42.7 and 43.7,
+        // 400 58.3 and 60.8, 800 97.6 and 98.3, 1024 123.6 and 120.7, 2000 222 and 208;
+        // 256 of 32 up to 60 94.4 and 96.9; 8 heads: 256 up to 400 49.8 and 51.8, 128 up
+        // to 200 21.7 and 20.6, 500 31.0 and 32.0, 1000 45.2 and 46.0; 96 up to 500 22.1
+        // and 21.4, 64 up to 400 15.4 and 13.9.
+        p.stream = kv <= 1024 && likely * heads >= 1024;
     }
     if (p.by_unit) cap = likely;
     // no more blocks than steps of work
@@ -1292,10 +1301,14 @@ uint32_t borders_of(const AttnArgs &a, const Pass &p) {  // and key heads: block
 template <int D, int BITS, bool SYM, int ROWS, bool FORMS>
 hipError_t launch_tiles(const AttnArgs &a, const Pass &p, const Span &span, hipStream_t st) {
     const dim3 grid((uint32_t)(p.cap * a.c.heads));
-    if constexpr (ROWS < 128)
-        hipLaunchKernelGGL((attn_few_kernel<D, BITS, SYM, ROWS, kFewWaves, FORMS>), grid, dim3(64 * kFewWaves), 0, st, a, span);
-    else
+    if constexpr (ROWS < 128) {
+        constexpr bool either = Few<D, BITS, SYM, ROWS>::kEither;
+        const auto kernel = either && !p.stream ? attn_few_kernel<D, BITS, SYM, ROWS, kFewWaves, !either, FORMS>
+                                                : attn_few_kernel<D, BITS, SYM, ROWS, kFewWaves, true, FORMS>;
+        hipLaunchKernelGGL(kernel, grid, dim3(64 * kFewWaves), 0, st, a, span);
+    } else {
         hipLaunchKernelGGL((attn_many_kernel<D, BITS, SYM, ROWS / 32, FORMS>), grid, dim3(2 * ROWS), 0, st, a, span);
+    }
     return hipGetLastError();
 }
 
