@@ -833,7 +833,9 @@ def kv_cache_weigh(q: torch.Tensor, lse: torch.Tensor, cache: KVCache, weights: 
     head's group, lse being what attention returned for these rows. causal: rows
     are their sequences' last tokens (paged_attention, prefix_attention's own
     tokens), whose own weights start from 0; otherwise they see the whole sequence
-    (cross_attention, a shared prefix). workspace: uint8, of at least
+    (cross_attention, a shared prefix). A new prompt that is weighed by its last
+    rows only is weighed with weights None and out the array: its pages hold the
+    weights of the tokens that had them before. workspace: uint8, of at least
     kv_cache_weigh_workspace(...) bytes. -> out, by default weights itself."""
     qs = _rows(cache, q, "q", None)
     if q.dtype is not _BF16:

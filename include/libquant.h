@@ -592,7 +592,11 @@ lq_status prefix_attention(const lq_kv_cache *cache, const void *q_bf16, int64_t
  * Slots that hold no position of such a sequence are left as they were. No page
  * may be held by two sequences of a call: each would write it.
  * To weigh a prompt by its last rows only, give only those as rows, their
- * row_starts counting them: positions count from the end.
+ * row_starts counting them: positions count from the end. The tokens before
+ * them are added to what weights holds in their slots, and that is whatever the
+ * page's last sequence left: neither kv_cache_write nor kv_cache_evict clears
+ * it. So a new prompt is weighed from NULL, weights_out being the array, in a
+ * call apart from sequences that go on, or its slots are cleared first.
  * Weights are relative to their exact value off by at most a few times 2^-24
  * of the largest |scale q . k_hat| and |lse|, and by 2^-24 for each addition;
  * sums in a fixed order: equal calls give equal bits. workspace (of
