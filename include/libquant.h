@@ -597,11 +597,13 @@ lq_status prefix_attention(const lq_kv_cache *cache, const void *q_bf16, int64_t
  * page's last sequence left: neither kv_cache_write nor kv_cache_evict clears
  * it. So a new prompt is weighed from NULL, weights_out being the array, in a
  * call apart from sequences that go on, or its slots are cleared first.
- * Weights are relative to their exact value off by at most a few times 2^-24
- * of the largest |scale q . k_hat| and |lse|, and by 2^-24 for each addition;
- * sums in a fixed order: equal calls give equal bits. workspace (of
- * kv_cache_weigh_workspace_bytes), other arguments and errors as
- * paged_attention; at most 2^30 rows.
+ * With codes c, scale s and zero z of a key (symmetric: z = mid = 2^(bits - 1))
+ * and a score x, exp(x - lse) is off by at most exp(e) - 1 + 2^-21 of itself,
+ *   e = 2^-24 ((head_dim + 8) |scale| s sum |q| (|c - mid| + |z - mid|) + 6 (|x| + |lse|)):
+ * a score whose terms cancel has the error of its terms. A sum of n of them adds
+ * (n + 8) 2^-24 of itself and of the old weight. Sums are in a fixed order: equal
+ * calls give equal bits. workspace (of kv_cache_weigh_workspace_bytes), other
+ * arguments and errors as paged_attention; at most 2^30 rows.
  */
 int64_t kv_cache_weigh_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t b,
                                        int64_t max_pages, int64_t page_size, int64_t max_rows, int64_t max_kv);
