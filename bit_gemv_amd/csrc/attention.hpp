@@ -246,7 +246,9 @@ __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void at
         const int qh = h * group + (int)(live ? rr - tok * (uint32_t)group : 0);
         const uint32_t last_row = (tile * ROWS + ROWS - 1 < total ? tile * ROWS + ROWS - 1 : total - 1) / (uint32_t)group;
         const int row_pos = live ? (int)(rows.first + tok) : -1;              // last position the row sees
-        const int safe = (int)(rows.first + tile * ROWS / (uint32_t)group);     // every row sees up to here
+        // every row sees up to here; short of kNoKey, also of rows past any table
+        const int64_t safe64 = rows.first + tile * ROWS / (uint32_t)group;
+        const int safe = safe64 < kNoKey - 16 ? (int)safe64 : kNoKey - 16;
         int64_t kend64 = rows.first + last_row + 1;
         kend64 = kend64 > rows.len ? rows.len : kend64;
         const int kend = kend64 < 0 ? 0 : (int)kend64;

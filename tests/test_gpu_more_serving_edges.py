@@ -283,3 +283,24 @@ def test_some_pages_of_wide_rows_stay_in_their_place(d, bits, sym):
         for pages in to:
             whole = pages[:keep // page]                # slots behind the last token may hold anything
             assert np.array_equal(got[whole], want[whole], equal_nan=True), name
+
+
+@pytest.mark.parametrize("call", ["paged", "prefix"])
+@pytest.mark.parametrize("last", [(1 << 31) - 1, (1 << 31) - 200, (1 << 31) - 300])
+def test_rows_past_any_table_pass_over_pages_outside_the_pool(call, last):
+    """Of single rows that stand at the ends of what int32 holds, over tiles of 32
+    keys whose first half is in no page: positions there are not attended to."""
+    rng = np.random.default_rng(40)
+    b, ref, q = _case([(128, 1), (64, 1)], rng, group=4)
+    gpu, table = to_gpu(ref), b.table.copy()
+    table[0, 0] = table[0, 4] = table[1, 2] = -1
+    kv, starts = [last, last], [0, 1, 2]
+    sets = [_pieces(ref, table[i], 16 * table.shape[1]) for i in range(2)]
+    for hints in ((1, 0), (1, 128)):
+        if call == "prefix":
+            _prefix(gpu, q, ref, (table[:1], [128], [0, 2]), (table, kv, starts), [_pieces(ref, table[0], 128) + s for s in sets],
+                    hints)
+        else:
+            need = bg.paged_attention_workspace(2, 4, gpu, 2, table.shape[1], *hints)
+            _run_attention(q, ref, sets, need, lambda x, **a: bg.paged_attention(
+                x, gpu, dev(table), _i32(kv), _i32(starts), max_rows=hints[0], max_kv=hints[1], **a), f"paged {kv} {hints}")
