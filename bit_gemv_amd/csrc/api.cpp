@@ -682,7 +682,7 @@ constexpr int64_t kMaxWholeRows = int64_t(1) << 30;
 // may overlap neither the inputs nor `more`.
 lq_status check_attention(const char *fn, const lq_kv_cache *cache, const void *q_bf16, int64_t q_stride, int64_t need,
                           const void *workspace, int64_t workspace_bytes, const void *out_bf16, const float *lse,
-                          const Range (&more)[3], const lq::AttnArgs &a) {
+                          const Range (&more)[3], const lq::AttnCall &a) {
     const int64_t d = cache->head_dim, width = a.q_heads * d, rows = a.batch.rows;
     if (q_stride < width || q_stride % 8)
         return fail(LQ_ERR_INVALID_ARG, "%s: q_stride must be a multiple of 8 and at least q_heads * head_dim", fn);
@@ -723,7 +723,7 @@ lq_status attention(const char *fn, bool whole, const lq_kv_cache *cache, const 
                     int64_t q_stride, float scale, const int32_t *block_table, int64_t max_pages, const int32_t *kv_lens,
                     const int32_t *row_starts, int64_t b, int64_t max_rows, int64_t max_kv, void *workspace,
                     int64_t workspace_bytes, void *out_bf16, float *lse, void *stream) {
-    lq::AttnArgs a{};
+    lq::AttnCall a{};
     lq_status st = check_kv(fn, cache, rows, block_table, max_pages, kv_lens, row_starts, b, max_rows, &a.c, &a.batch);
     if (st != LQ_OK) return st;
     if (max_kv < 0) return fail(LQ_ERR_INVALID_ARG, "%s: negative size", fn);

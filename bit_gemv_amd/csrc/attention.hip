@@ -10,6 +10,6 @@ int64_t attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, 
     return plan_of(rows, q_heads, heads, head_dim, 4, b, max_pages * page_size, max_rows, max_kv, whole).bytes;
 }
 
-hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st) { return launch_one<false>(a, plan_of(a), st); }
+hipError_t launch_paged_attention(const AttnCall &a, hipStream_t st) { return launch_one<false>(a, plan_of(a), st); }
 
 }  // namespace lq

@@ -62,7 +62,7 @@ LQ_DEVICE float pow2_floor(float v) { return __uint_as_float(__float_as_uint(v) 
 // in its span: whole units are written out, a unit's part (the span's first or
 // last piece) goes to the workspace and attn_join_kernel joins the parts.
 // kByUnit: every unit counts as one step, blocks take whole units. kWhole and
-// kApart: AttnArgs' whole and apart, looked at where FORMS. (In one number: further
+// kApart: AttnCall's whole and apart, looked at where FORMS. (In one number: further
 // arguments take scalar registers all along, and decode of 16 sequences in INT4 3 %
 // more time.) paged_attention is compiled without them: asked for at run time they
 // cost it 0.3 to 1.7 % (decode of 16 sequences 32.0 and 32.4 us, four chunks of
@@ -540,18 +540,17 @@ __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void at
             for (int w = 0; w < WAVES; ++w) lr += lds_l[w][r] * __builtin_amdgcn_exp2f(lds_m[w][r] - mr);
             const uint32_t wt = wr / (uint32_t)group;
             const int64_t at = (rows.begin + wt) * a.q_heads + h * group + (wr - wt * (uint32_t)group);
-            // relative to the maximum in fp32, or the result
-            float *const part = !whole                          ? span.o + (slot_of + r) * D
-                                : FORMS && (span.form & kApart) ? reinterpret_cast<float *>(a.out) + at * D
-                                                                : nullptr;
-            const float norm = part ? 1.0f : inverse_sum(lr);
+            // fp32 relative to the maximum, or the result
+            const bool relative = !whole || (FORMS && (span.form & kApart));
+            float *const part = FORMS && whole ? reinterpret_cast<float *>(a.out) + at * D : span.o + (slot_of + r) * D;
+            const float norm = relative ? 1.0f : inverse_sum(lr);
 #pragma unroll
             for (int d = 4 * c; d < D; d += 4 * kTeam) {
                 f32x4 v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int w = 0; w < WAVES; ++w) v += *reinterpret_cast<const f32x4 *>(&lds_o[w][r][d]);
                 v *= norm;
-                if (part) {
+                if (relative) {
                     *reinterpret_cast<f32x4 *>(part + d) = v;
                 } else {
                     const bf16x2_t b0{(__bf16)v[0], (__bf16)v[1]}, b1{(__bf16)v[2], (__bf16)v[3]};
@@ -560,8 +559,8 @@ __global__ __launch_bounds__(64 * WAVES, (Few<D, BITS, SYM, ROWS>::OCC)) void at
                 }
             }
             if (c == 0) {
-                if (part) {
-                    float *ml = !whole ? span.ml + (slot_of + r) * 2 : a.lse + at * 2;
+                if (relative) {
+                    float *ml = FORMS && whole ? a.lse + at * 2 : span.ml + (slot_of + r) * 2;
                     ml[0] = lr == 0.0f ? -__builtin_inff() : mr;
                     ml[1] = lr;
                 } else if (a.lse) {
@@ -1059,11 +1058,10 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
         if (live) {
             const int64_t at = (rows.begin + tok) * a.q_heads + qh;
             const int64_t slot = slot_of + wave * 32 + n;
-            float *const part = !whole                          ? span.o + slot * D
-                                : FORMS && (span.form & kApart) ? reinterpret_cast<float *>(a.out) + at * D
-                                                                : nullptr;
+            const bool relative = !whole || (FORMS && (span.form & kApart));
+            float *const part = FORMS && whole ? reinterpret_cast<float *>(a.out) + at * D : span.o + slot * D;
             l *= sref * (1.0f / kHead);
-            const float f = (part ? 1.0f : inverse_sum(l)) * (sref * (1.0f / kHead));
+            const float f = (relative ? 1.0f : inverse_sum(l)) * (sref * (1.0f / kHead));
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int mrow = 8 * (i / 4) + 4 * half + i % 4;
@@ -1074,7 +1072,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
 #pragma unroll
                     for (int e = 0; e < C::DW; ++e) v[e] = (o[e * (C::TP / 32) + g][i] - vz) * f;
                     const int d = (g * 32 + mrow) * C::DW;
-                    if (part) {
+                    if (relative) {
 #pragma unroll
                         for (int e = 0; e < C::DW; e += 2)
                             *reinterpret_cast<float2 *>(part + d + e) = float2{v[e], v[e + 1]};
@@ -1088,8 +1086,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_many_kernel(Att
                 }
             }
             if (half == 0) {
-                if (part) {
-                    float *ml = !whole ? span.ml + slot * 2 : a.lse + at * 2;
+                if (relative) {
+                    float *ml = FORMS && whole ? a.lse + at * 2 : span.ml + slot * 2;
                     ml[0] = l == 0.0f ? -__builtin_inff() : m;
                     ml[1] = l;
                 } else if (a.lse) {
@@ -1291,17 +1289,17 @@ Plan plan_of(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int
     return p;
 }
 
-Span span_of(const AttnArgs &a, const Pass &p, char *workspace) {
+Span span_of(const AttnCall &a, const Pass &p, char *workspace) {
     float *o = reinterpret_cast<float *>(workspace);
     const int form = (p.by_unit ? kByUnit : 0) | (a.whole ? kWhole : 0) | (a.apart ? kApart : 0);
     return {o, o + (int64_t)2 * p.cap * a.c.heads * p.row_tile * a.c.head_dim, p.cap, form, p.least, p.most};
 }
-uint32_t borders_of(const AttnArgs &a, const Pass &p) {  // and key heads: blocks of the join
+uint32_t borders_of(const AttnCall &a, const Pass &p) {  // and key heads: blocks of the join
     return p.by_unit ? 0 : (uint32_t)((p.cap - 1) * a.c.heads);
 }
 
 template <int D, int BITS, bool SYM, int ROWS, bool FORMS>
-hipError_t launch_tiles(const AttnArgs &a, const Pass &p, const Span &span, hipStream_t st) {
+hipError_t launch_tiles(const AttnCall &a, const Pass &p, const Span &span, hipStream_t st) {
     const dim3 grid((uint32_t)(p.cap * a.c.heads));
     if constexpr (ROWS < 128) {
         constexpr bool either = Few<D, BITS, SYM, ROWS>::kEither;
@@ -1317,7 +1315,7 @@ hipError_t launch_tiles(const AttnArgs &a, const Pass &p, const Span &span, hipS
 // The pass's kernel and the join; with `few`, the kernel for few rows between
 // them (its workspace behind the pass's own) and one join for both.
 template <int D, int BITS, bool SYM, int ROWS, bool FORMS>
-hipError_t launch_pass(const AttnArgs &a, const Pass &p, const Pass *few, hipStream_t st) {
+hipError_t launch_pass(const AttnCall &a, const Pass &p, const Pass *few, hipStream_t st) {
     char *ws = static_cast<char *>(a.workspace);
     const Span span = span_of(a, p, ws);
     hipError_t e = launch_tiles<D, BITS, SYM, ROWS, FORMS>(a, p, span, st);
@@ -1341,7 +1339,7 @@ hipError_t launch_pass(const AttnArgs &a, const Pass &p, const Pass *few, hipStr
 }
 
 template <int D, int BITS, bool SYM, bool FORMS>
-hipError_t launch_plan(const AttnArgs &a, const Plan &p, hipStream_t st) {
+hipError_t launch_plan(const AttnCall &a, const Plan &p, hipStream_t st) {
     const Pass *few = p.passes == 2 ? &p.pass[1] : nullptr;
     switch (p.pass[0].row_tile) {
         case 8: return launch_pass<D, BITS, SYM, 8, FORMS>(a, p.pass[0], nullptr, st);
@@ -1353,7 +1351,7 @@ hipError_t launch_plan(const AttnArgs &a, const Plan &p, hipStream_t st) {
 
 // FORMS: a.whole and a.apart are looked at; without, they are 0.
 template <bool FORMS>
-hipError_t launch_one(const AttnArgs &a, const Plan &p, hipStream_t st) {
+hipError_t launch_one(const AttnCall &a, const Plan &p, hipStream_t st) {
 #define LQ_ATTN(D, BITS, SYM) \
     if (a.c.head_dim == D && a.c.bits == BITS && (a.c.symmetric != 0) == SYM) return launch_plan<D, BITS, SYM, FORMS>(a, p, st);
 #define LQ_ATTN_D(D) LQ_ATTN(D, 4, false) LQ_ATTN(D, 4, true) LQ_ATTN(D, 8, false) LQ_ATTN(D, 8, true)
@@ -1363,7 +1361,7 @@ hipError_t launch_one(const AttnArgs &a, const Plan &p, hipStream_t st) {
     return hipErrorInvalidValue;
 }
 
-Plan plan_of(const AttnArgs &a) {
+Plan plan_of(const AttnCall &a) {
     return plan_of(a.batch.rows, a.q_heads, a.c.heads, a.c.head_dim, a.c.bits, a.batch.b,
                    a.batch.max_pages << a.c.page_shift, a.max_rows, a.max_kv, a.whole);
 }

@@ -5,7 +5,7 @@
 
 namespace lq {
 
-hipError_t launch_cross_attention(const AttnArgs &a, hipStream_t st) { return launch_one<true>(a, plan_of(a), st); }
+hipError_t launch_cross_attention(const AttnCall &a, hipStream_t st) { return launch_one<true>(a, plan_of(a), st); }
 
 namespace {
 
@@ -231,7 +231,7 @@ int64_t prefix_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int
 
 hipError_t launch_prefix_attention(const PrefixArgs &a, hipStream_t st) {
     if (a.prefix.b == 0) return launch_paged_attention(a.own, st);
-    AttnArgs side[2] = {a.own, a.own};
+    AttnCall side[2] = {a.own, a.own};
     side[1].batch = a.prefix;
     side[1].whole = 1;
     side[1].max_rows = a.max_prefix_rows;
@@ -239,7 +239,7 @@ hipError_t launch_prefix_attention(const PrefixArgs &a, hipStream_t st) {
     Source source[2];
     char *ws = static_cast<char *>(a.own.workspace);
     for (int i = 0; i < 2; ++i) {
-        AttnArgs &x = side[i];
+        AttnCall &x = side[i];
         x.apart = 1;
         x.out = reinterpret_cast<uint16_t *>(ws);
         x.lse = reinterpret_cast<float *>(ws + part_bytes(x.batch.rows, x.q_heads, x.c.head_dim));

@@ -50,6 +50,10 @@ struct AttnArgs {
     void *workspace;
     uint16_t *out;
     float *lse;
+};
+
+// A call, with the forms beside paged_attention's, which the kernels have in Span.
+struct AttnCall : AttnArgs {
     int whole = 0;  // the rows are no tokens of the sequence: each sees all that it holds
     // For a result that is joined with another: whole units' rows relative to their
     // maximum, fp32, go to out, their maximum (log2) and sum to lse, [rows][q_heads][2];
@@ -60,7 +64,7 @@ struct AttnArgs {
 // Attention over a prefix that several sequences share and over their own
 // tokens: `own` is the whole call, `prefix` the groups of rows that share one.
 struct PrefixArgs {
-    AttnArgs own;
+    AttnCall own;
     KvBatch prefix;
     int64_t max_prefix_rows, max_prefix;
 };
@@ -78,7 +82,7 @@ struct WeighArgs {
     float *out;
     int64_t max_rows, max_kv;
     void *workspace;
-    int whole;  // as AttnArgs'
+    int whole;  // as AttnCall's
 };
 
 // Eviction by weight from the sequences' pages to the front of to_table's.
@@ -105,8 +109,8 @@ int64_t attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, 
 int64_t prefix_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim, int64_t page_size,
                                int64_t p, int64_t prefix_pages, int64_t max_prefix_rows, int64_t max_prefix, int64_t b,
                                int64_t max_pages, int64_t max_rows, int64_t max_kv);
-hipError_t launch_paged_attention(const AttnArgs &a, hipStream_t st);  // neither whole nor apart
-hipError_t launch_cross_attention(const AttnArgs &a, hipStream_t st);
+hipError_t launch_paged_attention(const AttnCall &a, hipStream_t st);  // neither whole nor apart
+hipError_t launch_cross_attention(const AttnCall &a, hipStream_t st);
 hipError_t launch_prefix_attention(const PrefixArgs &a, hipStream_t st);
 
 // One sequence's rows: [begin, begin + n) of the row tensors, row begin + i at
