@@ -562,7 +562,10 @@ lq_status cross_attention(const lq_kv_cache *cache, const void *q_bf16, int64_t 
  * paged_attention. Each of the two sums has paged_attention's arithmetic (the
  * value scales' range counts for each of them by itself); they are joined in
  * fp32 and rounded once. At most 2^30 rows. Arguments otherwise, workspace and
- * errors as paged_attention.
+ * errors as paged_attention. The workspace holds, beside what paged_attention and
+ * cross_attention need for the two sums, every row's two results in fp32:
+ * 8 rows q_heads (head_dim + 2) bytes and less than 1024 (16384 rows of 64 heads
+ * of 128: 1.1 GB); a long prompt is better given in chunks. None of that for p = 0.
  */
 int64_t prefix_attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t head_dim,
                                          int64_t page_size, int64_t p, int64_t prefix_pages, int64_t max_prefix_rows,
