@@ -18,7 +18,7 @@ namespace {
 // attn_finish_kernel joins what either has of a row: one launch of 12 us for 64
 // sequences of 64 heads, where joins of each pass and a merge took 26, and of 7 for
 // 4, where they took 17. 64 rows behind 8192 shared tokens: own tokens (up to 1024
-// each) 22 us, bound by HBM, the prefix 41, by the matrix units, of 75 in all.
+// each) 22 us, bound by HBM, the prefix 38, of 70 in all.
 struct Launched {
     Span span;
     int log_tile, step;  // rows of a tile (log2), keys of a step

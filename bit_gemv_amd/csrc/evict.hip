@@ -11,10 +11,12 @@
 // batch of tokens is read whole before any of it is written, and what later
 // batches read lies behind what earlier ones write, so one block takes all tokens
 // of a sequence and head, or of some bytes of their codes. Into other pages
-// batches are shared out as well, unless some of them are the sequence's own. Bound by HBM with scattered rows of 64 or 128 bytes
-// and quads of values of which one token in two to four stays: 16 sequences of up to
-// 8192 tokens to 2048, 8 heads, INT8, 46 us for 178 MB, 3.9 TB/s; 6 of up to 30000 to
-// 4000, 32 heads, INT4, 108 us for 437 MB.
+// batches are shared out as well, unless some of them are the sequence's own. Bound
+// by HBM with scattered rows of 64 or 128 bytes and quads of values of which one
+// token in two to four stays: 16 sequences of up to 8192 tokens to 2048, 8 heads,
+// INT8, 53 us for 178 MB, 3.4 TB/s; 6 of up to 30000 to 4000, 32 heads, INT4, 109 us
+// for 437 MB, 4.0 TB/s (three sets of inputs in turn; one set again and again, which
+// the last cache holds in part, 33 and 93, and in place 39 and 97).
 #include "common.hpp"
 #include "kv.hpp"
 

@@ -11,7 +11,7 @@
 // 8 heads of 128, INT8, 156 us for 772 MB. Chunks are bound by the matrix and the
 // vector units, whose times add up: of 64 scores of 128 elements a wave's products
 // take 16 clocks, exponentials 8, scaling and sum 8. The last 500 rows of three
-// prompts of up to 6000 tokens, 32 heads of 128, INT4: 66 us, 0.67 PFLOP/s.
+// prompts of up to 6000 tokens, 32 heads of 128, INT4: 68 us, 0.65 PFLOP/s.
 #include "codes.hpp"
 #include "kv.hpp"
 
@@ -86,9 +86,10 @@ struct Steps {
 // Wave w of a block walks its span's 32-key tiles w, w + 4, ..., the next two
 // tiles' codes on their way: a tile's registers take the one after the next as
 // soon as it has been multiplied. Two tiles on their way and one: 158 and 173 us
-// for 64 sequences of up to 16384 tokens. Streaming loads and ordinary ones: 157 and
-// 154, but 32 sequences up to 8000 38.3 and 39.6 (INT4 26.5 and 28.3, 64-wide 22.8
-// and 25.8).
+// for 64 sequences of up to 16384 tokens. Streaming loads and ordinary ones: there 157
+// and 154, 64 up to 1000 18.0 and 17.2, 32 up to 8000 of 256-wide heads 91.3 and 88.7;
+// but of 128-wide 38.3 and 39.6, INT4 26.5 and 28.3, 64-wide 22.8 and 25.8. Streaming
+// is taken: it loses 5 % at most, ordinary loads up to 13.
 template <int D, int BITS>
 struct Few {
     static constexpr int kRow = D * BITS / 8;    // code bytes of a key
