@@ -328,7 +328,8 @@ static hipError_t launch_move(const EvictArgs &a, hipStream_t st) {
     if (kv > a.keep) kv = a.keep;  // tokens that may move
     Shares sh{1, 1, 1};
     // Two blocks of 512 threads a CU and a few rounds of them: values first, which
-    // read four bytes for one. 1, 2 and 4 parts of each without batches side by side:
+    // read four bytes for one. Of one set of inputs, what stayed read back after each
+    // call: 1, 2 and 4 parts of each without batches side by side,
     // 16 sequences to 2048 tokens 56, 56 and 53 us, 47 with 2 and 2 and two batches
     // (this), 49 with 2 and 4; 6 to 4000 118, 121 and 129, 108 with 1 and 2 and four
     // batches (this), 119 with 2 and 4. 256 and 1024 threads 51 and 114, 51 and 115.
